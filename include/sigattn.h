@@ -225,6 +225,70 @@ sigattn_status sigattn_log_length_bias(const int32_t *seqlens, int Z, float *bia
  * and head; fp32: per query row and head) of every sample. */
 size_t sigattn_dbias_workspace_bytes(int Z, int L, int H, sigattn_dtype dtype);
 
+/* Masked attention: spans, a cap on the scores, a bias that falls with distance,
+ * and heads that share keys.
+ *
+ *   x_ij = cap tanh(alpha q_i . k_j / cap) - slopes[h] |i - j| + b
+ *          (cap = 0: alpha q_i . k_j - slopes[h] |i - j| + b)
+ *   P_ij = sigma(x_ij) where lo_i <= j < hi_i, j < n and i < n; 0 elsewhere
+ *   O    = P V
+ *
+ * Query i and key j are positions of one padded row of L places with n true
+ * tokens.  q, dout, o, dq: [Z][L][H][D]; k, v, dk, dv: [Z][L][Hk][D] with H a
+ * multiple of Hk: query head h reads key head h / (H / Hk), and dk, dv are the
+ * sums over the query heads that read them.
+ *
+ * seqlens: device int32[Z], the true lengths n (clamped and flagged as in
+ * sigattn_fwd).  spans: device int32[Z][L][2], {lo, hi} of each row, or NULL
+ * for rows that see all n keys; any values are allowed (they are clipped to
+ * [0, n), and a row with lo >= hi sees nothing: its O and dQ are exact zeros and
+ * it adds nothing to dK, dV).  One interval a row covers causal, prefix, document
+ * and window masks (sigattn_mask_spans makes those), and key tiles outside the
+ * intervals of a tile's rows are neither loaded nor computed; spans that scatter
+ * within 128 neighbouring rows give the same results but skip less.
+ * bias_z: device float[Z], one bias per sample, or NULL for the scalar bias.
+ * cap: 0, or a positive finite number.  slopes: device float[H], or NULL.
+ *
+ * Rows at or beyond n may hold anything, NaN included: they are never read into
+ * a result.  Within a sample a masked key or query must still be finite (it is
+ * multiplied by a weight of zero).
+ *
+ * sigattn_bwd_span writes dq, dk, dv in full and needs neither O nor any saved
+ * statistic.  Its workspace (device memory, 16-byte aligned, at least
+ * sigattn_bwd_span_workspace_bytes(Z, L, dtype) bytes; 0 for fp32) is
+ * overwritten; calls that may overlap, captured graphs included, need one each.
+ * Errors: SIGATTN_ERR_INVALID_ARG (also: H not a multiple of Hk, a negative or
+ * non-finite cap, a missing or small workspace), _UNSUPPORTED_HEADDIM,
+ * _UNSUPPORTED_DTYPE, _UNSUPPORTED_DEVICE, _MISALIGNED (also: spans not 8-byte
+ * aligned), _TOO_LARGE (fp32 beyond 2^34 rows), _CUDA.  On error nothing is
+ * launched. */
+sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, void *o,
+                                const int32_t *seqlens, const int32_t *spans, int Z, int L, int H,
+                                int Hk, int D, float alpha, float bias, const float *bias_z,
+                                float cap, const float *slopes, sigattn_dtype dtype, void *stream);
+sigattn_status sigattn_bwd_span(const void *q, const void *k, const void *v, const void *dout,
+                                void *dq, void *dk, void *dv, const int32_t *seqlens,
+                                const int32_t *spans, int Z, int L, int H, int Hk, int D, float alpha,
+                                float bias, const float *bias_z, float cap, const float *slopes,
+                                void *workspace, size_t workspace_bytes, sigattn_dtype dtype,
+                                void *stream);
+size_t sigattn_bwd_span_workspace_bytes(int Z, int L, sigattn_dtype dtype);
+
+/* Writes the spans of the usual masks, int32[Z][L][2] on the device.  Row i of a
+ * sample of n tokens starts from [0, n), or, with docs (device int32[Z][L], a
+ * document id per token), from the run of equal ids around i; then
+ *   causal:   hi = min(hi, i + 1)
+ *   prefix:   (device int32[Z], with causal) hi = min(end, max(i + 1, start +
+ *             prefix[z])): the first prefix[z] tokens of the sample, or of each
+ *             document, are seen by all its rows
+ *   window:   (> 0, not with prefix) lo = max(lo, i - window + 1), and without
+ *             causal hi = min(hi, i + window)
+ * Rows at or beyond n, and rows that see nothing, get {0, 0}.  prefix and docs
+ * may be NULL.  Errors: SIGATTN_ERR_INVALID_ARG, _MISALIGNED, _CUDA. */
+sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix, const int32_t *docs,
+                                  int causal, int window, int Z, int L, int32_t *spans,
+                                  void *stream);
+
 /* Selects how later bf16 calls in this process evaluate sigma (process-wide,
  * default SIGATTN_SIGMOID_TANH, the pages' form; see sigattn_sigmoid_mode).  Returns
  * SIGATTN_ERR_INVALID_ARG for an unknown mode.

@@ -23,7 +23,8 @@ __all__ = [
     "version", "library_path", "load_library", "SIGMOID_TANH", "SIGMOID_EXP", "EXPORTS",
     "SigmoidAttention", "bwd_dq", "bwd_dkdv", "last_cuda_error", "fwd_noalloc", "NOALLOC_MAX_Z",
     "fwd_bias", "bwd_bias", "dbias_workspace_bytes", "fwd_rect", "bwd_rect", "fwd_bwd_host",
-    "fwd_bwd_host_workspace_bytes", "launch_order", "log_length_bias",
+    "fwd_bwd_host_workspace_bytes", "launch_order", "log_length_bias", "fwd_span", "bwd_span",
+    "bwd_span_workspace_bytes", "mask_spans",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +54,7 @@ EXPORTS = (
     "sigattn_fwd_noalloc", "sigattn_fwd_bias", "sigattn_bwd_bias", "sigattn_dbias_workspace_bytes",
     "sigattn_fwd_rect", "sigattn_bwd_rect", "sigattn_fwd_bwd_host",
     "sigattn_fwd_bwd_host_workspace_bytes", "sigattn_launch_order", "sigattn_log_length_bias",
+    "sigattn_fwd_span", "sigattn_bwd_span", "sigattn_bwd_span_workspace_bytes", "sigattn_mask_spans",
 )
 
 
@@ -127,6 +129,8 @@ def load_library():
         lib.sigattn_log_length_bias.restype = ci
         lib.sigattn_launch_order.argtypes = [vp, ci, vp]
         lib.sigattn_launch_order.restype = ci
+        from . import span
+        span.register(lib)
         _lib = lib
         return lib
 
@@ -502,3 +506,4 @@ def launch_order(work) -> list:
 
 
 from .autograd import SigmoidAttention  # noqa: E402  (needs the functions above)
+from .span import bwd_span, bwd_span_workspace_bytes, fwd_span, mask_spans  # noqa: E402

@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
 
 // db_z = sum of the per-CTA (or per-row) partials of sample z, in double and in
 // a fixed order: thread t adds partials t, t + 256, ...; then a fixed tree.
-__global__ void __launch_bounds__(256) dbias_reduce_kernel(const float *part, int64_t per_z,
+static __global__ void __launch_bounds__(256) dbias_reduce_kernel(const float *part, int64_t per_z,
                                                            float *dbias) {
     __shared__ double red[256];
     const int z = blockIdx.x;

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256) f32_dkdv_kernel(const F32Params p) {
 
 // The bf16 kernels' sigma routine on an array (alpha = 1, b = 0).
 template <int MODE>
-__global__ void sigmoid_eval_kernel(const float *x, float *y, float *dy, int64_t n) {
+static __global__ void sigmoid_eval_kernel(const float *x, float *y, float *dy, int64_t n) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= n) return;
     const SigmoidCoef cf = make_coef<MODE>(1.0f, 0.0f);
@@ -197,7 +197,7 @@ __global__ void sigmoid_eval_kernel(const float *x, float *y, float *dy, int64_t
 
 // Waits on a barrier that nothing signals; the bounded wait must give up,
 // record the timeout and let the kernel exit normally.
-__global__ void wait_timeout_selftest_kernel(int *status, uint64_t timeout_ns) {
+static __global__ void wait_timeout_selftest_kernel(int *status, uint64_t timeout_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
     if (threadIdx.x == 0) {

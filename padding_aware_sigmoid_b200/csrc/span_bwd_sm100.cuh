@@ -1,0 +1,688 @@
+// Backward of the masked attention (span_score.cuh), bf16: a dQ kernel by query
+// tiles and a dK/dV kernel by key tiles, no atomics, with the structure of the
+// padding-only backward (bwd_sm100.cuh) and these differences:
+//
+//  - dQ visits the key tiles of its rows' hull.  dK/dV visits the query tiles
+//    whose hull meets its keys: first to last of them, from a table that
+//    span_prep_kernel writes (one entry per 128 rows), so neither kernel
+//    touches a tile that no pair needs under causal, prefix, document or
+//    window masks;
+//  - a key head serves `group` query heads: the dK/dV CTA of a key head runs
+//    through the query tiles of all of them and accumulates in tensor memory,
+//    so shared heads need no second pass and the sum's order is fixed;
+//  - the MMA warp zeroes the rows at or beyond n of the tiles that serve as
+//    the contraction side (K in dQ; Q and dO in dK/dV), so that NaN in padding
+//    never meets a weight of zero.
+//
+// Bound: dQ issues 6 D and dK/dV 8 D tensor FLOP per pair against one MUFU op
+// (two with a cap): tensor-bound at D = 128, near the MUFU's rate at D = 64.
+#pragma once
+
+#include "bwd_sm100.cuh"
+#include "span_score.cuh"
+
+namespace sigattn {
+
+struct SpanBwdParams {
+    __nv_bfloat16 *dq, *dk, *dv;
+    SpanSource src;
+    int H, Hk, group;
+    float alpha, bias, cap;
+    const float *bias_z, *slopes;
+    const int2 *clean;     // [Z][tiles * 128] clipped spans (span_prep_kernel)
+    const int4 *hull;      // [Z][tiles] {least lo, greatest hi, greatest lo, least hi}
+    uint64_t timeout_ns;
+};
+
+// Clipped spans of every row, rows of padding (0, 0), and per 128-row tile the
+// hull of its rows' spans: {least lo and greatest hi of the rows that see a
+// key, greatest lo and least hi of all 128 rows}.  A key tile [k0, k1) is met
+// when least lo < k1 and greatest hi > k0, and is seen whole by every row when
+// greatest lo <= k0 and least hi >= k1.
+static __global__ void __launch_bounds__(128) span_prep_kernel(const SpanSource src, int2 *clean, int4 *hull) {
+    __shared__ int4 part[4];
+    const int z = blockIdx.y, i = blockIdx.x * 128 + threadIdx.x;
+    const int n = span_tokens(src, z);
+    const int2 r = row_span(src, z, i, n);
+    clean[static_cast<size_t>(z) * gridDim.x * 128 + i] = r;
+    const bool some = r.x < r.y;
+    const int4 w = make_int4(__reduce_min_sync(0xffffffffu, some ? r.x : INT_MAX),
+                             __reduce_max_sync(0xffffffffu, r.y), __reduce_max_sync(0xffffffffu, r.x),
+                             __reduce_min_sync(0xffffffffu, r.y));
+    if (lane_id() == 0) part[warp_id()] = w;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int4 a = part[0];
+        for (int u = 1; u < 4; ++u) {
+            a.x = min(a.x, part[u].x);
+            a.y = max(a.y, part[u].y);
+            a.z = max(a.z, part[u].z);
+            a.w = min(a.w, part[u].w);
+        }
+        hull[static_cast<size_t>(z) * gridDim.x + blockIdx.x] = a;
+    }
+}
+
+template <int D>
+struct SpanBwdLayout : BwdLayout<D, BwdStages<D>::X, BwdStages<D>::Y> {
+    using Base = BwdLayout<D, BwdStages<D>::X, BwdStages<D>::Y>;
+    static constexpr int OFF_HULL = (Base::OFF_SAMPLE + 7) & ~7;   // {first, last} of each warp
+    static constexpr int SMEM_ALLOC = OFF_HULL + 32 * 8 + 1024;
+    static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+};
+
+// dq_sigma_tile (bwd_sm100.cuh) with the masked score function: one key tile
+// of a dQ sigma warpgroup.  `row` is this thread's query, `key0` the tile's
+// first key, `span` the keys its row sees.
+template <int D, int MODE, int SCORE>
+__device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_s, uint32_t dcol,
+                                             uint64_t *s_full, uint32_t s_par, uint64_t *s_free,
+                                             uint64_t *dp_full, uint32_t dp_par, uint64_t *ds_ready,
+                                             const ScoreCoef &cf, int row, int key0, int2 span,
+                                             const WaitCtx &wctx) {
+    using SG = BwdSigma<D>;
+    if (!__all_sync(0xffffffffu, mbar_wait(s_full, s_par, wctx))) return false;
+    tc_fence_after();
+    uint32_t r[SG::kCols];
+    tmem_ld_cols(trow + col_s + SG::kCols * w, r);
+    tc_fence_before();
+    mbar_arrive(s_free);
+    const int first = key0 + SG::kCols * w;    // this warpgroup's first key
+    const bool whole = __all_sync(0xffffffffu, span.x <= first && span.y >= first + SG::kCols);
+    constexpr int kChunks = SG::kCols / 32;
+    float2 g[16];
+    auto gains = [&](int ch) {
+        const float rel = static_cast<float>(row - first - 32 * ch);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float2 pr;
+            score_pg2<MODE, SCORE>(__uint_as_float(r[32 * ch + 2 * i]), __uint_as_float(r[32 * ch + 2 * i + 1]), cf,
+                                   rel - static_cast<float>(2 * i), pr, g[i]);
+        }
+    };
+    gains(0);   // before dP is waited for
+    const uint32_t dc = dcol + SG::kCols * w;
+    if (!__all_sync(0xffffffffu, mbar_wait(dp_full, dp_par, wctx))) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int ch = 0; ch < kChunks; ++ch) {
+        if (ch > 0) gains(ch);
+        uint32_t d[32];
+        tmem_ld32(trow + dc + 32 * ch, d);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 ds = mul2(g[i], f2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])));
+            pk[i] = pack_bf16x2(ds.x, ds.y);
+        }
+        if (!whole) keep_bits(pk, bit_range(span.x - first - 32 * ch, span.y - first - 32 * ch));
+        tmem_st16(trow + dc + 16 * ch, pk);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(ds_ready);
+    return true;
+}
+
+// dkdv_sigma_tile (bwd_sm100.cuh) with the masked score function: one query
+// tile of a dK/dV sigma warpgroup, whose columns are the queries from q_first
+// on.  `key` is this thread's key; `whole`: every row of the tile sees every
+// key of this CTA's tile; otherwise `clean` points at the spans of the columns.
+template <int D, int MODE, int SCORE>
+__device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_t *s_full, uint64_t *s_free,
+                                               uint64_t *dp_full, uint64_t *p_ready, uint64_t *ds_ready,
+                                               uint32_t par, const ScoreCoef &cf, int key, int q_first,
+                                               bool whole, const int2 *clean, const WaitCtx &wctx) {
+    using SG = BwdSigma<D>;
+    constexpr int W = SG::kPacked / 16;   // words of 32 columns
+    float2 g[SG::kPacked];
+    uint32_t pk[SG::kPacked];
+    uint32_t bits[W];
+    if (!whole) {
+        // two columns' spans per load, the same address in every lane
+        const int4 *pair = reinterpret_cast<const int4 *>(clean);
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+            bits[u] = 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int4 s = __ldg(pair + 16 * u + i);
+                if (static_cast<unsigned>(key - s.x) < static_cast<unsigned>(s.y - s.x)) bits[u] |= 1u << (2 * i);
+                if (static_cast<unsigned>(key - s.z) < static_cast<unsigned>(s.w - s.z)) bits[u] |= 2u << (2 * i);
+            }
+        }
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(s_full, par, wctx))) return false;
+    tc_fence_after();
+    {
+        uint32_t r[SG::kCols];
+        tmem_ld_cols(tS, r);
+        // S^T is in registers: the MMA warp may compute the next S^T now
+        tc_fence_before();
+        mbar_arrive(s_free);
+        const float rel = static_cast<float>(key - q_first);
+#pragma unroll
+        for (int ii = 0; ii < SG::kPacked; ++ii) {
+            float2 pr;
+            score_pg2<MODE, SCORE>(__uint_as_float(r[2 * ii]), __uint_as_float(r[2 * ii + 1]), cf,
+                                   rel - static_cast<float>(2 * ii), pr, g[ii]);
+            pk[ii] = pack_bf16x2(pr.x, pr.y);
+        }
+    }
+    auto keep = [&](uint32_t (&x)[SG::kPacked]) {
+#pragma unroll
+        for (int u = 0; u < W; ++u) keep_bits(*reinterpret_cast<uint32_t(*)[16]>(&x[16 * u]), bits[u]);
+    };
+    if (!whole) keep(pk);
+    if (!__all_sync(0xffffffffu, mbar_wait(dp_full, par, wctx))) return false;
+    tc_fence_after();
+    uint32_t ds[SG::kPacked];
+    {
+        // the first kPacked of this warpgroup's dP^T columns, then P^T over them
+        uint32_t d[SG::kPacked];
+        tmem_ld_cols(tD, d);
+        tmem_st_cols(tD, pk);
+#pragma unroll
+        for (int ii = 0; ii < SG::kPacked / 2; ++ii) {
+            const float2 v = mul2(g[ii], f2(__uint_as_float(d[2 * ii]), __uint_as_float(d[2 * ii + 1])));
+            ds[ii] = pack_bf16x2(v.x, v.y);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_ready);
+    }
+    {
+        // the other kPacked dP^T columns, then dS^T over them
+        uint32_t d[SG::kPacked];
+        tmem_ld_cols(tD + SG::kPacked, d);
+#pragma unroll
+        for (int ii = 0; ii < SG::kPacked / 2; ++ii) {
+            const float2 v = mul2(g[SG::kPacked / 2 + ii],
+                                  f2(__uint_as_float(d[2 * ii]), __uint_as_float(d[2 * ii + 1])));
+            ds[SG::kPacked / 2 + ii] = pack_bf16x2(v.x, v.y);
+        }
+    }
+    if (!whole) keep(ds);
+    tmem_st_cols(tD + SG::kPacked, ds);
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(ds_ready);
+    return true;
+}
+
+// Streams step r = 0, 1, ... (tile row0, head h) of one tensor map into a ring
+// of S slots; false when a wait gave up.
+template <int S, int NSUB>
+__device__ __forceinline__ bool span_ring_load(const CUtensorMap *map, uint64_t *full, uint64_t *empty,
+                                               uint8_t *base, int tile_bytes, int r, int row0, int h, int z,
+                                               const WaitCtx &w) {
+    const int st = r % S;
+    if (r >= S && !mbar_wait(&empty[st], ((r / S) - 1) & 1, w)) return false;
+    mbar_arrive_expect_tx(&full[st], tile_bytes);
+    for (int s = 0; s < NSUB; ++s)
+        tma_load_4d(map, &full[st], base + st * tile_bytes + s * (128 * 64 * 2), 64 * s, h, row0, z);
+    return true;
+}
+
+// dQ: one CTA per 128-row query tile (the last rows' tiles first).  Tensor
+// memory as bwd_dq_kernel: [0,128) S, [128,256) and [256,384) dP of even / odd
+// steps, [384,384+D) dQ.
+template <int D, int MODE, int SCORE>
+__global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
+    span_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                   const SpanBwdParams p) {
+    constexpr int SX = BwdStages<D>::X, SY = BwdStages<D>::Y;
+    using Lay = SpanBwdLayout<D>;
+    using SG = BwdSigma<D>;
+    constexpr uint32_t kColS = 0, kColDP0 = 128, kColDP1 = 256, kColDQ = 384;
+    static_assert(kColDQ + D <= Lay::TMEM_COLS, "TMEM budget");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1k(smem_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
+    uint64_t *res_full = bars;
+    uint64_t *x_full = bars + 1;              // K ring
+    uint64_t *x_empty = x_full + SX;
+    uint64_t *y_full = x_empty + SX;          // V ring
+    uint64_t *y_empty = y_full + SY;
+    uint64_t *s_full = y_empty + SY;
+    uint64_t *dp_full = s_full + 1;           // [2]
+    uint64_t *s_free = dp_full + 2;
+    uint64_t *ds_ready = s_free + 1;          // [2]
+    uint64_t *drain = ds_ready + 2;
+    static_assert(7 <= Lay::MAX_HANDOFF, "barrier count");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
+
+    const int warp = warp_id(), lane = lane_id();
+    const int z = blockIdx.z, h = blockIdx.y, kvh = h / p.group;
+    const int qtile = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+    const int L = p.src.L;
+    const int n = span_tokens(p.src, z);
+    const int4 hull = p.hull[static_cast<size_t>(z) * gridDim.x + qtile];
+    if (hull.y == 0) {
+        // no row of this tile sees a key: zeros, written by every thread
+        zero_rows<D>(p.dq, z, h, qtile * 128, min(128, L - qtile * 128), L, p.H);
+        return;
+    }
+    const int J0 = hull.x / 128, steps = (hull.y + 127) / 128 - J0;
+    const bool ragged = (n & 127) != 0 && J0 + steps == (n + 127) / 128;
+    if (threadIdx.x == 0) {
+        mbar_init(res_full, 1);
+        for (int s = 0; s < SX; ++s) {
+            mbar_init(&x_full[s], 1);
+            mbar_init(&x_empty[s], 1);
+        }
+        for (int s = 0; s < SY; ++s) {
+            mbar_init(&y_full[s], 1);
+            mbar_init(&y_empty[s], 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(&dp_full[0], 1);
+        mbar_init(&dp_full[1], 1);
+        mbar_init(s_free, SG::kArrivals);
+        mbar_init(&ds_ready[0], SG::kArrivals);
+        mbar_init(&ds_ready[1], SG::kArrivals);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+        prefetch_tensormap(&tmDO);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Lay::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wctx{abort_flag, p.src.status, p.timeout_ns};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint8_t *sQ = smem + Lay::OFF_A, *sDO = smem + Lay::OFF_B;
+            mbar_arrive_expect_tx(res_full, 2 * Lay::TILE_BYTES);
+            for (int s = 0; s < Lay::NSUB; ++s) {
+                tma_load_4d(&tmQ, res_full, sQ + s * Lay::SUB_BYTES, 64 * s, h, qtile * 128, z);
+                tma_load_4d(&tmDO, res_full, sDO + s * Lay::SUB_BYTES, 64 * s, h, qtile * 128, z);
+            }
+            int ix = 0;
+            for (int r = 0; r < steps; ++r) {
+                if (!span_ring_load<SX, Lay::NSUB>(&tmK, x_full, x_empty, smem + Lay::OFF_X, Lay::TILE_BYTES, r,
+                                                   (J0 + r) * 128, kvh, z, wctx))
+                    break;
+                ix = r + 1;
+            }
+            mbar_wait_drain(res_full, 0, p.timeout_ns);
+            ring_drain<SX>(x_full, ix, p.timeout_ns);
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            int iy = 0;
+            for (int r = 0; r < steps; ++r) {
+                if (!span_ring_load<SY, Lay::NSUB>(&tmV, y_full, y_empty, smem + Lay::OFF_Y, Lay::TILE_BYTES, r,
+                                                   (J0 + r) * 128, kvh, z, wctx))
+                    break;
+                iy = r + 1;
+            }
+            ring_drain<SY>(y_full, iy, p.timeout_ns);
+        }
+    } else if (warp == 1) {
+        // the whole warp runs converged; elect.sync picks the issuing lane
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wctx));
+        };
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_q = idesc_bf16_f32(128, D, false, true);
+        const uint32_t sQ = smem_u32(smem + Lay::OFF_A), sDO = smem_u32(smem + Lay::OFF_B);
+        const uint32_t xring = smem_u32(smem + Lay::OFF_X), yring = smem_u32(smem + Lay::OFF_Y);
+        constexpr uint32_t kDescHi = desc_hi(1024);
+        auto kslot = [&](int r) { return xring + (r % SX) * Lay::TILE_BYTES; };
+        auto vslot = [&](int r) { return yring + (r % SY) * Lay::TILE_BYTES; };
+        // X (128 rows of Q or dO) times Y^T (128 rows of K or V) into TMEM column `col`
+        auto issue_xyT = [&](uint32_t col, uint32_t xbase, uint32_t ybase) {
+            const uint32_t x_lo = desc_lo(xbase, 16), y_lo = desc_lo(ybase, 16);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t koff = ((kk >> 2) * Lay::SUB_BYTES + (kk & 3) * 32) >> 4;
+                mma_ss_lhw(tmem + col, x_lo + koff, y_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
+            }
+        };
+        bool ok = wait(res_full, 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+            issue_xyT(kColS, sQ, kslot(0));
+            mma_commit_w(s_full);
+            issue_xyT(kColDP0, sDO, vslot(0));
+            mma_commit_w(&dp_full[0]);
+            mma_commit_w(&y_empty[0]);
+        }
+        for (int r = 0; ok && r < steps; ++r) {
+            const bool more = r + 1 < steps;
+            if (more) {
+                if (!(ok = wait(&x_full[(r + 1) % SX], ((r + 1) / SX) & 1))) break;
+                if (!(ok = wait(s_free, r & 1))) break;
+                tc_fence_after();
+                issue_xyT(kColS, sQ, kslot(r + 1));
+                mma_commit_w(s_full);
+                if (!(ok = wait(&y_full[(r + 1) % SY], ((r + 1) / SY) & 1))) break;
+                // buffer (r+1) % 2 still holds dS_{r-1}: dQ += dS_{r-1} K_{r-1} was issued
+                // earlier by this thread and MMAs run in issue order
+                tc_fence_after();
+                issue_xyT((r + 1) & 1 ? kColDP1 : kColDP0, sDO, vslot(r + 1));
+                mma_commit_w(&dp_full[(r + 1) & 1]);
+                mma_commit_w(&y_empty[(r + 1) % SY]);
+            }
+            if (!more && ragged)
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_X + (r % SX) * Lay::TILE_BYTES, n & 127);
+            if (!(ok = wait(&ds_ready[r & 1], (r >> 1) & 1))) break;
+            tc_fence_after();
+            const uint32_t dcol = r & 1 ? kColDP1 : kColDP0;
+            const uint32_t k_lo = desc_lo(kslot(r), Lay::SUB_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mma_ts_lhw(tmem + kColDQ, tmem + dcol + SG::packed_col(kk), k_lo + kk * ((16 * 128) >> 4), kDescHi,
+                           idesc_q, (r > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_w(&x_empty[r % SX]);
+        }
+        mma_commit_w(drain);
+        mbar_wait_drain(drain, 0, p.timeout_ns);
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int w = (warp - 4) >> 2;      // warpgroup: tile columns [kCols w, kCols (w + 1))
+        const int quarter = warp & 3;
+        const int row = qtile * 128 + quarter * 32 + lane;
+        const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+        const int2 span = row_span(p.src, z, row, n);
+        __nv_bfloat16 *drow = p.dq + (static_cast<size_t>(z) * L + row) * (static_cast<size_t>(p.H) * D) +
+                              static_cast<size_t>(h) * D;
+        const ScoreCoef cf = make_score<MODE, SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
+                                                     SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
+        bool ok = true;
+        for (int r = 0; r < steps; ++r) {
+            ok = span_dq_tile<D, MODE, SCORE>(tmem + lane_bits, w, kColS, r & 1 ? kColDP1 : kColDP0, s_full, r & 1,
+                                              s_free, &dp_full[r & 1], (r >> 1) & 1, &ds_ready[r & 1], cf, row,
+                                              (J0 + r) * 128, span, wctx);
+            if (!ok) break;
+        }
+        // every MMA of this CTA has finished once the MMA warp's final commit lands
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
+        constexpr int kEpi = D / SG::NG >= 32 ? D / SG::NG : 32;
+        if (ok && w * kEpi < D) {
+            tc_fence_after();
+            store_row_from_tmem<D>(tmem + lane_bits + kColDQ, drow, row < L, span.x < span.y, p.alpha, w * kEpi,
+                                   kEpi);
+        }
+    }
+
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Lay::TMEM_COLS);
+    }
+}
+
+// dK/dV: one CTA per 128-key tile of a key head; streams the query tiles that
+// meet it, head after head of its group.  Tensor memory as bwd_dkdv_kernel:
+// [0,128) S^T, [128,256) dP^T then P^T and dS^T over it, dV, dK.
+template <int D, int MODE, int SCORE>
+__global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
+    span_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                     const SpanBwdParams p) {
+    constexpr int SX = BwdStages<D>::X, SY = BwdStages<D>::Y;
+    using Lay = SpanBwdLayout<D>;
+    using SG = BwdSigma<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1k(smem_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
+    uint64_t *res_full = bars;
+    uint64_t *x_full = bars + 1;              // Q ring
+    uint64_t *x_empty = x_full + SX;
+    uint64_t *y_full = x_empty + SX;          // dO ring
+    uint64_t *y_empty = y_full + SY;
+    uint64_t *s_full = y_empty + SY;
+    uint64_t *dp_full = s_full + 1;
+    uint64_t *s_free = dp_full + 1;
+    uint64_t *p_ready = s_free + 1;
+    uint64_t *ds_ready = p_ready + 1;
+    uint64_t *drain = ds_ready + 1;
+    static_assert(6 <= Lay::MAX_HANDOFF, "barrier count");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
+    int2 *met = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
+
+    const int warp = warp_id(), lane = lane_id();
+    const int z = blockIdx.z, kvh = blockIdx.y, ktile = blockIdx.x;
+    const int L = p.src.L, tiles = gridDim.x;
+    const int n = span_tokens(p.src, z);
+    const int k0 = ktile * 128, k1 = min(k0 + 128, n);
+    // first and last query tile whose hull meets this key tile
+    const int4 *hull = p.hull + static_cast<size_t>(z) * tiles;
+    {
+        int first = INT_MAX, last = -1;
+        for (int i = threadIdx.x; i < tiles; i += SG::kThreads) {
+            const int4 t = hull[i];
+            if (t.x < k1 && t.y > k0) {
+                first = min(first, i);
+                last = max(last, i);
+            }
+        }
+        first = __reduce_min_sync(0xffffffffu, first);
+        last = __reduce_max_sync(0xffffffffu, last);
+        if (lane == 0) met[warp] = make_int2(first, last);
+    }
+    __syncthreads();
+    int I0 = INT_MAX, I1 = -1;
+#pragma unroll
+    for (int u = 0; u < SG::kThreads / 32; ++u) {
+        I0 = min(I0, met[u].x);
+        I1 = max(I1, met[u].y);
+    }
+    if (I1 < 0) {
+        // no row sees a key of this tile: zeros, written by every thread
+        const int rows = min(128, L - k0);
+        zero_rows<D>(p.dk, z, kvh, k0, rows, L, p.Hk);
+        zero_rows<D>(p.dv, z, kvh, k0, rows, L, p.Hk);
+        return;
+    }
+    const int per_head = I1 - I0 + 1, steps = per_head * p.group;
+    const bool ragged = (n & 127) != 0 && I1 == n / 128;
+    if (threadIdx.x == 0) {
+        mbar_init(res_full, 1);
+        for (int s = 0; s < SX; ++s) {
+            mbar_init(&x_full[s], 1);
+            mbar_init(&x_empty[s], 1);
+        }
+        for (int s = 0; s < SY; ++s) {
+            mbar_init(&y_full[s], 1);
+            mbar_init(&y_empty[s], 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(s_free, SG::kArrivals);
+        mbar_init(p_ready, SG::kArrivals);
+        mbar_init(ds_ready, SG::kArrivals);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+        prefetch_tensormap(&tmDO);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Lay::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wctx{abort_flag, p.src.status, p.timeout_ns};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint8_t *sK = smem + Lay::OFF_A, *sV = smem + Lay::OFF_B;
+            mbar_arrive_expect_tx(res_full, 2 * Lay::TILE_BYTES);
+            for (int s = 0; s < Lay::NSUB; ++s) {
+                tma_load_4d(&tmK, res_full, sK + s * Lay::SUB_BYTES, 64 * s, kvh, k0, z);
+                tma_load_4d(&tmV, res_full, sV + s * Lay::SUB_BYTES, 64 * s, kvh, k0, z);
+            }
+            int ix = 0, i = I0, h = kvh * p.group;
+            for (int r = 0; r < steps; ++r) {
+                if (!span_ring_load<SX, Lay::NSUB>(&tmQ, x_full, x_empty, smem + Lay::OFF_X, Lay::TILE_BYTES, r,
+                                                   i * 128, h, z, wctx))
+                    break;
+                ix = r + 1;
+                if (++i > I1) {
+                    i = I0;
+                    ++h;
+                }
+            }
+            mbar_wait_drain(res_full, 0, p.timeout_ns);
+            ring_drain<SX>(x_full, ix, p.timeout_ns);
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            int iy = 0, i = I0, h = kvh * p.group;
+            for (int r = 0; r < steps; ++r) {
+                if (!span_ring_load<SY, Lay::NSUB>(&tmDO, y_full, y_empty, smem + Lay::OFF_Y, Lay::TILE_BYTES, r,
+                                                   i * 128, h, z, wctx))
+                    break;
+                iy = r + 1;
+                if (++i > I1) {
+                    i = I0;
+                    ++h;
+                }
+            }
+            ring_drain<SY>(y_full, iy, p.timeout_ns);
+        }
+    } else if (warp == 1) {
+        // the whole warp runs converged; elect.sync picks the issuing lane
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wctx));
+        };
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_kv = idesc_bf16_f32(128, D, false, true);
+        const uint32_t sK = smem_u32(smem + Lay::OFF_A), sV = smem_u32(smem + Lay::OFF_B);
+        const uint32_t xring = smem_u32(smem + Lay::OFF_X), yring = smem_u32(smem + Lay::OFF_Y);
+        auto qslot = [&](int r) { return xring + (r % SX) * Lay::TILE_BYTES; };
+        auto doslot = [&](int r) { return yring + (r % SY) * Lay::TILE_BYTES; };
+        constexpr uint32_t kDescHi = desc_hi(1024);
+        auto issue_xyT = [&](uint32_t col, uint32_t xbase, uint32_t ybase) {
+            const uint32_t x_lo = desc_lo(xbase, 16), y_lo = desc_lo(ybase, 16);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t koff = ((kk >> 2) * Lay::SUB_BYTES + (kk & 3) * 32) >> 4;
+                mma_ss_lhw(tmem + col, x_lo + koff, y_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
+            }
+        };
+        // acc += A(TMEM, packed over `acol`) * B (128 query rows, MN-major)
+        auto issue_acc = [&](uint32_t acc, uint32_t acol, uint32_t bbase, bool first) {
+            const uint32_t b_lo = desc_lo(bbase, Lay::SUB_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mma_ts_lhw(tmem + acc, tmem + acol + SG::packed_col(kk), b_lo + kk * ((16 * 128) >> 4), kDescHi,
+                           idesc_kv, (!first || kk > 0) ? 1u : 0u);
+        };
+        bool ok = wait(res_full, 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+            issue_xyT(Lay::COL_S, sK, qslot(0));
+            mma_commit_w(s_full);
+            issue_xyT(Lay::COL_DP, sV, doslot(0));
+            mma_commit_w(dp_full);
+        }
+        int left = per_head;          // query tiles left of this head
+        for (int r = 0; ok && r < steps; ++r) {
+            const bool more = r + 1 < steps;
+            if (more) {
+                if (!(ok = wait(&x_full[(r + 1) % SX], ((r + 1) / SX) & 1))) break;
+                if (!(ok = wait(s_free, r & 1))) break;
+                tc_fence_after();
+                issue_xyT(Lay::COL_S, sK, qslot(r + 1));
+                mma_commit_w(s_full);
+            }
+            if (ragged && left == 1) {
+                // S^T and dP^T may still be reading these rows: as columns that are masked
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_Y + (r % SY) * Lay::TILE_BYTES, n & 127);
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_X + (r % SX) * Lay::TILE_BYTES, n & 127);
+            }
+            if (!(ok = wait(p_ready, r & 1))) break;
+            tc_fence_after();
+            issue_acc(Lay::COL_ACC0, Lay::COL_DP, doslot(r), r == 0);       // dV += P^T dO
+            mma_commit_w(&y_empty[r % SY]);
+            if (!(ok = wait(ds_ready, r & 1))) break;
+            tc_fence_after();
+            issue_acc(Lay::COL_ACC1, Lay::COL_DP + SG::kPacked, qslot(r), r == 0);  // dK += dS^T Q
+            mma_commit_w(&x_empty[r % SX]);
+            if (more) {
+                // dP^T of r + 1 overwrites P^T and dS^T of r, read by the two MMAs just
+                // issued (MMAs run in issue order)
+                if (!(ok = wait(&y_full[(r + 1) % SY], ((r + 1) / SY) & 1))) break;
+                tc_fence_after();
+                issue_xyT(Lay::COL_DP, sV, doslot(r + 1));
+                mma_commit_w(dp_full);
+            }
+            if (--left == 0) left = per_head;
+        }
+        mma_commit_w(drain);
+        mbar_wait_drain(drain, 0, p.timeout_ns);
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int w = (warp - 4) >> 2;      // warpgroup: query columns [kCols w, kCols (w + 1))
+        const int quarter = warp & 3;
+        const int key = k0 + quarter * 32 + lane;
+        const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+        const size_t roff = (static_cast<size_t>(z) * L + key) * (static_cast<size_t>(p.Hk) * D) +
+                            static_cast<size_t>(kvh) * D;
+        constexpr int kOut = SG::NG / 2;
+        const bool is_dv = w < kOut;
+        __nv_bfloat16 *dst = (is_dv ? p.dv : p.dk) + roff;
+        const int2 *clean = p.clean + static_cast<size_t>(z) * tiles * 128 + SG::kCols * w;
+        const uint32_t tS = tmem + lane_bits + Lay::COL_S + SG::kCols * w;
+        const uint32_t tD = tmem + lane_bits + Lay::COL_DP + SG::kCols * w;
+        const float bias = bias_of(p.bias_z, p.bias, z);
+        int i = I0, h = kvh * p.group;
+        ScoreCoef cf = make_score<MODE, SCORE>(p.alpha, bias, p.cap, SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
+        bool ok = true;
+        for (int r = 0; r < steps; ++r) {
+            const int4 t = __ldg(hull + i);
+            const bool whole = t.z <= k0 && t.w >= k1;
+            ok = span_dkdv_tile<D, MODE, SCORE>(tS, tD, s_full, s_free, dp_full, p_ready, ds_ready, r & 1, cf, key,
+                                                i * 128 + SG::kCols * w, whole, clean + i * 128, wctx);
+            if (!ok) break;
+            if (++i > I1) {
+                i = I0;
+                ++h;
+                if (SCORE & kScoreSlope && r + 1 < steps)
+                    cf = make_score<MODE, SCORE>(p.alpha, bias, p.cap, p.slopes[h]);
+            }
+        }
+        // every MMA of this CTA has finished once the MMA warp's final commit lands
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
+        if (ok) {
+            tc_fence_after();
+            store_row_from_tmem<D>(tmem + lane_bits + (is_dv ? Lay::COL_ACC0 : Lay::COL_ACC1), dst, key < L, key < n,
+                                   is_dv ? 1.0f : p.alpha, (w % kOut) * (D / kOut), D / kOut);
+        }
+    }
+
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Lay::TMEM_COLS);
+    }
+}
+
+}  // namespace sigattn

@@ -1,0 +1,355 @@
+// Forward of the masked attention (span_score.cuh), bf16: one CTA per pair of
+// 128-row query tiles of one (sample, head), the structure of the padding-only
+// forward at D = 128 (fwd_sm100.cuh), with these differences:
+//
+//  - the CTA reads its 256 rows' spans first; tile t visits the key tiles of
+//    its rows' hull only, [j0_t, j1_t), and the rings stream the union of the
+//    two.  A pair of causal tiles so costs its visible tiles plus half a
+//    diagonal tile each, and packed documents cost what their own keys cost;
+//  - pairs are started from the last rows on: with causal spans those see the
+//    most keys, and the short ones fill in behind them;
+//  - query head h reads key head h / (H / Hk);
+//  - a warp masks a 64-key half only where one of its rows does not see all of
+//    it (the rows' bounds are in registers; whole tiles pay one vote);
+//  - the MMA warp zeroes the value rows at or beyond n of the last key tile
+//    while the sigma warps work on its scores, so that NaN in padding never
+//    meets the product.
+//
+// Bound: as the padding-only forward, one MUFU op per score (two with a cap)
+// against 4 D tensor FLOP; at D = 128 without a cap the two pipes balance.
+#pragma once
+
+#include "fwd_sm100.cuh"
+#include "span_score.cuh"
+
+namespace sigattn {
+
+struct SpanFwdParams {
+    __nv_bfloat16 *o;
+    SpanSource src;
+    int H, group;          // query heads, query heads per key head
+    float alpha, bias, cap;
+    const float *bias_z;   // device float[Z] or null
+    const float *slopes;   // device float[H] or null
+    uint64_t timeout_ns;
+};
+
+template <int D>
+struct SpanFwdLayout : FwdLayout<D, FwdStages<D>::K, FwdStages<D>::V> {
+    using Base = FwdLayout<D, FwdStages<D>::K, FwdStages<D>::V>;
+    static constexpr int OFF_HULL = (Base::OFF_SAMPLE + 7) & ~7;   // 8 warps x {lo, hi}
+    static constexpr int SMEM_ALLOC = OFF_HULL + 64 + 1024;
+    static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+};
+
+template <int D, int MODE, int SCORE>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    span_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const SpanFwdParams p) {
+    constexpr int KS = FwdStages<D>::K, VS = FwdStages<D>::V;
+    using Lay = SpanFwdLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1k(smem_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
+    uint64_t *q_full = bars;
+    uint64_t *k_full = bars + 1;
+    uint64_t *k_empty = k_full + KS;
+    uint64_t *v_full = k_empty + KS;
+    uint64_t *v_empty = v_full + VS;
+    uint64_t *s_full = v_empty + VS;
+    uint64_t *p_full = s_full + 2;
+    uint64_t *drain = p_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
+    int2 *hull = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
+
+    const int warp = warp_id(), lane = lane_id();
+    const int z = blockIdx.z, h = blockIdx.y, kvh = h / p.group;
+    const int qtile0 = static_cast<int>(gridDim.x - 1 - blockIdx.x) * 2;
+    const int L = p.src.L;
+    const int n = span_tokens(p.src, z);
+    if (warp < 8) {
+        const int2 r = row_span(p.src, z, qtile0 * 128 + static_cast<int>(threadIdx.x), n);
+        const int lo = __reduce_min_sync(0xffffffffu, r.x < r.y ? r.x : INT_MAX);
+        const int hi = __reduce_max_sync(0xffffffffu, r.y);
+        if (lane == 0) hull[warp] = make_int2(lo, hi);
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        for (int s = 0; s < KS; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < VS; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 256);  // the two sigma warpgroups of tile t
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    // key tiles [j0[t], j1[t]) of query tile t; an empty tile has j0 = j1 = 0
+    int j0[2], j1[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        int lo = INT_MAX, hi = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int2 r = hull[4 * t + w];
+            lo = min(lo, r.x);
+            hi = max(hi, r.y);
+        }
+        j0[t] = hi > 0 ? lo / 128 : 0;
+        j1[t] = (hi + 127) / 128;
+    }
+    const bool live0 = j1[0] > 0, live1 = j1[1] > 0;
+    const size_t row_stride = static_cast<size_t>(p.H) * D;
+    if (!live0 && !live1) {
+        // no row sees a key: zeros, written by every thread
+        const int r0 = qtile0 * 128, rows = min(256, L - r0);
+        constexpr int V4 = D / 8;
+        for (int e = threadIdx.x; e < rows * V4; e += kFwdThreads) {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<size_t>(z) * L + r0 + e / V4) * row_stride +
+                                                   static_cast<size_t>(h) * D);
+            dst[e % V4] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    const int J0 = live0 ? (live1 ? min(j0[0], j0[1]) : j0[0]) : j0[1];
+    const int J1 = max(j1[0], j1[1]);
+    const int steps = J1 - J0;
+    // the last key tile, when n ends inside it: its value rows are cleaned
+    const bool ragged = (n & 127) != 0 && J1 == (n + 127) / 128;
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Lay::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wctx{abort_flag, p.src.status, p.timeout_ns};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint8_t *sQ = smem + Lay::OFF_Q;
+            uint8_t *sK = smem + Lay::OFF_K;
+            mbar_arrive_expect_tx(q_full, (live0 + live1) * Lay::TILE_BYTES);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!(t ? live1 : live0)) continue;
+                for (int s = 0; s < Lay::NSUB; ++s)
+                    tma_load_4d(&tmQ, q_full, sQ + t * Lay::TILE_BYTES + s * Lay::SUB_BYTES, 64 * s, h,
+                                (qtile0 + t) * 128, z);
+            }
+            int issued = 0;
+            for (int r = 0; r < steps; ++r) {
+                const int sk = r % KS;
+                if (r >= KS && !mbar_wait(&k_empty[sk], ((r / KS) - 1) & 1, wctx)) break;
+                mbar_arrive_expect_tx(&k_full[sk], Lay::TILE_BYTES);
+                for (int s = 0; s < Lay::NSUB; ++s)
+                    tma_load_4d(&tmK, &k_full[sk], sK + sk * Lay::TILE_BYTES + s * Lay::SUB_BYTES, 64 * s, kvh,
+                                (J0 + r) * 128, z);
+                issued = r + 1;
+            }
+            // every issued load must land before the CTA's shared memory is released
+            mbar_wait_drain(q_full, 0, p.timeout_ns);
+            for (int r = (issued > KS ? issued - KS : 0); r < issued; ++r)
+                mbar_wait_drain(&k_full[r % KS], (r / KS) & 1, p.timeout_ns);
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            uint8_t *sV = smem + Lay::OFF_V;
+            int issued = 0;
+            for (int r = 0; r < steps; ++r) {
+                const int sv = r % VS;
+                if (r >= VS && !mbar_wait(&v_empty[sv], ((r / VS) - 1) & 1, wctx)) break;
+                mbar_arrive_expect_tx(&v_full[sv], Lay::TILE_BYTES);
+                for (int s = 0; s < Lay::NSUB; ++s)
+                    tma_load_4d(&tmV, &v_full[sv], sV + sv * Lay::TILE_BYTES + s * Lay::SUB_BYTES, 64 * s, kvh,
+                                (J0 + r) * 128, z);
+                issued = r + 1;
+            }
+            for (int r = (issued > VS ? issued - VS : 0); r < issued; ++r)
+                mbar_wait_drain(&v_full[r % VS], (r / VS) & 1, p.timeout_ns);
+        }
+    } else if (warp == 1) {
+        // the whole warp runs converged; elect.sync picks the issuing lane
+        auto wt = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wctx));
+        };
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+        const uint32_t sQ = smem_u32(smem + Lay::OFF_Q);
+        const uint32_t sK = smem_u32(smem + Lay::OFF_K);
+        const uint32_t sV = smem_u32(smem + Lay::OFF_V);
+        constexpr uint32_t kDescHi = desc_hi(1024);
+        auto issue_s = [&](int t, uint32_t kbase) {
+            const uint32_t q_lo = desc_lo(sQ + t * Lay::TILE_BYTES, 16), k_lo = desc_lo(kbase, 16);
+            const uint32_t d_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t koff = ((kk >> 2) * Lay::SUB_BYTES + (kk & 3) * 32) >> 4;
+                mma_ss_lhw(d_tmem, q_lo + koff, k_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_w(&s_full[t]);
+        };
+        auto issue_pv = [&](int t, uint32_t vbase, bool first) {
+            const uint32_t d_tmem = tmem + (t ? Lay::COL_O1 : Lay::COL_O0);
+            const uint32_t a_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0);
+            const uint32_t v_lo = desc_lo(vbase, Lay::SUB_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mma_ts_lhw(d_tmem, a_tmem + kk * 8 + (kk >= 4 ? 32 : 0), v_lo + kk * ((16 * 128) >> 4), kDescHi,
+                           idesc_o, (!first || kk > 0) ? 1u : 0u);
+        };
+        // Per key tile j: for each query tile that visits j, O_t += P_t V_j once
+        // its P is there, then S_t of j + 1 over it.  MMAs from one thread
+        // run in issue order, so P_t has been read before the next scores are
+        // written.  A key tile that neither visits (a gap between the two hulls)
+        // passes through the rings unread.
+        bool ok = wt(q_full, 0) && wt(&k_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (j0[t] == J0 && J0 < j1[t]) issue_s(t, sK);
+            mma_commit_w(&k_empty[0]);
+        }
+        for (int r = 0; ok && r < steps; ++r) {
+            const int j = J0 + r, sv = r % VS, sk = (r + 1) % KS;
+            const bool more = r + 1 < steps;
+            const uint32_t vbase = sV + sv * Lay::TILE_BYTES;
+            const uint32_t knext = sK + sk * Lay::TILE_BYTES;
+            if (!(ok = wt(&v_full[sv], (r / VS) & 1))) break;
+            if (!more && ragged)
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_V + sv * Lay::TILE_BYTES, n & 127);
+            bool have_k = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (j >= j0[t] && j < j1[t]) {
+                    if (!(ok = wt(&p_full[t], (j - j0[t]) & 1))) break;
+                    tc_fence_after();
+                    issue_pv(t, vbase, j == j0[t]);
+                }
+                if (t == 1) mma_commit_w(&v_empty[sv]);
+                if (more && j + 1 >= j0[t] && j + 1 < j1[t]) {
+                    if (!have_k && !(ok = wt(&k_full[sk], ((r + 1) / KS) & 1))) break;
+                    have_k = true;
+                    tc_fence_after();
+                    issue_s(t, knext);
+                }
+            }
+            if (!ok) break;
+            if (more) {
+                if (!have_k && !(ok = wt(&k_full[sk], ((r + 1) / KS) & 1))) break;
+                mma_commit_w(&k_empty[sk]);
+            }
+        }
+        // no MMA may still be running when TMEM is released
+        mma_commit_w(drain);
+        mbar_wait_drain(drain, 0, p.timeout_ns);
+        __syncwarp();
+    } else if (warp >= 4) {
+        // sigma warpgroups: warpgroup g works on query tile t = g / 2, key columns
+        // [64 c, 64 c + 64) of each key tile, c = g % 2
+        const int g = (warp - 4) >> 2;
+        const int t = g >> 1, c = g & 1;
+        const int quarter = warp & 3;  // TMEM lane quarter this warp may access
+        const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+        const int row = (qtile0 + t) * 128 + quarter * 32 + lane;
+        const int2 span = row_span(p.src, z, row, n);
+        const int ja = t ? j0[1] : j0[0], jb = t ? j1[1] : j1[0];
+        bool ok = true;
+        if (jb > 0) {
+            const ScoreCoef cf = make_score<MODE, SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
+                                                         SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
+            const uint32_t tS = tmem + lane_bits + (t ? Lay::COL_S1 : Lay::COL_S0) + 64 * c;
+            for (int j = ja; j < jb; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (j - ja) & 1, wctx));
+                if (!ok) break;
+                tc_fence_after();
+                const int key0 = j * 128 + 64 * c;   // first key of this half
+                const bool whole = __all_sync(0xffffffffu, span.x <= key0 && span.y >= key0 + 64);
+                // two chunks of 32 scores per thread; P of chunk u lies over S
+                // columns [16 u, 16 u + 16) of this half, already read
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t r[32];
+                    tmem_ld32(tS + 32 * u, r);
+                    uint32_t pk[16];
+                    const float rel = static_cast<float>(row - key0 - 32 * u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 pr = score_p2<MODE, SCORE>(__uint_as_float(r[2 * i]),
+                                                                __uint_as_float(r[2 * i + 1]), cf,
+                                                                rel - static_cast<float>(2 * i));
+                        pk[i] = pack_bf16x2(pr.x, pr.y);
+                    }
+                    if (!whole)
+                        keep_bits(pk, bit_range(span.x - key0 - 32 * u, span.y - key0 - 32 * u));
+                    tmem_st16(tS + 16 * u, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[t]);
+            }
+            // every MMA of this CTA has finished once the MMA warp's final commit lands
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
+        }
+        // epilogue: warpgroup g writes columns [c D/2, c D/2 + D/2) of query tile t
+        constexpr int HALF = D / 2;
+        __nv_bfloat16 *orow = p.o + (static_cast<size_t>(z) * L + row) * row_stride +
+                              static_cast<size_t>(h) * D + c * HALF;
+        if (jb > 0) {
+            if (ok) {
+                tc_fence_after();
+                const uint32_t tO = tmem + lane_bits + (t ? Lay::COL_O1 : Lay::COL_O0) + c * HALF;
+                const bool valid = span.x < span.y;
+#pragma unroll
+                for (int cc = 0; cc < HALF / 32; ++cc) {
+                    uint32_t r[32];
+                    tmem_ld32(tO + 32 * cc, r);
+                    if (row < L) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(orow + 32 * cc);
+#pragma unroll
+                        for (int v4 = 0; v4 < 4; ++v4) {
+                            uint4 w;
+                            w.x = valid ? pack_bf16x2(__uint_as_float(r[8 * v4 + 0]), __uint_as_float(r[8 * v4 + 1])) : 0u;
+                            w.y = valid ? pack_bf16x2(__uint_as_float(r[8 * v4 + 2]), __uint_as_float(r[8 * v4 + 3])) : 0u;
+                            w.z = valid ? pack_bf16x2(__uint_as_float(r[8 * v4 + 4]), __uint_as_float(r[8 * v4 + 5])) : 0u;
+                            w.w = valid ? pack_bf16x2(__uint_as_float(r[8 * v4 + 6]), __uint_as_float(r[8 * v4 + 7])) : 0u;
+                            dst[v4] = w;
+                        }
+                    }
+                }
+            }
+        } else if (row < L) {
+            // no row of this tile sees a key: exact zeros
+            uint4 *dst = reinterpret_cast<uint4 *>(orow);
+#pragma unroll
+            for (int v4 = 0; v4 < HALF / 8; ++v4) dst[v4] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+
+    // every warp converges before the block-wide barrier (the producer roles
+    // ran on one lane)
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Lay::TMEM_COLS);
+    }
+}
+
+}  // namespace sigattn

@@ -1,0 +1,303 @@
+"""GPU tests of the masked attention: exact counts under every mask, numeric parity with the definition in 64 bits (bounds
+derived in tests/_span_ref.py), NaN in padding, gradients against differences, capture, streams and the mask builder."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _compare as C
+from tests import _span_ref as R
+
+pytestmark = pytest.mark.gpu
+
+sa = pytest.importorskip("padding_aware_sigmoid_b200")
+
+MASKS = ["none", "full", "causal", "prefix", "docs", "docs_causal", "window", "holes", "scatter"]
+
+
+@pytest.fixture
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield torch.device("cuda", 0)
+    assert sa.last_device_status() == 0
+
+
+@pytest.fixture
+def exp_mode():
+    old = sa.get_sigmoid_mode()
+    sa.set_sigmoid_mode(sa.SIGMOID_EXP)
+    yield
+    sa.set_sigmoid_mode(old)
+
+
+def _lens(Z, L, seed):
+    g = np.random.default_rng(seed)
+    n = g.integers(0, L + 1, size=Z).astype(np.int32)
+    n[0] = L
+    return n
+
+
+def _spans(mask, n, L, dev, seed=3):
+    return None if mask == "none" else R.make_spans(mask, n, L, seed).to(dev)
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("shape", [(3, 1, 2, 2, 64), (2, 77, 2, 1, 64), (3, 128, 2, 2, 128), (2, 129, 4, 2, 128),
+                                   (2, 300, 6, 2, 64), (3, 515, 4, 1, 128), (2, 1100, 2, 2, 64)])
+def test_visible_pairs_are_counted_exactly(dev, mask, shape):
+    """With all scores 0 sigma is exactly 1/2 and its derivative 1/4, so marked keys and queries are counted: every output is
+    a small integer that bf16 holds, and one wrong pair shows."""
+    Z, L, H, Hk, D = shape
+    n = _lens(Z, L, L + H)
+    spans = _spans(mask, n, L, dev)
+    g = np.random.default_rng(L * 7 + H)
+    share = min(1.0, 40 / L)
+    mark = lambda heads: torch.as_tensor((g.random((Z, L, heads)) < share).astype(np.float32))     # noqa: E731
+    mq, mk, mv, mo = mark(H), mark(Hk), mark(Hk), mark(H)
+    t = lambda heads: torch.zeros(Z, L, heads, D)      # noqa: E731
+    q, k, v, do = t(H), t(Hk), t(Hk), t(H)
+    q[..., 0], k[..., 1] = mq, mk                # q . k = 0
+    v[..., 2], do[..., 2] = 2.0, 1.0             # dP = 2, dS = 1/2
+    v[..., 3], do[..., 4] = 2.0 * mv, 2.0 * mo
+    dt = torch.bfloat16
+    q, k, v, do = (x.to(dev, dt) for x in (q, k, v, do))
+    seq = torch.as_tensor(n, device=dev)
+    out = torch.full_like(q, float("nan"))
+    o = sa.fwd_span(q, k, v, seq, 2.0, 0.0, spans=spans, out=out)
+    dq, dk, dv = sa.bwd_span(q, k, v, do, seq, 2.0, 0.0, spans=spans, dq=torch.full_like(q, float("nan")),
+                             dk=torch.full_like(k, float("nan")), dv=torch.full_like(v, float("nan")))
+    m = R.visible(spans, n, L).double()
+    G = H // Hk
+    fold = lambda x: x.view(Z, Hk, G, L).sum(2)        # noqa: E731
+    up = lambda x: x.permute(0, 2, 1).double()         # noqa: E731
+    want_o = (m[:, None] @ up(mv).repeat_interleave(G, 1)[..., None])[..., 0].permute(0, 2, 1)
+    assert torch.equal(o[..., 3].cpu().double(), want_o)
+    want_q = (m[:, None] @ up(mk).repeat_interleave(G, 1)[..., None])[..., 0].permute(0, 2, 1)
+    assert torch.equal(dq[..., 1].cpu().double(), want_q)
+    want_k = fold((m.mT[:, None] @ up(mq)[..., None])[..., 0]).permute(0, 2, 1)
+    assert torch.equal(dk[..., 0].cpu().double(), want_k)
+    want_v = fold((m.mT[:, None] @ up(mo)[..., None])[..., 0]).permute(0, 2, 1)
+    assert torch.equal(dv[..., 4].cpu().double(), want_v)
+    for x in (o, dq, dk, dv):
+        assert not x[..., 5:].any()
+
+
+def _tensors(Z, L, H, Hk, D, dtype, dev, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda h, s: (torch.randn(Z, L, h, D, generator=g) * s).to(dtype).to(dev)      # noqa: E731
+    return r(H, scale), r(Hk, scale), r(Hk, 1.0), r(H, 1.0)
+
+
+CASES = [  # Z, L, H, Hk, D, mask, cap, slopes
+    (2, 1, 2, 1, 128, "causal", 0.0, False),
+    (2, 200, 2, 2, 64, "none", 30.0, False),
+    (3, 257, 4, 2, 128, "causal", 20.0, True),
+    (2, 385, 3, 1, 64, "prefix", 0.0, True),
+    (2, 640, 2, 2, 128, "docs", 50.0, False),
+    (2, 511, 4, 4, 64, "docs_causal", 30.0, True),
+    (1, 900, 2, 1, 128, "window", 0.0, True),
+    (2, 300, 6, 2, 64, "holes", 0.0, False),
+    (2, 260, 2, 1, 128, "scatter", 30.0, True),
+]
+
+
+def _run_case(case, dev, dtype, tanh):
+    Z, L, H, Hk, D, mask, cap, sl = case
+    n = _lens(Z, L, L)
+    q, k, v, do = _tensors(Z, L, H, Hk, D, dtype, dev, L + D, 2.0 if cap else 1.0)
+    spans = _spans(mask, n, L, dev)
+    slopes = torch.linspace(0.5, 0.01, H, device=dev) if sl else None
+    bias = -math.log(L) / 2 + 0.25 * np.arange(Z)
+    bz = torch.as_tensor(bias.astype(np.float32), device=dev)
+    seq = torch.as_tensor(n, device=dev)
+    alpha = D ** -0.5
+    o = sa.fwd_span(q, k, v, seq, alpha, bz, spans=spans, cap=cap, slopes=slopes)
+    grads = sa.bwd_span(q, k, v, do, seq, alpha, bz, spans=spans, cap=cap, slopes=slopes)
+    sees = R.visible(spans, n, L)
+    ref, bound = R.reference(q, k, v, do, sees, alpha, bias.astype(np.float32), cap, slopes, dtype == torch.float32)
+    for name, x in zip(("O", "dQ", "dK", "dV"), (o, *grads)):
+        if tanh:
+            C.assert_close(x.float().cpu().numpy(), ref[name].numpy(), "bf16", name)
+        else:
+            R.assert_within(x, ref[name], bound[name], name)
+        dead = ~(sees.any(-1) if name in ("O", "dQ") else sees.any(1))
+        assert not x[dead.to(dev)].any(), f"{name}: rows that take no part are not zero"
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_parity_exp(dev, exp_mode, case):
+    _run_case(case, dev, torch.bfloat16, False)
+
+
+@pytest.mark.parametrize("case", CASES[1:])
+def test_parity_tanh(dev, case):
+    _run_case(case, dev, torch.bfloat16, True)
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_parity_fp32(dev, case):
+    _run_case(case, dev, torch.float32, False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_in_padding_never_reaches_a_result(dev, dtype, D):
+    Z, L, H, Hk = 3, 400, 4, 2
+    n = np.asarray([400, 131, 0], np.int32)
+    q, k, v, do = _tensors(Z, L, H, Hk, D, dtype, dev, 5)
+    seq = torch.as_tensor(n, device=dev)
+    for mask in ("none", "causal", "docs"):
+        spans = _spans(mask, n, L, dev)
+        clean = (sa.fwd_span(q, k, v, seq, 0.1, -2.0, spans=spans), *sa.bwd_span(q, k, v, do, seq, 0.1, -2.0, spans=spans))
+        bad = []
+        for t in (q, k, v, do):
+            b = t.clone()
+            for z in range(Z):
+                b[z, n[z]:] = float("nan")
+                b[z, n[z]:, :, ::3] = float("inf")
+            bad.append(b)
+        dirty = (sa.fwd_span(*bad[:3], seq, 0.1, -2.0, spans=spans), *sa.bwd_span(*bad, seq, 0.1, -2.0, spans=spans))
+        for a, b in zip(clean, dirty):
+            assert torch.equal(a, b)
+
+
+def test_equals_the_padding_only_call_without_terms(dev):
+    """No spans, no cap, no slopes: the same operation as fwd / bwd (which share one rounding of P and of dS each)."""
+    Z, L, H, D = 2, 700, 2, 128
+    q, k, v, do = _tensors(Z, L, H, H, D, torch.bfloat16, dev, 9)
+    seq = torch.as_tensor(np.asarray([700, 333], np.int32), device=dev)
+    assert torch.equal(sa.fwd(q, k, v, seq, seq, 0.09, -6.0), sa.fwd_span(q, k, v, seq, 0.09, -6.0))
+    for a, b in zip(sa.bwd(q, k, v, do, seq, seq, 0.09, -6.0), sa.bwd_span(q, k, v, do, seq, 0.09, -6.0)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cap,sl", [(0.0, False), (4.0, True)])
+def test_gradients_against_differences(dev, cap, sl):
+    """fp32 path: central differences of <O, dO> along random directions.  The step's second-order error is h^2 / 6 of a third
+    derivative of order 1, the values' rounding n 2^-24 / h: both below 1e-3 of the directional derivative's scale at h = 1e-2."""
+    Z, L, H, Hk, D = 1, 90, 2, 1, 64
+    n = np.asarray([83], np.int32)
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.float32, dev, 21)
+    spans = _spans("docs_causal", n, L, dev)
+    slopes = torch.tensor([0.3, 0.05], device=dev) if sl else None
+    seq = torch.as_tensor(n, device=dev)
+    f = lambda a, b, c: float((sa.fwd_span(a, b, c, seq, 0.125, -1.0, spans=spans, cap=cap, slopes=slopes).double() *   # noqa: E731
+                               do.double()).sum())
+    grads = sa.bwd_span(q, k, v, do, seq, 0.125, -1.0, spans=spans, cap=cap, slopes=slopes)
+    for at, grad in enumerate(grads):
+        d = torch.randn(grad.shape, generator=torch.Generator().manual_seed(at)).to(dev)
+        h = 1e-2
+        up, down = [q, k, v], [q, k, v]
+        up[at], down[at] = up[at] + h * d, down[at] - h * d
+        got = (f(*up) - f(*down)) / (2 * h)
+        want = float((grad.double() * d.double()).sum())
+        scale = float((grad.double() * d.double()).norm())
+        assert abs(got - want) <= 2e-3 * max(scale, abs(want)) + 1e-3
+
+
+def test_capture_and_replay_with_new_inputs(dev):
+    Z, L, H, Hk, D = 2, 500, 4, 2, 64
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 31)
+    seq = torch.as_tensor(np.asarray([500, 260], np.int32), device=dev)
+    spans = sa.mask_spans(seq, L, causal=True)
+    slopes = torch.full((H,), 0.1, device=dev)
+    ws = torch.empty(sa.bwd_span_workspace_bytes(Z, L, q.dtype), dtype=torch.uint8, device=dev)
+    outs = [torch.empty_like(t) for t in (q, q, k, v)]
+
+    def step():
+        sa.mask_spans(seq, L, causal=True, out=spans)
+        sa.fwd_span(q, k, v, seq, 0.125, -3.0, spans=spans, cap=10.0, slopes=slopes, out=outs[0])
+        sa.bwd_span(q, k, v, do, seq, 0.125, -3.0, spans=spans, cap=10.0, slopes=slopes, dq=outs[1], dk=outs[2],
+                    dv=outs[3], workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        for t, u in zip((q, k, v, do), _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, seed)):
+            t.copy_(u)
+        seq.copy_(torch.as_tensor(np.asarray([77 * seed, 500 - seed], np.int32)))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in outs]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, outs))
+
+
+def test_two_streams_at_once_and_repeats_are_bitwise_equal(dev):
+    Z, L, H, Hk, D = 3, 777, 6, 2, 128
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 41)
+    seq = torch.as_tensor(np.asarray([777, 400, 129], np.int32), device=dev)
+    spans = _spans("docs_causal", [777, 400, 129], L, dev)
+    call = lambda: (sa.fwd_span(q, k, v, seq, 0.1, -4.0, spans=spans, cap=30.0),      # noqa: E731
+                    *sa.bwd_span(q, k, v, do, seq, 0.1, -4.0, spans=spans, cap=30.0))
+    want = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in range(2)]
+    got = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(call())
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, g))
+
+
+def test_lengths_out_of_range_are_clamped_and_flagged():
+    dev = torch.device("cuda", 0)
+    q, k, v, do = _tensors(2, 100, 2, 2, 64, torch.bfloat16, dev, 51)
+    seq = torch.as_tensor(np.asarray([150, -3], np.int32), device=dev)
+    sa.last_device_status()
+    o = sa.fwd_span(q, k, v, seq, 0.1, -1.0)
+    assert sa.last_device_status() == 8
+    fine = torch.as_tensor(np.asarray([100, 0], np.int32), device=dev)
+    assert torch.equal(o, sa.fwd_span(q, k, v, fine, 0.1, -1.0))
+    sa.bwd_span(q, k, v, do, seq, 0.1, -1.0)
+    assert sa.last_device_status() == 8
+
+
+def _by_rule(n, L, causal, prefix, docs, window):
+    out = np.zeros((len(n), L, 2), np.int32)
+    for z, m in enumerate(n):
+        for i in range(m):
+            lo, hi = 0, m
+            if docs is not None:
+                lo = i
+                while lo > 0 and docs[z][lo - 1] == docs[z][i]:
+                    lo -= 1
+                hi = i + 1
+                while hi < m and docs[z][hi] == docs[z][i]:
+                    hi += 1
+            end, start = hi, lo
+            if causal:
+                hi = min(end, i + 1 if prefix is None else max(i + 1, start + max(0, int(prefix[z]))))
+            if window:
+                lo = max(lo, i - window + 1)
+                if not causal:
+                    hi = min(hi, i + window)
+            out[z, i] = (lo, hi) if lo < hi else (0, 0)
+    return out
+
+
+@pytest.mark.parametrize("L", [1, 33, 1024, 1025, 2500])
+def test_mask_spans(dev, L):
+    g = np.random.default_rng(L)
+    n = [L, max(0, L // 3), 0]
+    seq = torch.as_tensor(np.asarray(n, np.int32), device=dev)
+    docs = np.cumsum(g.random((3, L)) < 0.01, axis=1).astype(np.int32) % 2       # ids come back: runs count, not ids
+    dd = torch.as_tensor(docs, device=dev)
+    pre = np.asarray([L // 2, 5, 2 ** 31 - 1], np.int32)
+    pd = torch.as_tensor(pre, device=dev)
+    for causal, prefix, doc, window in [(False, None, None, 0), (True, None, None, 0), (True, pre, None, 0),
+                                        (False, None, docs, 0), (True, None, docs, 0), (True, pre, docs, 0),
+                                        (True, None, docs, 17), (False, None, None, 1), (False, None, docs, 40),
+                                        (True, None, None, 2 ** 31 - 1)]:
+        got = sa.mask_spans(seq, L, causal=causal, prefix=None if prefix is None else pd,
+                            docs=None if doc is None else dd, window=window)
+        assert np.array_equal(got.cpu().numpy(), _by_rule(n, L, causal, prefix, doc, min(window, L)))
