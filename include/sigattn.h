@@ -68,7 +68,8 @@ typedef enum {
     SIGATTN_ERR_CUDA = 6,                 /* a CUDA runtime/driver call failed */
     SIGATTN_ERR_TIMEOUT = 7,              /* device: a bounded wait ran out */
     SIGATTN_ERR_SEQLEN_RANGE = 8,         /* device: a length was outside [0, L] */
-    SIGATTN_ERR_TOO_LARGE = 9             /* a size exceeds a fixed limit (sigattn_fwd_noalloc) */
+    SIGATTN_ERR_TOO_LARGE = 9,            /* a size exceeds a fixed limit (sigattn_fwd_noalloc) */
+    SIGATTN_ERR_PAGE_RANGE = 10           /* device: a page number was outside [0, pages) */
 } sigattn_status;
 
 typedef enum {
@@ -289,6 +290,67 @@ sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix,
                                   int causal, int window, int Z, int L, int32_t *spans,
                                   void *stream);
 
+/* A paged cache of keys and values, and attention against it.
+ *
+ * k_pages, v_pages: [pages][page_size][Hk][D], page_size 16, 32, 64, 128 or 256.
+ * page_table: device int32[Z][max_pages]; place at of sample z is row at %
+ * page_size of page page_table[z][at / page_size].  Entries that no place of a
+ * call reaches may hold anything.  A page number outside [0, pages) is flagged
+ * (SIGATTN_ERR_PAGE_RANGE in the device status word): nothing is written there,
+ * and reading it counts as keys that weigh zero.  Pages may be shared by
+ * samples for reading; writing one place twice in a call leaves either value.
+ *
+ * sigattn_cache_append writes seqlens_new[z] <= L tokens of k, v ([Z][L][Hk][D])
+ * behind the cache_lens[z] places that sample z has, and lens_out[z] =
+ * cache_lens[z] + seqlens_new[z] (device int32[Z]; may be cache_lens itself only
+ * when L = 1).  Keys are rotated on the way, and so are the queries q
+ * ([Z][L][H][D] -> q_out, which may be q; both NULL and H = 0 for none; rows of
+ * padding are written as zeros): token l has position p = prefix_len[0] +
+ * cache_lens[z] + l, and pair i of the first rot entries of each head turns by
+ * p inv_freq[i] (angles in 64 bits),
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * the pairs being entries (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved.
+ * rot: 0 (no rotation) or a multiple of 16 up to D; inv_freq: device
+ * float[rot / 2].  prefix_len: device int32[1] (a shared prefix before the
+ * sample's own places), or NULL for 0.  Places beyond max_pages * page_size are
+ * not written; that, and lengths outside their range, are flagged
+ * (SIGATTN_ERR_SEQLEN_RANGE) and clamped.  No place but the new tokens' is
+ * touched.
+ *
+ * sigattn_fwd_paged: queries q, output o [Z][L][H][D]; seqlens_q[z] <= L of them
+ * are sample z's last tokens, and seqlens_k[z] >= seqlens_q[z] its own tokens in
+ * the cache, theirs included.  Query l, at own place i = seqlens_k - seqlens_q + l,
+ * sees its own places up to i and, with a prefix, all prefix_len[0] places of
+ * the pages prefix_table (device int32[prefix_pages]), which are read once for
+ * the whole batch.  Scores as in sigattn_fwd_span, |i - j| being the distance
+ * between positions (the prefix comes first).  Padded query rows are written as
+ * exact zeros; cache places that no query sees may hold anything, NaN included.
+ * workspace (device, 16-byte aligned, sigattn_fwd_paged_workspace_bytes bytes,
+ * 0 for fp32) is overwritten; calls that may overlap, captured graphs included,
+ * need one each.  Results do not depend on scheduling.  Z is at most
+ * SIGATTN_PAGED_MAX_Z.
+ *
+ * Errors of both: SIGATTN_ERR_INVALID_ARG, _UNSUPPORTED_HEADDIM,
+ * _UNSUPPORTED_DTYPE, _UNSUPPORTED_DEVICE, _MISALIGNED, _TOO_LARGE (2^31 places,
+ * tokens, rows or, over all samples of sigattn_fwd_paged, 64-place tiles), _CUDA.  On error nothing is launched. */
+#define SIGATTN_PAGED_MAX_Z 4096
+sigattn_status sigattn_cache_append(const void *k, const void *v, const void *q, void *q_out,
+                                    void *k_pages, void *v_pages, const int32_t *page_table,
+                                    const int32_t *cache_lens, const int32_t *seqlens_new,
+                                    const int32_t *prefix_len, int32_t *lens_out, int Z, int L,
+                                    int H, int Hk, int D, int pages, int page_size, int max_pages,
+                                    const float *inv_freq, int rot, int interleaved,
+                                    sigattn_dtype dtype, void *stream);
+sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void *v_pages, void *o,
+                                 const int32_t *page_table, const int32_t *seqlens_k,
+                                 const int32_t *seqlens_q, const int32_t *prefix_table,
+                                 const int32_t *prefix_len, int Z, int L, int H, int Hk, int D,
+                                 int pages, int page_size, int max_pages, int prefix_pages,
+                                 float alpha, float bias, const float *bias_z, float cap,
+                                 const float *slopes, void *workspace, size_t workspace_bytes,
+                                 sigattn_dtype dtype, void *stream);
+size_t sigattn_fwd_paged_workspace_bytes(int Z, int L, int H, int Hk, int D, sigattn_dtype dtype);
+
 /* Selects how later bf16 calls in this process evaluate sigma (process-wide,
  * default SIGATTN_SIGMOID_TANH, the pages' form; see sigattn_sigmoid_mode).  Returns
  * SIGATTN_ERR_INVALID_ARG for an unknown mode.
@@ -312,7 +374,8 @@ sigattn_status sigattn_sigmoid_eval(const float *x, float *y, float *dy, int64_t
 
 /* Reads and clears the current device's status word: synchronises `stream`
  * and returns SIGATTN_OK or the first device-side error recorded since the
- * last call (SIGATTN_ERR_TIMEOUT or SIGATTN_ERR_SEQLEN_RANGE). */
+ * last call (SIGATTN_ERR_TIMEOUT, SIGATTN_ERR_SEQLEN_RANGE or
+ * SIGATTN_ERR_PAGE_RANGE). */
 sigattn_status sigattn_last_device_status(void *stream);
 
 /* Bound, in nanoseconds, on every wait inside the bf16 kernels (default

@@ -24,7 +24,8 @@ __all__ = [
     "SigmoidAttention", "bwd_dq", "bwd_dkdv", "last_cuda_error", "fwd_noalloc", "NOALLOC_MAX_Z",
     "fwd_bias", "bwd_bias", "dbias_workspace_bytes", "fwd_rect", "bwd_rect", "fwd_bwd_host",
     "fwd_bwd_host_workspace_bytes", "launch_order", "log_length_bias", "fwd_span", "bwd_span",
-    "bwd_span_workspace_bytes", "mask_spans",
+    "bwd_span_workspace_bytes", "mask_spans", "cache_append", "fwd_paged", "fwd_paged_workspace_bytes",
+    "PAGED_MAX_Z",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,7 +41,7 @@ STATUS_NAMES = {
     0: "SIGATTN_OK", 1: "SIGATTN_ERR_INVALID_ARG", 2: "SIGATTN_ERR_UNSUPPORTED_HEADDIM",
     3: "SIGATTN_ERR_UNSUPPORTED_DTYPE", 4: "SIGATTN_ERR_UNSUPPORTED_DEVICE",
     5: "SIGATTN_ERR_MISALIGNED", 6: "SIGATTN_ERR_CUDA", 7: "SIGATTN_ERR_TIMEOUT",
-    8: "SIGATTN_ERR_SEQLEN_RANGE", 9: "SIGATTN_ERR_TOO_LARGE",
+    8: "SIGATTN_ERR_SEQLEN_RANGE", 9: "SIGATTN_ERR_TOO_LARGE", 10: "SIGATTN_ERR_PAGE_RANGE",
 }
 
 NOALLOC_MAX_Z = 8192   # SIGATTN_NOALLOC_MAX_Z
@@ -55,6 +56,7 @@ EXPORTS = (
     "sigattn_fwd_rect", "sigattn_bwd_rect", "sigattn_fwd_bwd_host",
     "sigattn_fwd_bwd_host_workspace_bytes", "sigattn_launch_order", "sigattn_log_length_bias",
     "sigattn_fwd_span", "sigattn_bwd_span", "sigattn_bwd_span_workspace_bytes", "sigattn_mask_spans",
+    "sigattn_cache_append", "sigattn_fwd_paged", "sigattn_fwd_paged_workspace_bytes",
 )
 
 
@@ -129,8 +131,9 @@ def load_library():
         lib.sigattn_log_length_bias.restype = ci
         lib.sigattn_launch_order.argtypes = [vp, ci, vp]
         lib.sigattn_launch_order.restype = ci
-        from . import span
+        from . import cache, span
         span.register(lib)
+        cache.register(lib)
         _lib = lib
         return lib
 
@@ -506,4 +509,5 @@ def launch_order(work) -> list:
 
 
 from .autograd import SigmoidAttention  # noqa: E402  (needs the functions above)
+from .cache import PAGED_MAX_Z, cache_append, fwd_paged, fwd_paged_workspace_bytes  # noqa: E402
 from .span import bwd_span, bwd_span_workspace_bytes, fwd_span, mask_spans  # noqa: E402

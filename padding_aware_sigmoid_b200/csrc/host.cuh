@@ -157,10 +157,11 @@ struct FuncDevHash {
 inline std::mutex g_attr_mu;
 inline std::unordered_set<FuncDev, FuncDevHash> g_attr_set;
 
+// smem_most: the most dynamic shared memory any call asks of this kernel.
 template <typename... KArgs, typename... Args>
-sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem_most, size_t smem,
                       cudaStream_t stream, Args... args) {
-    if (smem > 48 * 1024) {
+    if (smem_most > 48 * 1024) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return cuda_fail(e);
@@ -168,7 +169,7 @@ sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
         std::lock_guard<std::mutex> lk(g_attr_mu);
         if (g_attr_set.count(key) == 0) {
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem));
+                                     static_cast<int>(smem_most));
             if (e != cudaSuccess) return cuda_fail(e);
             g_attr_set.insert(key);
         }
@@ -181,6 +182,11 @@ sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) return cuda_fail(e);
     return SIGATTN_OK;
+}
+template <typename... KArgs, typename... Args>
+sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                      Args... args) {
+    return launch(kernel, grid, block, smem, smem, stream, args...);
 }
 
 }  // namespace sigattn

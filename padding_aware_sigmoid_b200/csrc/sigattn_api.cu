@@ -600,6 +600,7 @@ const char *sigattn_status_string(sigattn_status s) {
         case SIGATTN_ERR_TIMEOUT: return "SIGATTN_ERR_TIMEOUT";
         case SIGATTN_ERR_SEQLEN_RANGE: return "SIGATTN_ERR_SEQLEN_RANGE";
         case SIGATTN_ERR_TOO_LARGE: return "SIGATTN_ERR_TOO_LARGE";
+        case SIGATTN_ERR_PAGE_RANGE: return "SIGATTN_ERR_PAGE_RANGE";
     }
     return "SIGATTN_UNKNOWN_STATUS";
 }
