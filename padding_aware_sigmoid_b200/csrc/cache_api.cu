@@ -62,22 +62,22 @@ PagedSizes paged_sizes(int Z, int L, int H, int Hk) {
 
 size_t before_bytes(int Z) { return (static_cast<size_t>(Z + 1) * 4 + 255) & ~size_t(255); }
 
-template <int D, int MODE, int SCORE>
+template <int D, int SCORE>
 sigattn_status paged_launch(const PagedParams &p, cudaStream_t st) {
     using Lay = PagedLayout<D>;
-    sigattn_status s = launch(paged_tiles_kernel<D, MODE, SCORE>, dim3(p.blocks), dim3(kPagedThreads),
+    sigattn_status s = launch(paged_tiles_kernel<D, SCORE>, dim3(p.blocks), dim3(kPagedThreads),
                               Lay::bytes(SIGATTN_PAGED_MAX_Z), Lay::bytes(p.Z), st, p);
     if (s != SIGATTN_OK) return s;
     const int64_t rows = static_cast<int64_t>(p.Z) * p.L * p.H;
     return launch(paged_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, p);
 }
-template <int D, int MODE>
+template <int D>
 sigattn_status paged_score(int score, const PagedParams &p, cudaStream_t st) {
     switch (score) {
-        case 0: return paged_launch<D, MODE, 0>(p, st);
-        case kScoreCap: return paged_launch<D, MODE, kScoreCap>(p, st);
-        case kScoreSlope: return paged_launch<D, MODE, kScoreSlope>(p, st);
-        default: return paged_launch<D, MODE, kScoreCap | kScoreSlope>(p, st);
+        case 0: return paged_launch<D, 0>(p, st);
+        case kScoreCap: return paged_launch<D, kScoreCap>(p, st);
+        case kScoreSlope: return paged_launch<D, kScoreSlope>(p, st);
+        default: return paged_launch<D, kScoreCap | kScoreSlope>(p, st);
     }
 }
 
@@ -230,10 +230,7 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
     p.blocks = std::min(kPagedMostBlocks,
                         g_sm_count[dev] * (D == 64 ? PagedLayout<64>::kBlocksPerSm : PagedLayout<128>::kBlocksPerSm));
     const int score = (cap > 0.0f ? kScoreCap : 0) | (slopes != nullptr ? kScoreSlope : 0);
-    const bool tanh = g_sigmoid_mode.load() == kSigmoidTanh;
-    if (D == 64)
-        return tanh ? paged_score<64, kSigmoidTanh>(score, p, st) : paged_score<64, kSigmoidExp>(score, p, st);
-    return tanh ? paged_score<128, kSigmoidTanh>(score, p, st) : paged_score<128, kSigmoidExp>(score, p, st);
+    return D == 64 ? paged_score<64>(score, p, st) : paged_score<128>(score, p, st);
 }
 
 }  // extern "C"

@@ -201,7 +201,7 @@ struct PagedRows {
 
 // Everything a block does with the tiles of one item kind: WM warps along the
 // rows (16 each), 4 / WM along the keys of a tile.
-template <int D, int MODE, int SCORE, int WM>
+template <int D, int SCORE, int WM>
 struct PagedItem {
     static constexpr int WK = 4 / WM, KW = kPagedTile / WK, NK = D / 16;
     uint32_t qf[NK][4];
@@ -229,7 +229,7 @@ struct PagedItem {
             rows.q[i] = p.q + (static_cast<size_t>(tok) * p.H + h) * D;
             rows.pos[i] = static_cast<float>(c.z < 0 ? prefix + at : at);
             rows.limit[i] = c.z < 0 ? prefix : at + 1;
-            cf[i] = make_score<MODE, SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
+            cf[i] = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                             SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         }
 #pragma unroll
@@ -270,7 +270,7 @@ struct PagedItem {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int key = key0 + k16 + 8 * n8 + 2 * (lane & 3);
-                    float2 w = score_p2<MODE, SCORE>(s[n8][2 * i], s[n8][2 * i + 1], cf[i],
+                    float2 w = score_p2<SCORE>(s[n8][2 * i], s[n8][2 * i + 1], cf[i],
                                                      rows.pos[i] - static_cast<float>(key));
                     w.x = key < rows.limit[i] ? w.x : 0.0f;
                     w.y = key + 1 < rows.limit[i] ? w.y : 0.0f;
@@ -370,7 +370,7 @@ __device__ __forceinline__ void paged_load(const PagedParams &p, const PagedCurs
     }
 }
 
-template <int D, int MODE, int SCORE>
+template <int D, int SCORE>
 __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
     paged_tiles_kernel(const PagedParams p) {
     using Lay = PagedLayout<D>;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
     // The tiles of one item, from `now` on; leaves `now` at the next item.
     int64_t t = t0;
     auto run = [&]<int WM>() {
-        PagedItem<D, MODE, SCORE, WM> it;
+        PagedItem<D, SCORE, WM> it;
         const PagedCursor c = now;
         it.begin(p, c, prefix);
         for (;;) {

@@ -78,7 +78,7 @@ template <int D, int MODE, int SCORE>
 __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_s, uint32_t dcol,
                                              uint64_t *s_full, uint32_t s_par, uint64_t *s_free,
                                              uint64_t *dp_full, uint32_t dp_par, uint64_t *ds_ready,
-                                             const ScoreCoef &cf, int row, int key0, int2 span,
+                                             const ScoreCoef &cf, int row, int key0, int2 span, int &pause,
                                              const WaitCtx &wctx) {
     using SG = BwdSigma<D>;
     if (!__all_sync(0xffffffffu, mbar_wait(s_full, s_par, wctx))) return false;
@@ -92,13 +92,8 @@ __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_
     constexpr int kChunks = SG::kCols / 32;
     float2 g[16];
     auto gains = [&](int ch) {
-        const float rel = static_cast<float>(row - first - 32 * ch);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float2 pr;
-            score_pg2<MODE, SCORE>(__uint_as_float(r[32 * ch + 2 * i]), __uint_as_float(r[32 * ch + 2 * i + 1]), cf,
-                                   rel - static_cast<float>(2 * i), pr, g[i]);
-        }
+        uint32_t unused[16];
+        score_chunk<MODE, SCORE, true>(r + 32 * ch, cf, static_cast<float>(row - first - 32 * ch), unused, g, pause);
     };
     gains(0);   // before dP is waited for
     const uint32_t dc = dcol + SG::kCols * w;
@@ -132,7 +127,7 @@ template <int D, int MODE, int SCORE>
 __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_t *s_full, uint64_t *s_free,
                                                uint64_t *dp_full, uint64_t *p_ready, uint64_t *ds_ready,
                                                uint32_t par, const ScoreCoef &cf, int key, int q_first,
-                                               bool whole, const int2 *clean, const WaitCtx &wctx) {
+                                               bool whole, const int2 *clean, int &pause, const WaitCtx &wctx) {
     using SG = BwdSigma<D>;
     constexpr int W = SG::kPacked / 16;   // words of 32 columns
     float2 g[SG::kPacked];
@@ -162,12 +157,9 @@ __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_
         mbar_arrive(s_free);
         const float rel = static_cast<float>(key - q_first);
 #pragma unroll
-        for (int ii = 0; ii < SG::kPacked; ++ii) {
-            float2 pr;
-            score_pg2<MODE, SCORE>(__uint_as_float(r[2 * ii]), __uint_as_float(r[2 * ii + 1]), cf,
-                                   rel - static_cast<float>(2 * ii), pr, g[ii]);
-            pk[ii] = pack_bf16x2(pr.x, pr.y);
-        }
+        for (int u = 0; u < W; ++u)
+            score_chunk<MODE, SCORE, true>(r + 32 * u, cf, rel - static_cast<float>(32 * u), pk + 16 * u, g + 16 * u,
+                                           pause);
     }
     auto keep = [&](uint32_t (&x)[SG::kPacked]) {
 #pragma unroll
@@ -401,13 +393,14 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         const int2 span = row_span(p.src, z, row, n);
         __nv_bfloat16 *drow = p.dq + (static_cast<size_t>(z) * L + row) * (static_cast<size_t>(p.H) * D) +
                               static_cast<size_t>(h) * D;
-        const ScoreCoef cf = make_score<MODE, SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
+        const ScoreCoef cf = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                                      SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         bool ok = true;
+        int pause = tail_pause(cf);
         for (int r = 0; r < steps; ++r) {
             ok = span_dq_tile<D, MODE, SCORE>(tmem + lane_bits, w, kColS, r & 1 ? kColDP1 : kColDP0, s_full, r & 1,
                                               s_free, &dp_full[r & 1], (r >> 1) & 1, &ds_ready[r & 1], cf, row,
-                                              (J0 + r) * 128, span, wctx);
+                                              (J0 + r) * 128, span, pause, wctx);
             if (!ok) break;
         }
         // every MMA of this CTA has finished once the MMA warp's final commit lands
@@ -653,19 +646,21 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         const uint32_t tD = tmem + lane_bits + Lay::COL_DP + SG::kCols * w;
         const float bias = bias_of(p.bias_z, p.bias, z);
         int i = I0, h = kvh * p.group;
-        ScoreCoef cf = make_score<MODE, SCORE>(p.alpha, bias, p.cap, SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
+        ScoreCoef cf = make_score<SCORE>(p.alpha, bias, p.cap, SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         bool ok = true;
+        int pause = tail_pause(cf);
         for (int r = 0; r < steps; ++r) {
             const int4 t = __ldg(hull + i);
             const bool whole = t.z <= k0 && t.w >= k1;
             ok = span_dkdv_tile<D, MODE, SCORE>(tS, tD, s_full, s_free, dp_full, p_ready, ds_ready, r & 1, cf, key,
-                                                i * 128 + SG::kCols * w, whole, clean + i * 128, wctx);
+                                                i * 128 + SG::kCols * w, whole, clean + i * 128, pause,
+                                                wctx);
             if (!ok) break;
             if (++i > I1) {
                 i = I0;
                 ++h;
                 if (SCORE & kScoreSlope && r + 1 < steps)
-                    cf = make_score<MODE, SCORE>(p.alpha, bias, p.cap, p.slopes[h]);
+                    cf = make_score<SCORE>(p.alpha, bias, p.cap, p.slopes[h]);
             }
         }
         // every MMA of this CTA has finished once the MMA warp's final commit lands

@@ -272,9 +272,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int ja = t ? j0[1] : j0[0], jb = t ? j1[1] : j1[0];
         bool ok = true;
         if (jb > 0) {
-            const ScoreCoef cf = make_score<MODE, SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
+            const ScoreCoef cf = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                                          SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
             const uint32_t tS = tmem + lane_bits + (t ? Lay::COL_S1 : Lay::COL_S0) + 64 * c;
+            int pause = tail_pause(cf);
             for (int j = ja; j < jb; ++j) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (j - ja) & 1, wctx));
                 if (!ok) break;
@@ -289,13 +290,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     tmem_ld32(tS + 32 * u, r);
                     uint32_t pk[16];
                     const float rel = static_cast<float>(row - key0 - 32 * u);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 pr = score_p2<MODE, SCORE>(__uint_as_float(r[2 * i]),
-                                                                __uint_as_float(r[2 * i + 1]), cf,
-                                                                rel - static_cast<float>(2 * i));
-                        pk[i] = pack_bf16x2(pr.x, pr.y);
-                    }
+                    score_chunk<MODE, SCORE, false>(r, cf, rel, pk, nullptr, pause);
                     if (!whole)
                         keep_bits(pk, bit_range(span.x - key0 - 32 * u, span.y - key0 - 32 * u));
                     tmem_st16(tS + 16 * u, pk);
