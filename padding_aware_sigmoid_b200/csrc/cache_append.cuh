@@ -84,151 +84,159 @@ struct AppendVec<float> {
 
 // TOK tokens a block.  A head row is D / N vectors of 16 bytes, handled in
 // D / 2N units of two vectors each: with half-split pairs a unit of the rotated
-// part is (vector u, vector u + rot / 2N), otherwise two neighbours.
+// part is (vector u, vector u + rot / 2N), otherwise two neighbours.  Every
+// thread reads its first UNR units before anything else is known about the
+// tokens (padded rows are there to be read, too), so the loads cover the
+// lookups and the angles.
 template <typename T, int D, int TOK>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
     using Vec = AppendVec<T>;
     constexpr int N = Vec::N, VECS = D / N, UNITS = VECS / 2;
+    constexpr int UNR = 3;
     __shared__ float2 turn[TOK][kAppendPairs];
     __shared__ int64_t dest[TOK];      // cache row (page * page_size + slot) times Hk, or < 0
     __shared__ int live[TOK];          // 1: a token of its sample, 0: padding
     __shared__ int after[TOK];         // its sample's new length, < 0: written by another token
     const int64_t tokens = static_cast<int64_t>(p.Z) * p.L;
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * TOK;
+    const int here = static_cast<int>(min(static_cast<int64_t>(TOK), tokens - tok0));
     const int capacity = p.max_pages << p.page_shift;     // checked on the host to fit
     const int tid = threadIdx.x;
-
-    // where each token goes
-    if (tid < TOK) {
-        const int64_t tok = tok0 + tid;
-        int ok = 0, sum = -1;
-        int64_t to = -1;
-        if (tok < tokens) {
-            const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
-            int have = p.cache_lens[z], add = p.seqlens_new[z];
-            if (have < 0 || have > capacity || add < 0 || add > p.L || add > capacity - have) {
-                record_status(p.status, kStatusSeqlenRange);
-                have = min(max(have, 0), capacity);
-                add = min(max(add, 0), p.L);
-            }
-            ok = l < add;
-            if (l == 0) sum = min(have + min(add, capacity - have), capacity);
-            const int64_t at = static_cast<int64_t>(have) + l;
-            if (ok && at < capacity) {
-                const int page = p.page_table[static_cast<size_t>(z) * p.max_pages + (at >> p.page_shift)];
-                if (page < 0 || page >= p.pages)
-                    record_status(p.status, kStatusPageRange);
-                else
-                    to = ((static_cast<int64_t>(page) << p.page_shift) + (at & ((1 << p.page_shift) - 1))) * p.Hk;
-            }
-        }
-        after[tid] = sum;
-        live[tid] = ok;
-        dest[tid] = to;
-    }
-    // the tokens' angles
     const int pairs = p.rot / 2;
-    const int base = p.prefix_len != nullptr ? max(*p.prefix_len, 0) : 0;
-    for (int e = tid; e < TOK * pairs; e += kAppendThreads) {
-        const int t = e / pairs, i = e % pairs;
-        const int64_t tok = tok0 + t;
-        if (tok < tokens) {
-            const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
-            const int have = min(max(p.cache_lens[z], 0), capacity);
-            if (l < p.seqlens_new[z])
-                turn[t][i] = position_angle(static_cast<double>(base) + have + l, p.inv_freq[i]);
-        }
-    }
-    __syncthreads();
-    // not before the barrier: with single tokens lens_out may be cache_lens
-    if (tid < TOK && after[tid] >= 0) p.lens_out[(tok0 + tid) / p.L] = after[tid];
-
     const int heads = p.H + 2 * p.Hk;       // queries, keys, values
-    const int per_token = heads * UNITS;
+    const int per_token = heads * UNITS, all = here * per_token;
     const int half_units = pairs / N;       // rotated units with half-split pairs
     const uint4 *q = static_cast<const uint4 *>(p.q), *k = static_cast<const uint4 *>(p.k),
                 *v = static_cast<const uint4 *>(p.v);
-    constexpr int U = 4;                    // units in flight per thread
-    for (int e0 = tid; e0 < TOK * per_token; e0 += U * kAppendThreads) {
-        uint4 a[U], b[U];
-        const uint4 *from[U];
-        uint4 *to[U];
-        int va[U], vb[U], tk[U], pair0[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int e = e0 + u * kAppendThreads;
-            from[u] = nullptr;
-            to[u] = nullptr;
-            if (e >= TOK * per_token) continue;
-            const int t = e / per_token, w = e % per_token;
-            const int head = w / UNITS, un = w % UNITS;
-            const int64_t tok = tok0 + t;
-            if (tok >= tokens) continue;
-            tk[u] = t;
-            pair0[u] = -1;
-            if (p.interleaved || un >= half_units) {
-                // two neighbouring vectors
-                va[u] = p.interleaved ? 2 * un : 2 * half_units + 2 * (un - half_units);
-                vb[u] = va[u] + 1;
-                if (p.interleaved && va[u] * N < p.rot) pair0[u] = va[u] * N / 2;
-            } else {
-                va[u] = un;
-                vb[u] = un + half_units;
-                pair0[u] = un * N;
-            }
-            if (head < p.H) {
-                const size_t row = (static_cast<size_t>(tok) * p.H + head) * VECS;
-                to[u] = static_cast<uint4 *>(p.q_out) + row;
-                if (live[t]) from[u] = q + row;
-            } else if (live[t] && dest[t] >= 0) {
-                const bool key = head < p.H + p.Hk;
-                const int hk = head - p.H - (key ? 0 : p.Hk);
-                from[u] = (key ? k : v) + (static_cast<size_t>(tok) * p.Hk + hk) * VECS;
-                to[u] = static_cast<uint4 *>(key ? p.k_pages : p.v_pages) + (static_cast<size_t>(dest[t]) + hk) * VECS;
-                if (!key) pair0[u] = -1;
-            }
-            if (from[u] != nullptr) {
-                a[u] = from[u][va[u]];
-                b[u] = from[u][vb[u]];
-            }
+
+    // one unit: its token and head, its vectors, its first pair (-1: not rotated)
+    struct Unit {
+        int t, head, va, vb, pair;
+    };
+    auto unit_of = [&](int e) {
+        Unit u;
+        u.t = TOK == 1 ? 0 : e / per_token;
+        const int w = e - u.t * per_token, un = w % UNITS;
+        u.head = w / UNITS;
+        u.pair = -1;
+        if (p.interleaved || un >= half_units) {
+            u.va = p.interleaved ? 2 * un : 2 * half_units + 2 * (un - half_units);
+            u.vb = u.va + 1;
+            if (p.interleaved && u.va * N < p.rot) u.pair = u.va * N / 2;
+        } else {
+            u.va = un;
+            u.vb = un + half_units;
+            u.pair = un * N;
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (to[u] == nullptr) continue;
-            if (from[u] == nullptr) {          // a padded query row
-                to[u][va[u]] = to[u][vb[u]] = make_uint4(0u, 0u, 0u, 0u);
-                continue;
+        if (u.head >= p.H + p.Hk) u.pair = -1;    // a value
+        return u;
+    };
+    auto load = [&](const Unit &u, uint4 &a, uint4 &b) {
+        const size_t tok = static_cast<size_t>(tok0 + u.t);
+        const uint4 *row = u.head < p.H ? q + (tok * p.H + u.head) * VECS
+                           : u.head < p.H + p.Hk ? k + (tok * p.Hk + (u.head - p.H)) * VECS
+                                                 : v + (tok * p.Hk + (u.head - p.H - p.Hk)) * VECS;
+        a = __ldg(row + u.va);
+        b = __ldg(row + u.vb);
+    };
+    auto finish = [&](const Unit &u, uint4 a, uint4 b) {
+        uint4 *to;
+        if (u.head < p.H) {
+            to = static_cast<uint4 *>(p.q_out) + (static_cast<size_t>(tok0 + u.t) * p.H + u.head) * VECS;
+            if (!live[u.t]) {      // a padded query row
+                to[u.va] = to[u.vb] = make_uint4(0u, 0u, 0u, 0u);
+                return;
             }
-            if (pair0[u] >= 0) {
-                float x[N], y[N];
-                Vec::open(a[u], x);
-                Vec::open(b[u], y);
-                const float2 *cs = &turn[tk[u]][pair0[u]];
-                if (p.interleaved) {
+        } else {
+            if (dest[u.t] < 0) return;
+            const bool key = u.head < p.H + p.Hk;
+            to = static_cast<uint4 *>(key ? p.k_pages : p.v_pages) +
+                 (static_cast<size_t>(dest[u.t]) + u.head - p.H - (key ? 0 : p.Hk)) * VECS;
+        }
+        if (u.pair >= 0) {
+            float x[N], y[N];
+            Vec::open(a, x);
+            Vec::open(b, y);
+            const float2 *cs = &turn[u.t][u.pair];
+            if (p.interleaved) {
 #pragma unroll
-                    for (int i = 0; i < N; i += 2) {
-                        const float2 c = cs[i / 2], d = cs[N / 2 + i / 2];
-                        const float x0 = x[i], y0 = y[i];
-                        x[i] = x0 * c.x - x[i + 1] * c.y;
-                        x[i + 1] = x[i + 1] * c.x + x0 * c.y;
-                        y[i] = y0 * d.x - y[i + 1] * d.y;
-                        y[i + 1] = y[i + 1] * d.x + y0 * d.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const float2 c = cs[i];
-                        const float x0 = x[i];
-                        x[i] = x0 * c.x - y[i] * c.y;
-                        y[i] = y[i] * c.x + x0 * c.y;
-                    }
+                for (int i = 0; i < N; i += 2) {
+                    const float2 c = cs[i / 2], d = cs[N / 2 + i / 2];
+                    const float x0 = x[i], y0 = y[i];
+                    x[i] = x0 * c.x - x[i + 1] * c.y;
+                    x[i + 1] = x[i + 1] * c.x + x0 * c.y;
+                    y[i] = y0 * d.x - y[i + 1] * d.y;
+                    y[i + 1] = y[i + 1] * d.x + y0 * d.y;
                 }
-                a[u] = Vec::close(x);
-                b[u] = Vec::close(y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float2 c = cs[i];
+                    const float x0 = x[i];
+                    x[i] = x0 * c.x - y[i] * c.y;
+                    y[i] = y[i] * c.x + x0 * c.y;
+                }
             }
-            to[u][va[u]] = a[u];
-            to[u][vb[u]] = b[u];
+            a = Vec::close(x);
+            b = Vec::close(y);
         }
+        to[u.va] = a;
+        to[u.vb] = b;
+    };
+
+    uint4 a[UNR], b[UNR];
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+        const int e = tid + u * kAppendThreads;
+        if (e < all) load(unit_of(e), a[u], b[u]);
+    }
+
+    // where each token goes, by the last warp
+    if (tid >= kAppendThreads - 32 && tid - (kAppendThreads - 32) < here) {
+        const int t = tid - (kAppendThreads - 32);
+        const int64_t tok = tok0 + t;
+        const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
+        int have = p.cache_lens[z], add = p.seqlens_new[z];
+        if (have < 0 || have > capacity || add < 0 || add > p.L || add > capacity - have) {
+            record_status(p.status, kStatusSeqlenRange);
+            have = min(max(have, 0), capacity);
+            add = min(max(add, 0), p.L);
+        }
+        after[t] = l == 0 ? min(have + min(add, capacity - have), capacity) : -1;
+        live[t] = l < add;
+        const int64_t at = static_cast<int64_t>(have) + l;
+        int64_t to = -1;
+        if (l < add && at < capacity) {
+            const int page = p.page_table[static_cast<size_t>(z) * p.max_pages + (at >> p.page_shift)];
+            if (page < 0 || page >= p.pages)
+                record_status(p.status, kStatusPageRange);
+            else
+                to = ((static_cast<int64_t>(page) << p.page_shift) + (at & ((1 << p.page_shift) - 1))) * p.Hk;
+        }
+        dest[t] = to;
+    }
+    // the tokens' angles
+    const int base = p.prefix_len != nullptr ? max(*p.prefix_len, 0) : 0;
+    for (int e = tid; e < here * pairs; e += kAppendThreads) {
+        const int t = TOK == 1 ? 0 : e / pairs, i = e - t * pairs;
+        const int64_t tok = tok0 + t;
+        const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
+        const int have = min(max(p.cache_lens[z], 0), capacity);
+        if (l < p.seqlens_new[z]) turn[t][i] = position_angle(static_cast<double>(base) + have + l, p.inv_freq[i]);
+    }
+    __syncthreads();
+    // not before the barrier: with single tokens lens_out may be cache_lens
+    if (tid < here && after[tid] >= 0) p.lens_out[(tok0 + tid) / p.L] = after[tid];
+
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+        const int e = tid + u * kAppendThreads;
+        if (e < all) finish(unit_of(e), a[u], b[u]);
+    }
+    for (int e = tid + UNR * kAppendThreads; e < all; e += kAppendThreads) {
+        const Unit un = unit_of(e);
+        load(un, a[0], b[0]);
+        finish(un, a[0], b[0]);
     }
 }
 

@@ -9,6 +9,14 @@ namespace sigattn {
 
 constexpr int kPagedF32Warps = 8;
 
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
 // The shapes, tables and lengths of `p` are those of the bf16 path; its
 // tensors are not used.
 template <int D>

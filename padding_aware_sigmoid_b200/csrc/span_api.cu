@@ -36,7 +36,7 @@ sigattn_status check_span(const SpanArgs &a, bool *empty) {
     if (a.seqlens == nullptr) return SIGATTN_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(a.spans) & 7u) != 0) return SIGATTN_ERR_MISALIGNED;
     // one warp per row: 8 rows a block
-    if (a.dtype == SIGATTN_FP32 && static_cast<int64_t>(a.Z) * a.L * a.H > (int64_t(INT_MAX) - 8) * 8)
+    if (a.dtype == SIGATTN_FP32 && static_cast<int64_t>(a.Z) * a.L * (a.H + a.Hk) > (int64_t(INT_MAX) - 8) * 8)
         return SIGATTN_ERR_TOO_LARGE;
     return SIGATTN_OK;
 }
@@ -170,8 +170,8 @@ sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, voi
         p.v = static_cast<const float *>(v);
         p.o = static_cast<float *>(o);
         const dim3 grid = f32_grid(static_cast<int64_t>(Z) * L * H);
-        return D == 64 ? launch(span_f32_rows_kernel<64, false>, grid, dim3(256), 0, st, p)
-                       : launch(span_f32_rows_kernel<128, false>, grid, dim3(256), 0, st, p);
+        return D == 64 ? launch(span_f32_fwd_kernel<64>, grid, dim3(256), 0, st, p)
+                       : launch(span_f32_fwd_kernel<128>, grid, dim3(256), 0, st, p);
     }
     CUtensorMap mq, mk, mv;
     if ((s = encode_bf16_map_uncached(&mq, q, Z, L, H, D)) != SIGATTN_OK) return s;
@@ -226,11 +226,8 @@ sigattn_status sigattn_bwd_span(const void *q, const void *k, const void *v, con
         p.dk = static_cast<float *>(dk);
         p.dv = static_cast<float *>(dv);
         const dim3 gq = f32_grid(static_cast<int64_t>(Z) * L * H), gk = f32_grid(static_cast<int64_t>(Z) * L * Hk);
-        s = D == 64 ? launch(span_f32_rows_kernel<64, true>, gq, dim3(256), 0, st, p)
-                    : launch(span_f32_rows_kernel<128, true>, gq, dim3(256), 0, st, p);
-        if (s != SIGATTN_OK) return s;
-        return D == 64 ? launch(span_f32_dkdv_kernel<64>, gk, dim3(256), 0, st, p)
-                       : launch(span_f32_dkdv_kernel<128>, gk, dim3(256), 0, st, p);
+        return D == 64 ? launch(span_f32_bwd_kernel<64>, dim3(gq.x + gk.x), dim3(256), 0, st, p, gq.x)
+                       : launch(span_f32_bwd_kernel<128>, dim3(gq.x + gk.x), dim3(256), 0, st, p, gq.x);
     }
     CUtensorMap mq, mk, mv, mdo;
     if ((s = encode_bf16_map_uncached(&mq, q, Z, L, H, D)) != SIGATTN_OK) return s;
