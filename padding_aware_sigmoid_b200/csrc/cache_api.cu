@@ -43,11 +43,18 @@ sigattn_status check_cache(const CacheShape &c, bool queries, bool *empty) {
 // Row warps (1, 2 or 4, 16 rows each) of a tile over `rows` query rows.
 int row_warps(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
-constexpr int kPagedMostBlocks = 1024;    // more than any device's grid
+constexpr int kPagedMostSms = 256;                   // more than any device has
+constexpr int kPagedMostBlocks = 3 * kPagedMostSms;  // of the tile kernel
+
+// Rows (over the batch, per key head) from which the prefix kernel takes the
+// prefix.
+constexpr int64_t kPrefixKernelRows = 32;
 
 struct PagedSizes {
     int prefix_warps, own_warps, part_rows;
     int64_t items;
+    int tile_tokens;      // tokens of a row tile of the prefix kernel; 0: it does not run
+    int64_t pairs;        // its pairs of row tiles
 };
 PagedSizes paged_sizes(int Z, int L, int H, int Hk) {
     PagedSizes s;
@@ -57,27 +64,77 @@ PagedSizes paged_sizes(int Z, int L, int H, int Hk) {
     s.part_rows = 16 * std::max(s.prefix_warps, s.own_warps);
     s.items = Hk * ((all + 16 * s.prefix_warps - 1) / (16 * s.prefix_warps) +
                     Z * ((own + 16 * s.own_warps - 1) / (16 * s.own_warps)));
+    s.tile_tokens = 0;
+    s.pairs = 0;
+    if (H / Hk <= 128 && all > kPrefixKernelRows) {
+        s.tile_tokens = 128 / (H / Hk);
+        s.pairs = (static_cast<int64_t>(Z) * L + 2 * s.tile_tokens - 1) / (2 * s.tile_tokens);
+    }
     return s;
 }
 
+size_t part_bytes(const PagedSizes &s, int D) {
+    return static_cast<size_t>(kPagedMostBlocks + s.items) * s.part_rows * D * sizeof(float);
+}
+// the splits are chosen so that all blocks of the prefix kernel fit the SMs once
+size_t prefix_part_bytes(const PagedSizes &s, int Hk, int D) {
+    return s.pairs == 0 ? 0 : (kPagedMostSms + static_cast<size_t>(s.pairs) * Hk) * 256 * D * sizeof(float);
+}
 size_t before_bytes(int Z) { return (static_cast<size_t>(Z + 1) * 4 + 255) & ~size_t(255); }
 
+// A bf16 tensor of four dimensions (innermost first, 128-byte swizzle).
+sigattn_status encode_box(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                          const cuuint32_t (&box)[4]) {
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, one,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        g_last_cuda_error.store(10000 + static_cast<int>(r));
+        return SIGATTN_ERR_CUDA;
+    }
+    return SIGATTN_OK;
+}
+// Pages [pages][page_size][Hk][D] in boxes of 64 entries of one head of `rows` places.
+sigattn_status encode_pages(CUtensorMap *m, const void *base, const CacheShape &c, int rows) {
+    const cuuint64_t D = c.D, Hk = c.Hk, page = c.page_size;
+    return encode_box(m, base, {D, Hk, page, static_cast<cuuint64_t>(c.pages)}, {D * 2, Hk * D * 2, page * Hk * D * 2},
+                      {64, 1, static_cast<cuuint32_t>(rows), 1});
+}
+
+struct PagedMaps {
+    CUtensorMap k, v;                        // boxes of the tile kernel
+    CUtensorMap prefix_q, prefix_k, prefix_v;
+};
+
+template <int D, int MODE, int SCORE>
+sigattn_status prefix_launch(const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
+    constexpr int KS = FwdStages<D>::K, VS = FwdStages<D>::V;
+    return launch(paged_prefix_kernel<D, MODE, SCORE>, dim3(p.splits, p.pairs, p.Hk), dim3(kFwdThreads),
+                  FwdLayout<D, KS, VS>::SMEM_ALLOC, st, m.prefix_q, m.prefix_k, m.prefix_v, p);
+}
 template <int D, int SCORE>
-sigattn_status paged_launch(const PagedParams &p, cudaStream_t st) {
+sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
     using Lay = PagedLayout<D>;
-    sigattn_status s = launch(paged_tiles_kernel<D, SCORE>, dim3(p.blocks), dim3(kPagedThreads),
-                              Lay::bytes(SIGATTN_PAGED_MAX_Z), Lay::bytes(p.Z), st, p);
+    sigattn_status s = SIGATTN_OK;
+    if (p.splits > 0) {
+        s = g_sigmoid_mode.load() == kSigmoidTanh ? prefix_launch<D, kSigmoidTanh, SCORE>(m, p, st)
+                                                  : prefix_launch<D, kSigmoidExp, SCORE>(m, p, st);
+        if (s != SIGATTN_OK) return s;
+    }
+    s = launch(paged_tiles_kernel<D, SCORE>, dim3(p.blocks), dim3(kPagedThreads), Lay::bytes(SIGATTN_PAGED_MAX_Z),
+               Lay::bytes(p.Z), st, m.k, m.v, p);
     if (s != SIGATTN_OK) return s;
     const int64_t rows = static_cast<int64_t>(p.Z) * p.L * p.H;
     return launch(paged_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, p);
 }
 template <int D>
-sigattn_status paged_score(int score, const PagedParams &p, cudaStream_t st) {
+sigattn_status paged_score(int score, const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
     switch (score) {
-        case 0: return paged_launch<D, 0>(p, st);
-        case kScoreCap: return paged_launch<D, kScoreCap>(p, st);
-        case kScoreSlope: return paged_launch<D, kScoreSlope>(p, st);
-        default: return paged_launch<D, kScoreCap | kScoreSlope>(p, st);
+        case 0: return paged_launch<D, 0>(m, p, st);
+        case kScoreCap: return paged_launch<D, kScoreCap>(m, p, st);
+        case kScoreSlope: return paged_launch<D, kScoreSlope>(m, p, st);
+        default: return paged_launch<D, kScoreCap | kScoreSlope>(m, p, st);
     }
 }
 
@@ -153,7 +210,7 @@ size_t sigattn_fwd_paged_workspace_bytes(int Z, int L, int H, int Hk, int D, sig
     if (Z <= 0 || L <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || (D != 64 && D != 128) || dtype != SIGATTN_BF16)
         return 0;
     const PagedSizes s = paged_sizes(Z, L, H, Hk);
-    return before_bytes(Z) + static_cast<size_t>(kPagedMostBlocks + s.items) * s.part_rows * D * sizeof(float);
+    return before_bytes(Z) + part_bytes(s, D) + prefix_part_bytes(s, Hk, D);
 }
 
 sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void *v_pages, void *o,
@@ -170,8 +227,9 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
         return SIGATTN_ERR_INVALID_ARG;
     if (empty) return SIGATTN_OK;
     if (Z > SIGATTN_PAGED_MAX_Z) return SIGATTN_ERR_TOO_LARGE;
+    if (pages == 0) return SIGATTN_ERR_INVALID_ARG;
     for (const void *t : {q, k_pages, v_pages, static_cast<const void *>(o)}) {
-        if (t == nullptr && !(pages == 0 && t != q && t != o)) return SIGATTN_ERR_INVALID_ARG;
+        if (t == nullptr) return SIGATTN_ERR_INVALID_ARG;
         if (!aligned16(t)) return SIGATTN_ERR_MISALIGNED;
     }
     if ((page_table == nullptr && max_pages > 0) || seqlens_k == nullptr || seqlens_q == nullptr)
@@ -187,11 +245,9 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
     if ((s = device_state(&dev, &cc, &status)) != SIGATTN_OK) return s;
     if (dtype == SIGATTN_BF16 && cc != 100) return SIGATTN_ERR_UNSUPPORTED_DEVICE;
     const PagedSizes z = paged_sizes(Z, L, H, Hk);
-    if (z.items > INT_MAX - 2 * kPagedMostBlocks) return SIGATTN_ERR_TOO_LARGE;
+    if (z.items > INT_MAX - 2 * kPagedMostBlocks || z.pairs > 65535 || Hk > 65535) return SIGATTN_ERR_TOO_LARGE;
     PagedParams p = {};
     p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k_pages = static_cast<const __nv_bfloat16 *>(k_pages);
-    p.v_pages = static_cast<const __nv_bfloat16 *>(v_pages);
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.page_table = page_table;
     p.seqlens_k = seqlens_k;
@@ -222,15 +278,35 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
         return D == 64 ? launch(paged_f32_kernel<64>, grid, block, 0, st, p, fq, fk, fv, fo)
                        : launch(paged_f32_kernel<128>, grid, block, 0, st, p, fq, fk, fv, fo);
     }
-    p.before = static_cast<int *>(workspace);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + before_bytes(Z));
+    if ((s = get_encoder()) != SIGATTN_OK) return s;
+    char *ws = static_cast<char *>(workspace);
+    p.before = reinterpret_cast<int *>(ws);
+    p.part = reinterpret_cast<float *>(ws + before_bytes(Z));
     p.prefix_warps = z.prefix_warps;
     p.own_warps = z.own_warps;
     p.part_rows = z.part_rows;
-    p.blocks = std::min(kPagedMostBlocks,
-                        g_sm_count[dev] * (D == 64 ? PagedLayout<64>::kBlocksPerSm : PagedLayout<128>::kBlocksPerSm));
+    const int sms = std::min(g_sm_count[dev], kPagedMostSms);
+    p.blocks = sms * (D == 64 ? PagedLayout<64>::kBlocksPerSm : PagedLayout<128>::kBlocksPerSm);
+    p.timeout_ns = g_timeout_ns.load();
+    PagedMaps m;
+    const int own_box = std::min(page_size, kPagedTile);
+    if ((s = encode_pages(&m.k, k_pages, c, own_box)) != SIGATTN_OK) return s;
+    if ((s = encode_pages(&m.v, v_pages, c, own_box)) != SIGATTN_OK) return s;
+    if (z.tile_tokens > 0 && prefix_len != nullptr && prefix_pages > 0) {
+        p.prefix_part = reinterpret_cast<float *>(ws + before_bytes(Z) + part_bytes(z, D));
+        p.tile_tokens = z.tile_tokens;
+        p.pairs = static_cast<int>(z.pairs);
+        p.splits = static_cast<int>(std::max<int64_t>(1, sms / (z.pairs * Hk)));
+        const int box = std::min(page_size, 128);
+        if ((s = encode_pages(&m.prefix_k, k_pages, c, box)) != SIGATTN_OK) return s;
+        if ((s = encode_pages(&m.prefix_v, v_pages, c, box)) != SIGATTN_OK) return s;
+        const cuuint64_t d = D, group = H / Hk, heads = Hk, tokens = static_cast<cuuint64_t>(Z) * L;
+        if ((s = encode_box(&m.prefix_q, q, {d, group, heads, tokens}, {d * 2, group * d * 2, group * heads * d * 2},
+                            {64, static_cast<cuuint32_t>(group), 1, static_cast<cuuint32_t>(z.tile_tokens)})) != SIGATTN_OK)
+            return s;
+    }
     const int score = (cap > 0.0f ? kScoreCap : 0) | (slopes != nullptr ? kScoreSlope : 0);
-    return D == 64 ? paged_score<64>(score, p, st) : paged_score<128>(score, p, st);
+    return D == 64 ? paged_score<64>(score, m, p, st) : paged_score<128>(score, m, p, st);
 }
 
 }  // extern "C"

@@ -10,31 +10,39 @@
 // an own part, and each of them of the parts of any split of the keys: no running
 // maximum, no rescaling, nothing but fp32 partial sums to add at the end.
 //
-// Work is a list of items, each a run of 64-key tiles:
-//   prefix items: (key head, tile of query rows), the rows being those of all
-//                 samples' tokens and of all query heads of the key head, so that
-//                 the prefix is read once per row tile and not once per sample;
-//   own items:    (sample, key head, tile of its query rows).
-// The tiles of all items form one sequence that is cut evenly over the grid
-// (block b of B <= T takes [b T / B, (b + 1) T / B)), whatever the lengths: a block walks its
-// range, keeps kStages tiles in flight with cp.async across item borders, and
-// writes one fp32 partial per item it touches.  Walking on either starts a new
-// block or a new item, so (block + item) numbers the partials without a table.
-// paged_join_kernel adds the partials of each row in that order (the result
-// does not depend on scheduling) and rounds once.
+// Two kernels compute, one adds up:
+//
+//  paged_prefix_kernel (tcgen05): the prefix against the rows of all samples'
+//    tokens and of all query heads of a key head, 256 rows a block, so that the
+//    prefix is read once per 256 rows and not once per sample.  The key range is
+//    split over blocks until they fill the device.
+//  paged_tiles_kernel (mma.sync): the samples' own keys, and the prefix where the
+//    batch has few rows.  Work is a list of items, each a run of 64-key tiles:
+//      prefix items: (key head, tile of the rows above);
+//      own items:    (sample, key head, tile of its query rows).
+//    The tiles of all items form one sequence that is cut evenly over the grid
+//    (block b of B <= T takes [b T / B, (b + 1) T / B)), whatever the lengths; a
+//    producer warp walks a block's range with TMA, across item borders, and the
+//    consumer warps write one fp32 partial per item that they touch.  Walking on
+//    either starts a new block or a new item, so (block + item) numbers the
+//    partials without a table.
+//  paged_join_kernel adds the partials of each row in a fixed order (the result
+//    does not depend on scheduling) and rounds once.
 //
 // Bound: memory.  Every key and value is read once per row tile; a 64-key tile
-// at D = 128 is 32 KB, 1.4 kclk of an SM's share of HBM, against 1.0 kclk of
-// mma.sync for a full 64-row tile and far less for the few rows of one sample.
+// at D = 128 is 32 KB, 1.4 kclk of an SM's share of HBM.  The few rows of one
+// sample leave a tcgen05 tile of 128 rows mostly empty and its sigma warps with
+// 128 rows of work; mma.sync works on 16 rows at a time.  Many rows turn that
+// round (64 rows of mma.sync take 3 kclk a tile), hence the two kernels.
 #pragma once
 
 #include "cache_append.cuh"
-#include "span_score.cuh"
+#include "span_fwd_sm100.cuh"
 
 namespace sigattn {
 
 struct PagedParams {
-    const __nv_bfloat16 *q, *k_pages, *v_pages;
+    const __nv_bfloat16 *q;
     __nv_bfloat16 *o;
     const int *page_table, *seqlens_k, *seqlens_q, *prefix_table, *prefix_len;
     int Z, L, H, Hk, group;
@@ -46,21 +54,31 @@ struct PagedParams {
     int prefix_warps, own_warps;   // warps along the rows (1, 2, 4): row tiles of 16 times that
     int part_rows;        // rows of one partial: the larger row tile
     int blocks;           // grid of the tile kernel
+    // the prefix kernel, when it runs (splits > 0; the tile kernel then leaves the prefix out)
+    float *prefix_part;   // [split][key head][pair][256][D]
+    int splits, pairs;    // blocks along the keys; pairs of row tiles
+    int tile_tokens;      // tokens of a row tile: 128 / group
     int *status;
+    uint64_t timeout_ns;
 };
 
-constexpr int kPagedThreads = 128;
+constexpr int kPagedConsumers = 128;
+constexpr int kPagedThreads = kPagedConsumers + 32;
 constexpr int kPagedTile = 64;    // keys per tile
 
 template <int D>
 struct PagedLayout {
     static constexpr int kStages = D == 128 ? 3 : 4;
     static constexpr int kBlocksPerSm = D == 128 ? 2 : 3;
-    static constexpr int kRow = D * 2;                         // bytes of one key
-    static constexpr int kOperand = kPagedTile * kRow;         // one K or V tile
+    static constexpr int NSUB = D / 64;
+    static constexpr int kAtom = kPagedTile * 128;             // [64 keys][64 entries], 128-byte swizzle
+    static constexpr int kOperand = NSUB * kAtom;              // one K or V tile
     static constexpr int OFF_RED = kStages * 2 * kOperand;     // [16][D] fp32 sum over warps
-    static constexpr int OFF_BEFORE = OFF_RED + 16 * D * 4;
-    static constexpr int bytes(int Z) { return OFF_BEFORE + (Z + 1) * 4 + 64; }
+    static constexpr int OFF_BAR = OFF_RED + 16 * D * 4;       // full[kStages], empty[kStages]
+    static constexpr int OFF_ABORT = OFF_BAR + 2 * kStages * 8;
+    static constexpr int OFF_SUMS = OFF_ABORT + 8;             // one int per consumer warp
+    static constexpr int OFF_BEFORE = OFF_SUMS + 24;
+    static constexpr int bytes(int Z) { return OFF_BEFORE + (Z + 1) * 4 + 1024; }
 };
 
 __device__ __forceinline__ int paged_prefix(const PagedParams &p) {
@@ -94,6 +112,7 @@ struct PagedPlan {
 };
 __device__ __forceinline__ PagedPlan paged_plan(const PagedParams &p, int prefix) {
     PagedPlan a;
+    if (p.splits > 0) prefix = 0;    // the prefix kernel's
     a.prefix_tiles = (prefix + kPagedTile - 1) / kPagedTile;
     a.prefix_rows = 16 * p.prefix_warps;
     a.prefix_rt = static_cast<int>((static_cast<int64_t>(p.Z) * p.L * p.group + a.prefix_rows - 1) / a.prefix_rows);
@@ -160,17 +179,6 @@ __device__ __forceinline__ void paged_next(const PagedParams &p, const PagedPlan
     } while (c.tiles == 0);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    // a row that does not exist reads nothing and arrives as zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -203,6 +211,7 @@ struct PagedRows {
 // rows (16 each), 4 / WM along the keys of a tile.
 template <int D, int SCORE, int WM>
 struct PagedItem {
+    using Lay = PagedLayout<D>;
     static constexpr int WK = 4 / WM, KW = kPagedTile / WK, NK = D / 16;
     uint32_t qf[NK][4];
     float acc[D / 8][4];
@@ -255,11 +264,12 @@ struct PagedItem {
             {
                 // lanes 0-7: keys 0-7 low half, 8-15: keys 0-7 high half, then keys 8-15
                 const int row = k16 + (lane & 7) + ((lane >> 4) << 3);
-                const uint32_t base = sK + row * (D * 2);
+                const uint32_t base = sK + row * 128;
 #pragma unroll
                 for (int kk = 0; kk < NK; ++kk) {
                     uint32_t b[4];
-                    ldmatrix4(base + (((2 * kk + ((lane >> 3) & 1)) ^ (row & 7)) << 4), b);
+                    ldmatrix4(base + (kk >> 2) * Lay::kAtom + (((2 * (kk & 3) + ((lane >> 3) & 1)) ^ (row & 7)) << 4),
+                              b);
                     mma16816(s[0], qf[kk], b[0], b[1]);
                     mma16816(s[1], qf[kk], b[2], b[3]);
                 }
@@ -279,11 +289,12 @@ struct PagedItem {
             {
                 // lanes 0-7: keys 0-7, 8-15: keys 8-15, then the next 8 columns
                 const int row = k16 + (lane & 15);
-                const uint32_t base = sV + row * (D * 2);
+                const uint32_t base = sV + row * 128;
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
                     uint32_t b[4];
-                    ldmatrix4_trans(base + (((2 * d + (lane >> 4)) ^ (row & 7)) << 4), b);
+                    ldmatrix4_trans(base + (d >> 2) * Lay::kAtom + (((2 * (d & 3) + (lane >> 4)) ^ (row & 7)) << 4),
+                                    b);
                     mma16816(acc[2 * d], a, b[0], b[1]);
                     mma16816(acc[2 * d + 1], a, b[2], b[3]);
                 }
@@ -310,7 +321,7 @@ struct PagedItem {
                             *at = make_float2(old.x + acc[d][2 * i], old.y + acc[d][2 * i + 1]);
                         }
                 }
-                __syncthreads();
+                sigma_warps_sync(kPagedConsumers);
             }
             if (wm == m && wk == 0) {
 #pragma unroll
@@ -328,76 +339,88 @@ struct PagedItem {
                         *reinterpret_cast<float2 *>(dst + 16 * m * D + at) = v;
                     }
             }
-            if (WK > 1 && m + 1 < WM) __syncthreads();
+            // the next writers of `red` wait for these readers
+            if (WK > 1) sigma_warps_sync(kPagedConsumers);
         }
     }
 };
 
-// Issues the loads of one tile (K then V) into a stage.  A key that does not
-// exist, or whose page number is bad (flagged), arrives as zeros.
-template <int D>
-__device__ __forceinline__ void paged_load(const PagedParams &p, const PagedCursor &c, int keys, uint32_t stage) {
-    constexpr int CH = D / 8;                       // 16-byte chunks of a key
-    constexpr int STEP = kPagedThreads / CH;        // keys per pass
-    const int *table = c.z < 0 ? p.prefix_table : p.page_table + static_cast<size_t>(c.z) * p.max_pages;
-    const int ch = threadIdx.x % CH, r0 = threadIdx.x / CH;
-    const int mask = (1 << p.page_shift) - 1;
-    // pages hold at least 16 keys: four numbers cover a tile
-    int64_t base[4];
+// Page number of each of the 16-key groups of tile `tile` that start a box (pages
+// hold at least 16 keys), or `pages` where there is no such page: a box there
+// lies outside the tensor and arrives as zeros.  Bad numbers are flagged.
+template <int KEYS>
+__device__ __forceinline__ void paged_numbers(const PagedParams &p, const int *table, int tile, int keys, int box,
+                                              int (&page)[KEYS / 16]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int key = c.tile * kPagedTile + 16 * i;
-        int page = -1;
-        if (key < keys) {
-            page = __ldg(table + (key >> p.page_shift));
-            if (page < 0 || page >= p.pages) {
-                if (threadIdx.x == 0) record_status(p.status, kStatusPageRange);
-                page = -1;
-            }
+    for (int i = 0; i < KEYS / 16; ++i) {
+        const int key = tile * KEYS + 16 * i;
+        page[i] = p.pages;
+        if ((16 * i) % box == 0 && key < keys) {
+            const int n = __ldg(table + (key >> p.page_shift));
+            if (n >= 0 && n < p.pages) page[i] = n;
+            else record_status(p.status, kStatusPageRange);
         }
-        base[i] = page < 0 ? -1
-                           : (((static_cast<int64_t>(page) << p.page_shift) + (key & mask)) * p.Hk + c.kvh) * D;
     }
+}
+// Loads a tile of KEYS keys of one operand, box by box.
+template <int KEYS, int NSUB>
+__device__ __forceinline__ void paged_boxes(const PagedParams &p, const CUtensorMap *map, uint64_t *bar, uint8_t *dst,
+                                            int tile, int kvh, int box, const int (&page)[KEYS / 16]) {
+    const int mask = (1 << p.page_shift) - 1;
 #pragma unroll
-    for (int i = 0; i < kPagedTile / STEP; ++i) {
-        const int r = r0 + i * STEP;
-        const int64_t b = base[(i * STEP) / 16];   // STEP divides 16
-        const bool ok = b >= 0 && c.tile * kPagedTile + r < keys;
-        const size_t off = ok ? static_cast<size_t>(b) + static_cast<size_t>(r & 15) * p.Hk * D + 8 * ch : 0;
-        const uint32_t dst = stage + r * (D * 2) + ((ch ^ (r & 7)) << 4);
-        cp_async16(dst, p.k_pages + off, ok);
-        cp_async16(dst + kPagedTile * D * 2, p.v_pages + off, ok);
+    for (int i = 0; i < KEYS / 16; ++i) {
+        if ((16 * i) % box != 0) continue;
+#pragma unroll
+        for (int s = 0; s < NSUB; ++s)
+            tma_load_4d(map, bar, dst + s * (KEYS * 128) + i * 16 * 128, 64 * s, kvh, (tile * KEYS + 16 * i) & mask,
+                        page[i]);
     }
 }
 
 template <int D, int SCORE>
 __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
-    paged_tiles_kernel(const PagedParams p) {
+    paged_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ PagedParams p) {
     using Lay = PagedLayout<D>;
     constexpr int S = Lay::kStages;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1k(smem_raw);
     float *red = reinterpret_cast<float *>(smem + Lay::OFF_RED);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR), *empty = full + S;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
+    int *sums = reinterpret_cast<int *>(smem + Lay::OFF_SUMS);
     int *before = reinterpret_cast<int *>(smem + Lay::OFF_BEFORE);
-    __shared__ int sums[4];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
 
+    if (tid == kPagedConsumers) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 4);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
     // own tiles of the samples before each: one scan over the batch
     int carry = 0;
-    for (int z0 = 0; z0 < p.Z; z0 += kPagedThreads) {
+    for (int z0 = 0; z0 < p.Z; z0 += kPagedConsumers) {
         const int z = z0 + tid;
-        int t = z < p.Z ? (paged_lengths(p, z).x + kPagedTile - 1) / kPagedTile : 0;
-        if (z < p.Z && paged_lengths(p, z).y == 0) t = 0;       // no query: nothing to do
+        int t = 0;
+        if (tid < kPagedConsumers && z < p.Z) {
+            const int2 n = paged_lengths(p, z);
+            t = n.y > 0 ? (n.x + kPagedTile - 1) / kPagedTile : 0;       // no query: nothing to do
+        }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane_id() >= o) t += u;
+            if (lane >= o) t += u;
         }
-        if (lane_id() == 31) sums[warp_id()] = t;
+        if (lane == 31) sums[warp] = t;
         __syncthreads();
-        for (int w = 0; w < 4; ++w) {
-            if (w < warp_id()) t += sums[w];
-        }
-        if (z < p.Z) before[z + 1] = carry + t;
+        for (int w = 0; w < 4; ++w)
+            if (w < warp) t += sums[w];
+        if (tid < kPagedConsumers && z < p.Z) before[z + 1] = carry + t;
         carry += sums[0] + sums[1] + sums[2] + sums[3];
         __syncthreads();
     }
@@ -411,41 +434,77 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
     const int64_t total = a.own_first + static_cast<int64_t>(carry) * p.Hk * a.own_rt;
     const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);   // each has at least one tile
     if (blockIdx.x >= blocks) return;
-    const int64_t t0 = total * blockIdx.x / blocks, t1 = total * (blockIdx.x + 1) / blocks;
-    PagedCursor now = paged_locate(p, a, before, t0), ahead = now;
-    const uint32_t ring = smem_u32(smem);
+    const int64_t t0 = total * blockIdx.x / blocks;
+    const int count = static_cast<int>(total * (blockIdx.x + 1) / blocks - t0);
+    PagedCursor now = paged_locate(p, a, before, t0);
     auto keys_of = [&](const PagedCursor &c) { return c.z < 0 ? prefix : paged_lengths(p, c.z).x; };
-    int64_t issued = t0;
-    auto issue = [&]() {
-        if (issued < t1) {
-            paged_load<D>(p, ahead, keys_of(ahead), ring + static_cast<uint32_t>((issued - t0) % S) * 2 * Lay::kOperand);
-            if (++issued < t1) paged_next(p, a, before, ahead);
-        }
-        cp_async_commit();    // a group per step, empty at the end, so that the wait counts right
-    };
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) issue();
+    const WaitCtx wctx{abort_flag, p.status, p.timeout_ns};
 
-    // The tiles of one item, from `now` on; leaves `now` at the next item.
-    int64_t t = t0;
+    if (warp == 4) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const int box = min(1 << p.page_shift, kPagedTile);
+            int page[kPagedTile / 16];
+            int keys = 0, issued = 0;
+            const int *table = nullptr;
+            for (int t = 0; t < count; ++t) {
+                if (t == 0 || now.tile == 0) {
+                    keys = keys_of(now);
+                    table = now.z < 0 ? p.prefix_table : p.page_table + static_cast<size_t>(now.z) * p.max_pages;
+                }
+                paged_numbers<kPagedTile>(p, table, now.tile, keys, box, page);
+                const int s = t % S;
+                if (t >= S && !mbar_wait(&empty[s], ((t / S) - 1) & 1, wctx)) break;
+                uint8_t *st = smem + s * 2 * Lay::kOperand;
+                mbar_arrive_expect_tx(&full[s], 2 * Lay::kOperand);
+                paged_boxes<kPagedTile, Lay::NSUB>(p, &tmK, &full[s], st, now.tile, now.kvh, box, page);
+                paged_boxes<kPagedTile, Lay::NSUB>(p, &tmV, &full[s], st + Lay::kOperand, now.tile, now.kvh, box, page);
+                issued = t + 1;
+                if (issued < count) paged_next(p, a, before, now);
+            }
+            // every issued load must land before the block's shared memory is released
+            for (int t = (issued > S ? issued - S : 0); t < issued; ++t)
+                mbar_wait_drain(&full[t % S], (t / S) & 1, p.timeout_ns);
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    // The tiles of one item, from `now` on; leaves `now` at the next item.  A wait
+    // that gave up does not change the flow: all four warps meet the same
+    // barriers, and the results of an aborted call are not used.
+    int t = 0;
     auto run = [&]<int WM>() {
         PagedItem<D, SCORE, WM> it;
         const PagedCursor c = now;
+        const int keys = keys_of(c);
         it.begin(p, c, prefix);
         for (;;) {
-            cp_async_wait<S - 2>();
-            __syncthreads();      // tile t is here, and tile t - 1's slot is free
-            issue();
-            const uint32_t st = ring + static_cast<uint32_t>((t - t0) % S) * 2 * Lay::kOperand;
-            it.tile(st, st + Lay::kOperand, now.tile * kPagedTile);
-            ++t;
-            if (t >= t1) break;
+            const int s = t % S;
+            uint8_t *st = smem + s * 2 * Lay::kOperand;
+            mbar_wait(&full[s], (t / S) & 1, wctx);
+            __syncwarp();
+            const int valid = keys - now.tile * kPagedTile;
+            if (valid < kPagedTile) {
+                // rows behind the last key may hold anything: as values they are zeroed, as
+                // keys their scores are never used
+                for (int e = valid * 8 + tid; e < kPagedTile * 8; e += kPagedConsumers)
+#pragma unroll
+                    for (int u = 0; u < Lay::NSUB; ++u)
+                        reinterpret_cast<uint4 *>(st + Lay::kOperand + u * Lay::kAtom)[e] = make_uint4(0u, 0u, 0u, 0u);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next TMA writes
+                sigma_warps_sync(kPagedConsumers);
+            }
+            it.tile(smem_u32(st), smem_u32(st + Lay::kOperand), now.tile * kPagedTile);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++t >= count) break;
             paged_next(p, a, before, now);
             if (now.item != c.item) break;
         }
         it.end(red, p.part + (static_cast<size_t>(blockIdx.x) + c.item) * p.part_rows * D);
     };
-    while (t < t1) {
+    while (t < count) {
         const int w = now.z < 0 ? p.prefix_warps : p.own_warps;
         if (w == 1) run.template operator()<1>();
         else if (w == 2) run.template operator()<2>();
@@ -453,10 +512,251 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
     }
 }
 
+// ============================================================================
+// The prefix against many rows: the pair-of-tiles forward (span_fwd_sm100.cuh)
+// on gathered rows and paged keys.  Row r of row tile i is query head r % group
+// of token i * tile_tokens + r / group: a TMA box of (64 entries, group heads,
+// one key head, tile_tokens tokens) brings a tile's rows in that order.  Grid
+// (splits, pairs, key heads); block s takes the prefix's key tiles
+// [s T / S, (s + 1) T / S) and writes its rows' fp32 sums.
+// ============================================================================
+template <int D, int MODE, int SCORE>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    paged_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
+    constexpr int KS = FwdStages<D>::K, VS = FwdStages<D>::V;
+    using Lay = FwdLayout<D, KS, VS>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_1k(smem_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
+    uint64_t *q_full = bars;
+    uint64_t *k_full = bars + 1;
+    uint64_t *k_empty = k_full + KS;
+    uint64_t *v_full = k_empty + KS;
+    uint64_t *v_empty = v_full + VS;
+    uint64_t *s_full = v_empty + VS;
+    uint64_t *p_full = s_full + 2;
+    uint64_t *drain = p_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
+
+    const int warp = warp_id(), lane = lane_id();
+    const int split = blockIdx.x, pair = blockIdx.y, kvh = blockIdx.z;
+    const int prefix = paged_prefix(p);
+    const int T = (prefix + 127) / 128, S = min(p.splits, T);
+    if (split >= S) return;
+    const int J0 = static_cast<int>(static_cast<int64_t>(T) * split / S);
+    const int steps = static_cast<int>(static_cast<int64_t>(T) * (split + 1) / S) - J0;
+    const bool ragged = (prefix & 127) != 0 && J0 + steps == T;
+    const int64_t tokens = static_cast<int64_t>(p.Z) * p.L;
+    const int64_t tok0 = static_cast<int64_t>(pair) * 2 * p.tile_tokens;
+    const int ntiles = tok0 + p.tile_tokens < tokens ? 2 : 1;
+    const int box = min(1 << p.page_shift, 128);
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        for (int s = 0; s < KS; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < VS; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 256);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Lay::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wctx{abort_flag, p.status, p.timeout_ns};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int rows = p.tile_tokens * p.group;
+            mbar_arrive_expect_tx(q_full, ntiles * Lay::NSUB * rows * 128);
+            for (int t = 0; t < ntiles; ++t)
+                for (int s = 0; s < Lay::NSUB; ++s)
+                    tma_load_4d(&tmQ, q_full, smem + Lay::OFF_Q + t * Lay::TILE_BYTES + s * Lay::SUB_BYTES, 64 * s, 0,
+                                kvh, static_cast<int>(tok0) + t * p.tile_tokens);
+            int issued = 0, page[8];
+            for (int r = 0; r < steps; ++r) {
+                const int sk = r % KS;
+                paged_numbers<128>(p, p.prefix_table, J0 + r, prefix, box, page);
+                if (r >= KS && !mbar_wait(&k_empty[sk], ((r / KS) - 1) & 1, wctx)) break;
+                mbar_arrive_expect_tx(&k_full[sk], Lay::TILE_BYTES);
+                paged_boxes<128, Lay::NSUB>(p, &tmK, &k_full[sk], smem + Lay::OFF_K + sk * Lay::TILE_BYTES, J0 + r, kvh,
+                                            box, page);
+                issued = r + 1;
+            }
+            mbar_wait_drain(q_full, 0, p.timeout_ns);
+            for (int r = (issued > KS ? issued - KS : 0); r < issued; ++r)
+                mbar_wait_drain(&k_full[r % KS], (r / KS) & 1, p.timeout_ns);
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            int issued = 0, page[8];
+            for (int r = 0; r < steps; ++r) {
+                const int sv = r % VS;
+                paged_numbers<128>(p, p.prefix_table, J0 + r, prefix, box, page);
+                if (r >= VS && !mbar_wait(&v_empty[sv], ((r / VS) - 1) & 1, wctx)) break;
+                mbar_arrive_expect_tx(&v_full[sv], Lay::TILE_BYTES);
+                paged_boxes<128, Lay::NSUB>(p, &tmV, &v_full[sv], smem + Lay::OFF_V + sv * Lay::TILE_BYTES, J0 + r, kvh,
+                                            box, page);
+                issued = r + 1;
+            }
+            for (int r = (issued > VS ? issued - VS : 0); r < issued; ++r)
+                mbar_wait_drain(&v_full[r % VS], (r / VS) & 1, p.timeout_ns);
+        }
+    } else if (warp == 1) {
+        auto wt = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wctx));
+        };
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+        const uint32_t sQ = smem_u32(smem + Lay::OFF_Q);
+        const uint32_t sK = smem_u32(smem + Lay::OFF_K);
+        const uint32_t sV = smem_u32(smem + Lay::OFF_V);
+        constexpr uint32_t kDescHi = desc_hi(1024);
+        auto issue_s = [&](int t, uint32_t kbase) {
+            const uint32_t q_lo = desc_lo(sQ + t * Lay::TILE_BYTES, 16), k_lo = desc_lo(kbase, 16);
+            const uint32_t d_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t koff = ((kk >> 2) * Lay::SUB_BYTES + (kk & 3) * 32) >> 4;
+                mma_ss_lhw(d_tmem, q_lo + koff, k_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_w(&s_full[t]);
+        };
+        auto issue_pv = [&](int t, uint32_t vbase, bool first) {
+            const uint32_t d_tmem = tmem + (t ? Lay::COL_O1 : Lay::COL_O0);
+            const uint32_t a_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0);
+            const uint32_t v_lo = desc_lo(vbase, Lay::SUB_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mma_ts_lhw(d_tmem, a_tmem + kk * 8 + (kk >= 4 ? 32 : 0), v_lo + kk * ((16 * 128) >> 4), kDescHi,
+                           idesc_o, (!first || kk > 0) ? 1u : 0u);
+        };
+        // order per key tile as in span_fwd_kernel
+        bool ok = wt(q_full, 0) && wt(&k_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+            for (int t = 0; t < ntiles; ++t) issue_s(t, sK);
+            mma_commit_w(&k_empty[0]);
+        }
+        for (int r = 0; ok && r < steps; ++r) {
+            const int sv = r % VS, sk = (r + 1) % KS;
+            const bool more = r + 1 < steps;
+            if (!(ok = wt(&v_full[sv], (r / VS) & 1))) break;
+            if (!more && ragged)
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_V + sv * Lay::TILE_BYTES, prefix & 127);
+            for (int t = 0; t < ntiles; ++t) {
+                if (!(ok = wt(&p_full[t], r & 1))) break;
+                tc_fence_after();
+                issue_pv(t, sV + sv * Lay::TILE_BYTES, r == 0);
+                if (t == ntiles - 1) mma_commit_w(&v_empty[sv]);
+                if (more) {
+                    if (t == 0 && !(ok = wt(&k_full[sk], ((r + 1) / KS) & 1))) break;
+                    tc_fence_after();
+                    issue_s(t, sK + sk * Lay::TILE_BYTES);
+                    if (t == ntiles - 1) mma_commit_w(&k_empty[sk]);
+                }
+            }
+        }
+        mma_commit_w(drain);
+        mbar_wait_drain(drain, 0, p.timeout_ns);
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int g = (warp - 4) >> 2;
+        const int t = g >> 1, c = g & 1;
+        const int quarter = warp & 3;
+        const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+        const int row = quarter * 32 + lane;
+        if (t < ntiles) {
+            // the token and head of this row
+            const int64_t tok = tok0 + static_cast<int64_t>(t) * p.tile_tokens + row / p.group;
+            const int h = kvh * p.group + row % p.group;
+            ScoreCoef cf = {0.0f, -64.0f, 0.0f, 0.0f};    // of rows that are not there: sigma of almost nothing
+            bool live = row < p.tile_tokens * p.group && tok < tokens;
+            float pos = 0.0f;
+            if (live) {
+                const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
+                const int2 n = paged_lengths(p, z);
+                live = l < n.y;
+                pos = static_cast<float>(prefix + n.x - n.y + l);
+                cf = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
+                                       SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
+            }
+            // the same choice in the whole warp
+            int pause = __all_sync(0xffffffffu, !live || tail_pause(cf) == 0) ? 0 : 1 << 30;
+            bool ok = true;
+            const uint32_t tS = tmem + lane_bits + (t ? Lay::COL_S1 : Lay::COL_S0) + 64 * c;
+            for (int r = 0; r < steps; ++r) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], r & 1, wctx));
+                if (!ok) break;
+                tc_fence_after();
+                const int key0 = (J0 + r) * 128 + 64 * c;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t x[32], pk[16];
+                    tmem_ld32(tS + 32 * u, x);
+                    score_chunk<MODE, SCORE, false>(x, cf, pos - static_cast<float>(key0 + 32 * u), pk, nullptr, pause);
+                    if (prefix - key0 < 64) keep_bits(pk, bit_range(0, prefix - key0 - 32 * u));
+                    tmem_st16(tS + 16 * u, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[t]);
+            }
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
+            if (ok) {
+                tc_fence_after();
+                constexpr int HALF = D / 2;
+                const uint32_t tO = tmem + lane_bits + (t ? Lay::COL_O1 : Lay::COL_O0) + c * HALF;
+                float4 *dst = reinterpret_cast<float4 *>(
+                    p.prefix_part +
+                    (((static_cast<size_t>(split) * p.Hk + kvh) * p.pairs + pair) * 256 + t * 128 + row) * D + c * HALF);
+#pragma unroll
+                for (int cc = 0; cc < HALF / 32; ++cc) {
+                    uint32_t x[32];
+                    tmem_ld32(tO + 32 * cc, x);
+                    if (live) {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            dst[8 * cc + v] = make_float4(__uint_as_float(x[4 * v]), __uint_as_float(x[4 * v + 1]),
+                                                          __uint_as_float(x[4 * v + 2]), __uint_as_float(x[4 * v + 3]));
+                    }
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Lay::TMEM_COLS);
+    }
+}
+
 // Adds up the partials of each output row, prefix items first, in block order.
 // One warp per row.
 template <int D>
-__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
     constexpr int E = D / 32;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
     if (r >= static_cast<int64_t>(p.Z) * p.L * p.H) return;
@@ -474,15 +774,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
         const int64_t per = static_cast<int64_t>(p.Hk) * a.own_rt;
         const int64_t total = a.own_first + p.before[p.Z] * per;
         const int64_t blocks = min(static_cast<int64_t>(p.blocks), total);
-        // partials of the item with tiles [first, first + tiles), row `row` of it
-        auto add = [&](int64_t first, int tiles, int64_t item, int row) {
-            if (tiles == 0) return;
-            const int64_t b0 = ((first + 1) * blocks - 1) / total;
-            const int64_t b1 = ((first + tiles) * blocks - 1) / total;
-            const float *src = p.part + ((b0 + item) * p.part_rows + row) * D + lane * E;
-            const size_t step = static_cast<size_t>(p.part_rows) * D;
-#pragma unroll 4
-            for (int64_t b = b0; b <= b1; ++b, src += step) {
+        auto sum = [&](const float *src, size_t step, int64_t count) {
+#pragma unroll 8
+            for (int64_t b = 0; b < count; ++b, src += step) {
                 if constexpr (E == 4) {
                     const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
                     acc[0] += v.x;
@@ -496,7 +790,21 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
                 }
             }
         };
-        {
+        // partials of the item with tiles [first, first + tiles), row `row` of it
+        auto add = [&](int64_t first, int tiles, int64_t item, int row) {
+            if (tiles == 0) return;
+            const int64_t b0 = ((first + 1) * blocks - 1) / total;
+            const int64_t b1 = ((first + tiles) * blocks - 1) / total;
+            sum(p.part + ((b0 + item) * p.part_rows + row) * D + lane * E, static_cast<size_t>(p.part_rows) * D,
+                b1 - b0 + 1);
+        };
+        if (p.splits > 0) {
+            const int T = (prefix + 127) / 128, S = min(p.splits, T);
+            const int64_t tile = tok / p.tile_tokens;      // row tile
+            const int row = static_cast<int>(tok % p.tile_tokens) * p.group + g;
+            const float *src = p.prefix_part + ((kvh * p.pairs + tile / 2) * 256 + (tile & 1) * 128 + row) * D + lane * E;
+            sum(src, static_cast<size_t>(p.Hk) * p.pairs * 256 * D, S);
+        } else {
             const int64_t row = tok * p.group + g;
             const int64_t item = static_cast<int64_t>(kvh) * a.prefix_rt + row / a.prefix_rows;
             add(item * a.prefix_tiles, a.prefix_tiles, item, static_cast<int>(row % a.prefix_rows));

@@ -12,6 +12,8 @@ import ctypes
 
 import torch
 
+from . import _BF16, _FP32, _check, _dtype_code, _stream_ptr, load_library
+
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
 
@@ -26,82 +28,100 @@ def register(lib):
         f.restype = _ci
 
 
-class on_device:
-    """Makes a tensor's device the current one for a call, when it is not."""
+_current_device = torch._C._cuda_getDevice
 
-    __slots__ = ("index", "before")
 
-    def __init__(self, t):
-        self.index = t.get_device()
-
-    def __enter__(self):
-        self.before = torch._C._cuda_getDevice()
-        if self.before != self.index:
-            torch._C._cuda_setDevice(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch._C._cuda_setDevice(self.before)
-        return False
+def run_on(device: int, f, args, name: str):
+    """Calls entry point f with `device` as the current one."""
+    if _current_device() == device:
+        code = f(*args)
+    else:
+        with torch.cuda.device(device):
+            code = f(*args)
+    if code:
+        _check(code, name)
 
 
 def check_pair(q, keys, what="k and v"):
-    """q [Z, L, H, D] and the tensors of its shared key heads [Z, L, Hk, D]."""
-    if q.dim() != 4:
+    """q [Z, L, H, D] and the tensors of its shared key heads [Z, L, Hk, D];
+    returns (shape of q, Hk, device index)."""
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("tensors must be [Z, L, H, D]")
-    if not q.is_cuda:
+    device, dtype = q.get_device(), q.dtype
+    if device < 0:
         raise ValueError("sigattn tensors must live on a CUDA device (no CPU fallback)")
     if not q.is_contiguous():
         raise ValueError("tensors must be contiguous [Z, L, H, D]")
-    Z, L, H, D = q.shape
-    ref = keys[0]
+    Z, L, H, D = shape
+    first = keys[0].shape
+    if len(first) != 4 or first[0] != Z or first[1] != L or first[3] != D:
+        raise ValueError(f"{what} must be [Z, L, Hk, D] with the queries' Z, L and D")
     for t in keys:
-        if t.dim() != 4 or t.shape != ref.shape or t.shape[:2] != q.shape[:2] or t.shape[3] != D:
+        if t.shape != first:
             raise ValueError(f"{what} must be [Z, L, Hk, D] with the queries' Z, L and D")
-        if t.dtype != q.dtype or t.device != q.device:
+        if t.dtype is not dtype or t.get_device() != device:
             raise ValueError("all tensors must share dtype and device")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous [Z, L, Hk, D]")
-    Hk = ref.shape[2]
+    Hk = first[2]
     if H and (Hk == 0 or H % Hk):
         raise ValueError(f"{H} query heads cannot share {Hk} key heads evenly")
+    return shape, Hk, device
 
 
 def check_like(ref, tensors):
     for t in tensors:
-        if t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device or not t.is_contiguous():
+        if t.shape != ref.shape or t.dtype is not ref.dtype or t.get_device() != ref.get_device() \
+                or not t.is_contiguous():
             raise ValueError("outputs and gradients must be contiguous, with the shape, dtype and device "
                              "of the tensor they belong to")
 
 
 def check_ints(t, shape, device, name):
-    if not (t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous()
-            and t.device == device):
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the tensors' device")
 
 
 def check_floats(t, count, device, name):
-    if not (t.dtype == torch.float32 and t.dim() == 1 and t.shape[0] == count and t.is_contiguous()
-            and t.device == device):
+    if t.dtype is not torch.float32 or t.shape != (count,) or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 [{count}] tensor on the tensors' device")
 
 
-def score_args(q, bias, cap, slopes):
+def score_args(Z, H, device, bias, cap, slopes):
     """(scalar bias, per-sample bias pointer, cap, slopes pointer) of a call."""
     bias_ptr = slopes_ptr = None
     if isinstance(bias, torch.Tensor):
-        check_floats(bias, q.shape[0], q.device, "bias")
+        check_floats(bias, Z, device, "bias")
         bias_ptr, bias = bias.data_ptr(), 0.0
     if slopes is not None:
-        check_floats(slopes, q.shape[2], q.device, "slopes")
+        check_floats(slopes, H, device, "slopes")
         slopes_ptr = slopes.data_ptr()
     return float(bias), bias_ptr, float(cap), slopes_ptr
 
 
-def _check_mask(q, seqlens, spans):
-    check_ints(seqlens, q.shape[:1], q.device, "seqlens")
-    if spans is not None:
-        check_ints(spans, (q.shape[0], q.shape[1], 2), q.device, "spans")
+def workspace_args(workspace, ref, device, size_of, args):
+    """(tensor to hold until the launch, pointer, bytes) of the caller's workspace,
+    or of one allocated for the call: its memory goes back to the allocator of the
+    current stream, in whose order it may be used again."""
+    if workspace is None:
+        need = size_of(*args)
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=ref.device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the tensors' device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _mask_args(Z, L, device, seqlens, spans):
+    """(lengths pointer, spans pointer) of a call."""
+    check_ints(seqlens, (Z,), device, "seqlens")
+    if spans is None:
+        return seqlens.data_ptr(), None
+    check_ints(spans, (Z, L, 2), device, "spans")
+    return seqlens.data_ptr(), spans.data_ptr()
 
 
 def fwd_span(q, k, v, seqlens, alpha: float, bias, spans=None, cap: float = 0.0, slopes=None, out=None):
@@ -110,26 +130,21 @@ def fwd_span(q, k, v, seqlens, alpha: float, bias, spans=None, cap: float = 0.0,
     float32 [Z] with one bias per sample.  ``spans``: int32 [Z, L, 2], the keys
     [lo, hi) that each row sees (``mask_spans``; None: all).  ``cap``: 0 for none.
     ``slopes``: float32 [H], how fast a head's scores fall with |i - j|."""
-    from . import _check, _dtype_code, _stream_ptr, load_library
-    check_pair(q, [k, v])
-    _check_mask(q, seqlens, spans)
-    b, bias_ptr, cap, slopes_ptr = score_args(q, bias, cap, slopes)
+    (Z, L, H, D), Hk, device = check_pair(q, (k, v))
+    lens_ptr, spans_ptr = _mask_args(Z, L, device, seqlens, spans)
+    b, bias_ptr, cap, slopes_ptr = score_args(Z, H, device, bias, cap, slopes)
     if out is None:
         out = torch.empty_like(q)
     else:
-        check_like(q, [out])
-    Z, L, H, D = q.shape
-    with on_device(q):
-        _check(load_library().sigattn_fwd_span(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), seqlens.data_ptr(),
-            None if spans is None else spans.data_ptr(), Z, L, H, k.shape[2], D, float(alpha), b, bias_ptr,
-            cap, slopes_ptr, _dtype_code(q), _stream_ptr(q)), "sigattn_fwd_span")
+        check_like(q, (out,))
+    run_on(device, load_library().sigattn_fwd_span,
+           (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lens_ptr, spans_ptr, Z, L, H, Hk, D,
+            float(alpha), b, bias_ptr, cap, slopes_ptr, _dtype_code(q), _stream_ptr(q)), "sigattn_fwd_span")
     return out
 
 
 def bwd_span_workspace_bytes(Z: int, L: int, dtype) -> int:
     """Device workspace bytes of ``bwd_span``."""
-    from . import _BF16, _FP32, load_library
     code = _FP32 if dtype == torch.float32 else _BF16
     return int(load_library().sigattn_bwd_span_workspace_bytes(int(Z), int(L), code))
 
@@ -139,29 +154,21 @@ def bwd_span(q, k, v, dout, seqlens, alpha: float, bias, spans=None, cap: float 
     """(dQ, dK, dV) of ``fwd_span`` given dout = dLoss/dO; P is recomputed, O is
     not needed.  ``workspace``: a device uint8 tensor of at least
     ``bwd_span_workspace_bytes`` bytes (allocated here when omitted)."""
-    from . import _check, _dtype_code, _stream_ptr, load_library
-    check_pair(q, [k, v])
-    _check_mask(q, seqlens, spans)
-    b, bias_ptr, cap, slopes_ptr = score_args(q, bias, cap, slopes)
+    (Z, L, H, D), Hk, device = check_pair(q, (k, v))
+    lens_ptr, spans_ptr = _mask_args(Z, L, device, seqlens, spans)
+    b, bias_ptr, cap, slopes_ptr = score_args(Z, H, device, bias, cap, slopes)
+    check_like(q, (dout,) if dq is None else (dout, dq))
+    check_like(k, [t for t in (dk, dv) if t is not None])
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    check_like(q, [dout, dq])
-    check_like(k, [dk, dv])
-    Z, L, H, D = q.shape
-    code = _dtype_code(q)
-    if workspace is None:
-        lib = load_library()
-        workspace = torch.empty(lib.sigattn_bwd_span_workspace_bytes(Z, L, code), dtype=torch.uint8,
-                                device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the tensors' device")
-    with on_device(q):
-        _check(load_library().sigattn_bwd_span(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-            dv.data_ptr(), seqlens.data_ptr(), None if spans is None else spans.data_ptr(), Z, L, H,
-            k.shape[2], D, float(alpha), b, bias_ptr, cap, slopes_ptr, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), code, _stream_ptr(q)), "sigattn_bwd_span")
+    lib, code = load_library(), _dtype_code(q)
+    workspace, ws_ptr, ws_bytes = workspace_args(workspace, q, device, lib.sigattn_bwd_span_workspace_bytes,
+                                                 (Z, L, code))
+    run_on(device, lib.sigattn_bwd_span,
+           (q.data_ptr(), k.data_ptr(), v.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            lens_ptr, spans_ptr, Z, L, H, Hk, D, float(alpha), b, bias_ptr, cap, slopes_ptr, ws_ptr, ws_bytes, code,
+            _stream_ptr(q)), "sigattn_bwd_span")
     return dq, dk, dv
 
 
@@ -174,25 +181,24 @@ def mask_spans(seqlens, L: int, causal: bool = False, prefix=None, docs=None, wi
     the run of equal ids around it, and a prefix counts from the run's start.
     ``window`` > 0: at most that many keys back (and, without ``causal``, forward),
     the row's own included."""
-    from . import _check, _stream_ptr, load_library
-    if not (isinstance(seqlens, torch.Tensor) and seqlens.is_cuda and seqlens.dim() == 1):
+    device = seqlens.get_device()
+    if device < 0 or seqlens.dim() != 1:
         raise ValueError("seqlens must be a contiguous int32 [Z] CUDA tensor")
     Z, L, window = seqlens.shape[0], int(L), int(window)
-    check_ints(seqlens, (Z,), seqlens.device, "seqlens")
+    check_ints(seqlens, (Z,), device, "seqlens")
     if prefix is not None:
-        check_ints(prefix, (Z,), seqlens.device, "prefix")
+        check_ints(prefix, (Z,), device, "prefix")
         if window:
             raise ValueError("a prefix and a window do not make one interval of keys")
         causal = True
     if docs is not None:
-        check_ints(docs, (Z, L), seqlens.device, "docs")
+        check_ints(docs, (Z, L), device, "docs")
     if out is None:
         out = torch.empty((Z, L, 2), dtype=torch.int32, device=seqlens.device)
     else:
-        check_ints(out, (Z, L, 2), seqlens.device, "out")
-    with on_device(seqlens):
-        _check(load_library().sigattn_mask_spans(
-            seqlens.data_ptr(), None if prefix is None else prefix.data_ptr(),
+        check_ints(out, (Z, L, 2), device, "out")
+    run_on(device, load_library().sigattn_mask_spans,
+           (seqlens.data_ptr(), None if prefix is None else prefix.data_ptr(),
             None if docs is None else docs.data_ptr(), int(bool(causal)), window, Z, L, out.data_ptr(),
             _stream_ptr(seqlens)), "sigattn_mask_spans")
     return out
