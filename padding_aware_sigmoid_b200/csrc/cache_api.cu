@@ -51,7 +51,8 @@ constexpr int kPagedMostBlocks = 3 * kPagedMostSms;  // of the tile kernel
 constexpr int64_t kPrefixKernelRows = 32;
 
 struct PagedSizes {
-    int prefix_warps, own_warps, part_rows;
+    int prefix_warps, own_warps;
+    int64_t prefix_rt, own_rt;     // row tiles per key head: of the prefix, of a sample
     int64_t items;
     int tile_tokens;      // tokens of a row tile of the prefix kernel; 0: it does not run
     int64_t pairs;        // its pairs of row tiles
@@ -61,9 +62,9 @@ PagedSizes paged_sizes(int Z, int L, int H, int Hk) {
     const int64_t own = static_cast<int64_t>(L) * (H / Hk), all = own * Z;
     s.prefix_warps = row_warps(all);
     s.own_warps = row_warps(own);
-    s.part_rows = 16 * std::max(s.prefix_warps, s.own_warps);
-    s.items = Hk * ((all + 16 * s.prefix_warps - 1) / (16 * s.prefix_warps) +
-                    Z * ((own + 16 * s.own_warps - 1) / (16 * s.own_warps)));
+    s.prefix_rt = (all + 16 * s.prefix_warps - 1) / (16 * s.prefix_warps);
+    s.own_rt = (own + 16 * s.own_warps - 1) / (16 * s.own_warps);
+    s.items = Hk * (s.prefix_rt + Z * s.own_rt);
     s.tile_tokens = 0;
     s.pairs = 0;
     if (H / Hk <= 128 && all > kPrefixKernelRows) {
@@ -74,13 +75,13 @@ PagedSizes paged_sizes(int Z, int L, int H, int Hk) {
 }
 
 size_t part_bytes(const PagedSizes &s, int D) {
-    return static_cast<size_t>(kPagedMostBlocks + s.items) * s.part_rows * D * sizeof(float);
+    return static_cast<size_t>(kPagedMostBlocks + s.items) * kPagedPartRows * D * sizeof(float);
 }
 // the splits are chosen so that all blocks of the prefix kernel fit the SMs once
 size_t prefix_part_bytes(const PagedSizes &s, int Hk, int D) {
     return s.pairs == 0 ? 0 : (kPagedMostSms + static_cast<size_t>(s.pairs) * Hk) * 256 * D * sizeof(float);
 }
-size_t before_bytes(int Z) { return (static_cast<size_t>(Z + 1) * 4 + 255) & ~size_t(255); }
+size_t blocks_bytes(const PagedSizes &s) { return (static_cast<size_t>(s.items) * sizeof(int2) + 255) & ~size_t(255); }
 
 // A bf16 tensor of four dimensions (innermost first, 128-byte swizzle).
 sigattn_status encode_box(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
@@ -113,8 +114,13 @@ sigattn_status prefix_launch(const PagedMaps &m, const PagedParams &p, cudaStrea
     return launch(paged_prefix_kernel<D, MODE, SCORE>, dim3(p.splits, p.pairs, p.Hk), dim3(kFwdThreads),
                   FwdLayout<D, KS, VS>::SMEM_ALLOC, st, m.prefix_q, m.prefix_k, m.prefix_v, p);
 }
+#ifndef PAGED_W8
+#define PAGED_W8 512
+#define PAGED_W4 4096
+#define PAGED_W2 16384
+#endif
 template <int D, int SCORE>
-sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
+sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, int blocks, cudaStream_t st) {
     using Lay = PagedLayout<D>;
     sigattn_status s = SIGATTN_OK;
     if (p.splits > 0) {
@@ -122,19 +128,29 @@ sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream
                                                   : prefix_launch<D, kSigmoidExp, SCORE>(m, p, st);
         if (s != SIGATTN_OK) return s;
     }
-    s = launch(paged_tiles_kernel<D, SCORE>, dim3(p.blocks), dim3(kPagedThreads), Lay::bytes(SIGATTN_PAGED_MAX_Z),
-               Lay::bytes(p.Z), st, m.k, m.v, p);
+    // The tile kernel needs nothing of the prefix kernel's, and the join reads
+    // its lengths before it waits: both may start early.
+    s = launch_with(paged_tiles_kernel<D, SCORE>, dim3(blocks), dim3(kPagedThreads), Lay::bytes(SIGATTN_PAGED_MAX_Z),
+                    Lay::bytes(p.Z), p.splits > 0, st, m.k, m.v, p);
     if (s != SIGATTN_OK) return s;
+    // Few rows: a block each, its warps sharing the row's partials.
     const int64_t rows = static_cast<int64_t>(p.Z) * p.L * p.H;
-    return launch(paged_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, p);
+    auto join = [&](auto kernel, int per_block) {
+        return launch_with(kernel, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)), dim3(kJoinThreads),
+                           0, 0, true, st, p);
+    };
+    if (rows <= PAGED_W8) return join(paged_join_kernel<D, 8>, 1);
+    if (rows <= PAGED_W4) return join(paged_join_kernel<D, 4>, 2);
+    if (rows <= PAGED_W2) return join(paged_join_kernel<D, 2>, 4);
+    return join(paged_join_kernel<D, 1>, 8);
 }
 template <int D>
-sigattn_status paged_score(int score, const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
+sigattn_status paged_score(int score, const PagedMaps &m, const PagedParams &p, int blocks, cudaStream_t st) {
     switch (score) {
-        case 0: return paged_launch<D, 0>(m, p, st);
-        case kScoreCap: return paged_launch<D, kScoreCap>(m, p, st);
-        case kScoreSlope: return paged_launch<D, kScoreSlope>(m, p, st);
-        default: return paged_launch<D, kScoreCap | kScoreSlope>(m, p, st);
+        case 0: return paged_launch<D, 0>(m, p, blocks, st);
+        case kScoreCap: return paged_launch<D, kScoreCap>(m, p, blocks, st);
+        case kScoreSlope: return paged_launch<D, kScoreSlope>(m, p, blocks, st);
+        default: return paged_launch<D, kScoreCap | kScoreSlope>(m, p, blocks, st);
     }
 }
 
@@ -210,7 +226,7 @@ size_t sigattn_fwd_paged_workspace_bytes(int Z, int L, int H, int Hk, int D, sig
     if (Z <= 0 || L <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || (D != 64 && D != 128) || dtype != SIGATTN_BF16)
         return 0;
     const PagedSizes s = paged_sizes(Z, L, H, Hk);
-    return before_bytes(Z) + part_bytes(s, D) + prefix_part_bytes(s, Hk, D);
+    return blocks_bytes(s) + part_bytes(s, D) + prefix_part_bytes(s, Hk, D);
 }
 
 sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void *v_pages, void *o,
@@ -280,20 +296,21 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
     }
     if ((s = get_encoder()) != SIGATTN_OK) return s;
     char *ws = static_cast<char *>(workspace);
-    p.before = reinterpret_cast<int *>(ws);
-    p.part = reinterpret_cast<float *>(ws + before_bytes(Z));
+    p.blocks_of = reinterpret_cast<int2 *>(ws);
+    p.part = reinterpret_cast<float *>(ws + blocks_bytes(z));
+    p.prefix_rt = static_cast<int>(z.prefix_rt);
+    p.own_rt = static_cast<int>(z.own_rt);
     p.prefix_warps = z.prefix_warps;
     p.own_warps = z.own_warps;
-    p.part_rows = z.part_rows;
     const int sms = std::min(g_sm_count[dev], kPagedMostSms);
-    p.blocks = sms * (D == 64 ? PagedLayout<64>::kBlocksPerSm : PagedLayout<128>::kBlocksPerSm);
+    const int blocks = sms * (D == 64 ? PagedLayout<64>::kBlocksPerSm : PagedLayout<128>::kBlocksPerSm);
     p.timeout_ns = g_timeout_ns.load();
     PagedMaps m;
     const int own_box = std::min(page_size, kPagedTile);
     if ((s = encode_pages(&m.k, k_pages, c, own_box)) != SIGATTN_OK) return s;
     if ((s = encode_pages(&m.v, v_pages, c, own_box)) != SIGATTN_OK) return s;
     if (z.tile_tokens > 0 && prefix_len != nullptr && prefix_pages > 0) {
-        p.prefix_part = reinterpret_cast<float *>(ws + before_bytes(Z) + part_bytes(z, D));
+        p.prefix_part = reinterpret_cast<float *>(ws + blocks_bytes(z) + part_bytes(z, D));
         p.tile_tokens = z.tile_tokens;
         p.pairs = static_cast<int>(z.pairs);
         p.splits = static_cast<int>(std::max<int64_t>(1, sms / (z.pairs * Hk)));
@@ -306,7 +323,7 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
             return s;
     }
     const int score = (cap > 0.0f ? kScoreCap : 0) | (slopes != nullptr ? kScoreSlope : 0);
-    return D == 64 ? paged_score<64>(score, m, p, st) : paged_score<128>(score, m, p, st);
+    return D == 64 ? paged_score<64>(score, m, p, blocks, st) : paged_score<128>(score, m, p, blocks, st);
 }
 
 }  // extern "C"

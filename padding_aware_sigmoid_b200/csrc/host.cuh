@@ -158,9 +158,11 @@ inline std::mutex g_attr_mu;
 inline std::unordered_set<FuncDev, FuncDevHash> g_attr_set;
 
 // smem_most: the most dynamic shared memory any call asks of this kernel.
+// overlap: the kernel may start while the one before it on the stream still
+// runs (programmatic dependent launch); it waits for it by itself.
 template <typename... KArgs, typename... Args>
-sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem_most, size_t smem,
-                      cudaStream_t stream, Args... args) {
+sigattn_status launch_with(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem_most, size_t smem,
+                           bool overlap, cudaStream_t stream, Args... args) {
     if (smem_most > 48 * 1024) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
@@ -179,6 +181,11 @@ sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = overlap ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) return cuda_fail(e);
     return SIGATTN_OK;
@@ -186,7 +193,7 @@ sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
 template <typename... KArgs, typename... Args>
 sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                       Args... args) {
-    return launch(kernel, grid, block, smem, smem, stream, args...);
+    return launch_with(kernel, grid, block, smem, smem, false, stream, args...);
 }
 
 }  // namespace sigattn

@@ -49,11 +49,10 @@ struct PagedParams {
     int pages, page_shift, max_pages, prefix_pages;
     float alpha, bias, cap;
     const float *bias_z, *slopes;
-    float *part;          // [block + item][rows][D]
-    int *before;          // [Z + 1] own tiles of the samples before z, written by block 0
+    float *part;          // [block + item][kPagedPartRows][D]
+    int2 *blocks_of;      // [item] first and last block of each item that has tiles
     int prefix_warps, own_warps;   // warps along the rows (1, 2, 4): row tiles of 16 times that
-    int part_rows;        // rows of one partial: the larger row tile
-    int blocks;           // grid of the tile kernel
+    int prefix_rt, own_rt;         // row tiles of the prefix and of a sample, per key head
     // the prefix kernel, when it runs (splits > 0; the tile kernel then leaves the prefix out)
     float *prefix_part;   // [split][key head][pair][256][D]
     int splits, pairs;    // blocks along the keys; pairs of row tiles
@@ -65,6 +64,10 @@ struct PagedParams {
 constexpr int kPagedConsumers = 128;
 constexpr int kPagedThreads = kPagedConsumers + 32;
 constexpr int kPagedTile = 64;    // keys per tile
+// Rows of one partial: each of the four warps writes its own 16 (WM warps along
+// the rows, 4 / WM along the keys of a tile), so that nothing waits at an item's
+// end; the join adds the warps along the keys as well.
+constexpr int kPagedPartRows = 64;
 
 template <int D>
 struct PagedLayout {
@@ -73,8 +76,7 @@ struct PagedLayout {
     static constexpr int NSUB = D / 64;
     static constexpr int kAtom = kPagedTile * 128;             // [64 keys][64 entries], 128-byte swizzle
     static constexpr int kOperand = NSUB * kAtom;              // one K or V tile
-    static constexpr int OFF_RED = kStages * 2 * kOperand;     // [16][D] fp32 sum over warps
-    static constexpr int OFF_BAR = OFF_RED + 16 * D * 4;       // full[kStages], empty[kStages]
+    static constexpr int OFF_BAR = kStages * 2 * kOperand;     // full[kStages], empty[kStages]
     static constexpr int OFF_ABORT = OFF_BAR + 2 * kStages * 8;
     static constexpr int OFF_SUMS = OFF_ABORT + 8;             // one int per consumer warp
     static constexpr int OFF_BEFORE = OFF_SUMS + 24;
@@ -104,6 +106,11 @@ __device__ __forceinline__ int2 paged_lengths(const PagedParams &p, int z) {
     return make_int2(nk, nq);
 }
 
+// Lets the next kernel of the stream start, and waits until the one before has
+// finished (both do nothing where the launch did not ask for it).
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The shape of the item list.
 struct PagedPlan {
     int prefix_tiles, prefix_rows, prefix_rt, prefix_items;   // tiles of the prefix; rows per tile; row tiles; items
@@ -115,10 +122,10 @@ __device__ __forceinline__ PagedPlan paged_plan(const PagedParams &p, int prefix
     if (p.splits > 0) prefix = 0;    // the prefix kernel's
     a.prefix_tiles = (prefix + kPagedTile - 1) / kPagedTile;
     a.prefix_rows = 16 * p.prefix_warps;
-    a.prefix_rt = static_cast<int>((static_cast<int64_t>(p.Z) * p.L * p.group + a.prefix_rows - 1) / a.prefix_rows);
+    a.prefix_rt = p.prefix_rt;
     a.prefix_items = a.prefix_rt * p.Hk;
     a.own_rows = 16 * p.own_warps;
-    a.own_rt = (p.L * p.group + a.own_rows - 1) / a.own_rows;
+    a.own_rt = p.own_rt;
     a.own_first = static_cast<int64_t>(a.prefix_tiles) * a.prefix_items;
     return a;
 }
@@ -302,45 +309,16 @@ struct PagedItem {
         }
     }
 
-    // Adds the warps along the keys up, in warp order (16 rows at a time), and
-    // writes the rows.
-    __device__ __forceinline__ void end(float *red, float *dst) {
+    // Writes the rows that exist: [warp along the keys][row of the tile][D].
+    __device__ __forceinline__ void end(float *dst) {
         const int lane = lane_id(), wm = warp_id() % WM, wk = warp_id() / WM;
-        const int r0 = lane / 4, c0 = 2 * (lane & 3);
+        dst += (wk * 16 * WM + wm * 16 + lane / 4) * D + 2 * (lane & 3);
 #pragma unroll
-        for (int m = 0; m < WM; ++m) {
+        for (int i = 0; i < 2; ++i) {
+            if (rows.q[i] == nullptr) continue;
 #pragma unroll
-            for (int w = 1; w < WK; ++w) {
-                if (wm == m && wk == w) {
-#pragma unroll
-                    for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float2 *at = reinterpret_cast<float2 *>(red + (r0 + 8 * i) * D + 8 * d + c0);
-                            const float2 old = w > 1 ? *at : make_float2(0.0f, 0.0f);
-                            *at = make_float2(old.x + acc[d][2 * i], old.y + acc[d][2 * i + 1]);
-                        }
-                }
-                sigma_warps_sync(kPagedConsumers);
-            }
-            if (wm == m && wk == 0) {
-#pragma unroll
-                for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (rows.q[i] == nullptr) continue;
-                        const int at = (r0 + 8 * i) * D + 8 * d + c0;
-                        float2 v = make_float2(acc[d][2 * i], acc[d][2 * i + 1]);
-                        if constexpr (WK > 1) {
-                            const float2 o = *reinterpret_cast<const float2 *>(red + at);
-                            v.x += o.x;
-                            v.y += o.y;
-                        }
-                        *reinterpret_cast<float2 *>(dst + 16 * m * D + at) = v;
-                    }
-            }
-            // the next writers of `red` wait for these readers
-            if (WK > 1) sigma_warps_sync(kPagedConsumers);
+            for (int d = 0; d < D / 8; ++d)
+                *reinterpret_cast<float2 *>(dst + 8 * i * D + 8 * d) = make_float2(acc[d][2 * i], acc[d][2 * i + 1]);
         }
     }
 };
@@ -385,13 +363,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
     constexpr int S = Lay::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1k(smem_raw);
-    float *red = reinterpret_cast<float *>(smem + Lay::OFF_RED);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR), *empty = full + S;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
     int *sums = reinterpret_cast<int *>(smem + Lay::OFF_SUMS);
     int *before = reinterpret_cast<int *>(smem + Lay::OFF_BEFORE);
     const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
 
+    grid_release();
     if (tid == kPagedConsumers) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
@@ -426,14 +404,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
     }
     if (tid == 0) before[0] = 0;
     __syncthreads();
-    if (blockIdx.x == 0)
-        for (int z = tid; z <= p.Z; z += kPagedThreads) p.before[z] = before[z];
-
     const int prefix = paged_prefix(p);
     const PagedPlan a = paged_plan(p, prefix);
     const int64_t total = a.own_first + static_cast<int64_t>(carry) * p.Hk * a.own_rt;
     const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);   // each has at least one tile
-    if (blockIdx.x >= blocks) return;
+    if (blockIdx.x >= blocks) {
+        grid_wait();
+        return;
+    }
     const int64_t t0 = total * blockIdx.x / blocks;
     const int count = static_cast<int>(total * (blockIdx.x + 1) / blocks - t0);
     PagedCursor now = paged_locate(p, a, before, t0);
@@ -442,30 +420,42 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            const int box = min(1 << p.page_shift, kPagedTile);
-            int page[kPagedTile / 16];
-            int keys = 0, issued = 0;
-            const int *table = nullptr;
-            for (int t = 0; t < count; ++t) {
-                if (t == 0 || now.tile == 0) {
-                    keys = keys_of(now);
-                    table = now.z < 0 ? p.prefix_table : p.page_table + static_cast<size_t>(now.z) * p.max_pages;
+        const int box = min(1 << p.page_shift, kPagedTile);
+        int page[kPagedTile / 16];
+        int keys = 0, issued = 0;
+        const int *table = nullptr;
+        for (int t = 0; t < count; ++t) {
+            if (t == 0 || now.tile == 0) {
+                keys = keys_of(now);
+                table = now.z < 0 ? p.prefix_table : p.page_table + static_cast<size_t>(now.z) * p.max_pages;
+                // the query rows that the consumers will want for this item, a line per lane
+                const int rows = now.z < 0 ? a.prefix_rows : a.own_rows;
+                for (int e = lane; e < rows * Lay::NSUB; e += 32) {
+                    const int64_t r = static_cast<int64_t>(now.rt) * rows + e / Lay::NSUB;
+                    const int64_t tok = r / p.group + (now.z < 0 ? 0 : static_cast<int64_t>(now.z) * p.L);
+                    if (tok < static_cast<int64_t>(p.Z) * p.L)
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                            p.q + (static_cast<size_t>(tok) * p.H + now.kvh * p.group + r % p.group) * D +
+                            64 * (e % Lay::NSUB)));
                 }
-                paged_numbers<kPagedTile>(p, table, now.tile, keys, box, page);
-                const int s = t % S;
-                if (t >= S && !mbar_wait(&empty[s], ((t / S) - 1) & 1, wctx)) break;
+            }
+            if (lane == 0) paged_numbers<kPagedTile>(p, table, now.tile, keys, box, page);
+            const int s = t % S;
+            if (t >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((t / S) - 1) & 1, wctx))) break;
+            if (lane == 0) {
                 uint8_t *st = smem + s * 2 * Lay::kOperand;
                 mbar_arrive_expect_tx(&full[s], 2 * Lay::kOperand);
                 paged_boxes<kPagedTile, Lay::NSUB>(p, &tmK, &full[s], st, now.tile, now.kvh, box, page);
                 paged_boxes<kPagedTile, Lay::NSUB>(p, &tmV, &full[s], st + Lay::kOperand, now.tile, now.kvh, box, page);
-                issued = t + 1;
-                if (issued < count) paged_next(p, a, before, now);
             }
-            // every issued load must land before the block's shared memory is released
-            for (int t = (issued > S ? issued - S : 0); t < issued; ++t)
-                mbar_wait_drain(&full[t % S], (t / S) & 1, p.timeout_ns);
+            __syncwarp();
+            issued = t + 1;
+            if (issued < count) paged_next(p, a, before, now);
         }
+        // every issued load must land before the block's shared memory is released
+        for (int t = (issued > S ? issued - S : 0); t < issued; ++t)
+            mbar_wait_drain(&full[t % S], (t / S) & 1, p.timeout_ns);
+        grid_wait();
         return;
     }
 
@@ -478,6 +468,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
         PagedItem<D, SCORE, WM> it;
         const PagedCursor c = now;
         const int keys = keys_of(c);
+        if (tid == 0 && c.tile == 0) p.blocks_of[c.item].x = blockIdx.x;
         it.begin(p, c, prefix);
         for (;;) {
             const int s = t % S;
@@ -498,11 +489,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
             it.tile(smem_u32(st), smem_u32(st + Lay::kOperand), now.tile * kPagedTile);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
+            if (tid == 0 && now.tile == now.tiles - 1) p.blocks_of[c.item].y = blockIdx.x;
             if (++t >= count) break;
             paged_next(p, a, before, now);
             if (now.item != c.item) break;
         }
-        it.end(red, p.part + (static_cast<size_t>(blockIdx.x) + c.item) * p.part_rows * D);
+        it.end(p.part + (static_cast<size_t>(blockIdx.x) + c.item) * kPagedPartRows * D);
     };
     while (t < count) {
         const int w = now.z < 0 ? p.prefix_warps : p.own_warps;
@@ -510,6 +502,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
         else if (w == 2) run.template operator()<2>();
         else run.template operator()<4>();
     }
+    // the join waits for this kernel alone: it has to end after the prefix kernel
+    grid_wait();
 }
 
 // ============================================================================
@@ -542,6 +536,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
     const int warp = warp_id(), lane = lane_id();
     const int split = blockIdx.x, pair = blockIdx.y, kvh = blockIdx.z;
+    grid_release();     // the tile kernel reads nothing of this one's
     const int prefix = paged_prefix(p);
     const int T = (prefix + 127) / 128, S = min(p.splits, T);
     if (split >= S) return;
@@ -725,21 +720,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
             if (ok) {
                 tc_fence_after();
-                constexpr int HALF = D / 2;
+                // fp32 rows through shared memory (the rings are idle: every load has landed
+                // and every MMA is done), so that whole sectors are written: this warp's 32
+                // rows of 64 columns, 16-byte chunks swizzled by row
+                constexpr int HALF = D / 2, CH = HALF / 4;
                 const uint32_t tO = tmem + lane_bits + (t ? Lay::COL_O1 : Lay::COL_O0) + c * HALF;
-                float4 *dst = reinterpret_cast<float4 *>(
-                    p.prefix_part +
-                    (((static_cast<size_t>(split) * p.Hk + kvh) * p.pairs + pair) * 256 + t * 128 + row) * D + c * HALF);
+                float4 *buf = reinterpret_cast<float4 *>(smem + Lay::OFF_K) + (warp - 4) * 32 * CH;
+                const unsigned there = __ballot_sync(0xffffffffu, live);
 #pragma unroll
                 for (int cc = 0; cc < HALF / 32; ++cc) {
                     uint32_t x[32];
                     tmem_ld32(tO + 32 * cc, x);
-                    if (live) {
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            dst[8 * cc + v] = make_float4(__uint_as_float(x[4 * v]), __uint_as_float(x[4 * v + 1]),
-                                                          __uint_as_float(x[4 * v + 2]), __uint_as_float(x[4 * v + 3]));
-                    }
+                    for (int v = 0; v < 8; ++v)
+                        buf[lane * CH + ((8 * cc + v) ^ (lane & 7))] =
+                            make_float4(__uint_as_float(x[4 * v]), __uint_as_float(x[4 * v + 1]),
+                                        __uint_as_float(x[4 * v + 2]), __uint_as_float(x[4 * v + 3]));
+                }
+                __syncwarp();
+                float *dst = p.prefix_part +
+                             (((static_cast<size_t>(split) * p.Hk + kvh) * p.pairs + pair) * 256 + t * 128 + quarter * 32) * D +
+                             c * HALF;
+#pragma unroll
+                for (int e = lane; e < 32 * CH; e += 32) {
+                    const int r = e / CH, ch = e % CH;
+                    if ((there >> r) & 1u) *reinterpret_cast<float4 *>(dst + r * D + 4 * ch) = buf[r * CH + (ch ^ (r & 7))];
                 }
             }
         }
@@ -753,71 +758,83 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
 }
 
-// Adds up the partials of each output row, prefix items first, in block order.
-// One warp per row.
-template <int D>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
-    constexpr int E = D / 32;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
-    if (r >= static_cast<int64_t>(p.Z) * p.L * p.H) return;
-    const int lane = lane_id();
-    const int h = static_cast<int>(r % p.H);
-    const int64_t tok = r / p.H;
-    const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
-    const int kvh = h / p.group, g = h % p.group;
+// Adds up the partials of each output row, prefix first, and rounds.  W warps
+// share a row, warp w taking every W-th partial, and their sums are added in warp
+// order; a block has 8 / W rows.
+constexpr int kJoinThreads = 256;
+template <int D, int W>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams p) {
+    constexpr int E = D / 32, R = 8 / W;
+    __shared__ float sums[W > 1 ? 8 : 1][W > 1 ? D : 1];
+    const unsigned rows = static_cast<unsigned>(p.Z) * p.L * p.H;      // below 2^31
+    const bool there = blockIdx.x * R + warp_id() / W < rows;
+    const unsigned r = there ? blockIdx.x * R + warp_id() / W : 0u;
+    const int lane = lane_id(), w = warp_id() % W;
+    const unsigned tok = r / p.H, h = r % p.H, z = tok / p.L, l = tok % p.L;
+    const unsigned kvh = h / p.group, g = h % p.group;
+    const unsigned own_row = l * p.group + g;
+    const unsigned own_rows = 16 * p.own_warps, prefix_rows = 16 * p.prefix_warps;
+    const unsigned own_item = p.prefix_rt * p.Hk + (z * p.Hk + kvh) * p.own_rt + own_row / own_rows;
+    const int2 n = paged_lengths(p, z);
+    const int prefix = paged_prefix(p);
+    const bool live = there && static_cast<int>(l) < n.y;
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    if (l < paged_lengths(p, z).y) {
-        const int prefix = paged_prefix(p);
-        const PagedPlan a = paged_plan(p, prefix);
-        const int64_t per = static_cast<int64_t>(p.Hk) * a.own_rt;
-        const int64_t total = a.own_first + p.before[p.Z] * per;
-        const int64_t blocks = min(static_cast<int64_t>(p.blocks), total);
-        auto sum = [&](const float *src, size_t step, int64_t count) {
+    int done = 0;     // partials before these
+    // `count` partials, `step` floats apart
+    auto sum = [&](const float *src, size_t step, int count) {
+        int b = (w - done) & (W - 1);
+        done += count;
 #pragma unroll 8
-            for (int64_t b = 0; b < count; ++b, src += step) {
-                if constexpr (E == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                    acc[0] += v.x;
-                    acc[1] += v.y;
-                    acc[2] += v.z;
-                    acc[3] += v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                    acc[0] += v.x;
-                    acc[1] += v.y;
-                }
+        for (; b < count; b += W) {
+            if constexpr (E == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + b * step));
+                acc[0] += v.x;
+                acc[1] += v.y;
+                acc[2] += v.z;
+                acc[3] += v.w;
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + b * step));
+                acc[0] += v.x;
+                acc[1] += v.y;
             }
-        };
-        // partials of the item with tiles [first, first + tiles), row `row` of it
-        auto add = [&](int64_t first, int tiles, int64_t item, int row) {
-            if (tiles == 0) return;
-            const int64_t b0 = ((first + 1) * blocks - 1) / total;
-            const int64_t b1 = ((first + tiles) * blocks - 1) / total;
-            sum(p.part + ((b0 + item) * p.part_rows + row) * D + lane * E, static_cast<size_t>(p.part_rows) * D,
-                b1 - b0 + 1);
-        };
+        }
+    };
+    // partials of row `row` of an item's `rows`: the warps along the keys lie `rows`
+    // rows apart, the blocks kPagedPartRows
+    auto add = [&](unsigned item, unsigned row, unsigned rows) {
+        const int2 b = __ldcg(&p.blocks_of[item]);
+        sum(p.part + (static_cast<size_t>(b.x + item) * kPagedPartRows + row) * D + lane * E,
+            static_cast<size_t>(rows) * D, (b.y - b.x + 1) * static_cast<int>(kPagedPartRows / rows));
+    };
+    grid_wait();
+    if (live) {
         if (p.splits > 0) {
             const int T = (prefix + 127) / 128, S = min(p.splits, T);
-            const int64_t tile = tok / p.tile_tokens;      // row tile
-            const int row = static_cast<int>(tok % p.tile_tokens) * p.group + g;
-            const float *src = p.prefix_part + ((kvh * p.pairs + tile / 2) * 256 + (tile & 1) * 128 + row) * D + lane * E;
-            sum(src, static_cast<size_t>(p.Hk) * p.pairs * 256 * D, S);
-        } else {
-            const int64_t row = tok * p.group + g;
-            const int64_t item = static_cast<int64_t>(kvh) * a.prefix_rt + row / a.prefix_rows;
-            add(item * a.prefix_tiles, a.prefix_tiles, item, static_cast<int>(row % a.prefix_rows));
+            const unsigned tile = tok / p.tile_tokens;      // row tile
+            const unsigned row = tok % p.tile_tokens * p.group + g;
+            sum(p.prefix_part + (static_cast<size_t>(kvh * p.pairs + tile / 2) * 256 + (tile & 1) * 128 + row) * D + lane * E,
+                static_cast<size_t>(p.Hk) * p.pairs * 256 * D, S);
+        } else if (prefix > 0) {
+            const unsigned row = tok * p.group + g;
+            add(kvh * p.prefix_rt + row / prefix_rows, row % prefix_rows, prefix_rows);
         }
-        {
-            const int row = l * p.group + g;
-            const int i = kvh * a.own_rt + row / a.own_rows;
-            const int tiles = p.before[z + 1] - p.before[z];
-            add(a.own_first + p.before[z] * per + static_cast<int64_t>(i) * tiles, tiles,
-                a.prefix_items + z * per + i, row % a.own_rows);
-        }
+        add(own_item, own_row % own_rows, own_rows);     // a live row has at least its own key
     }
-    __nv_bfloat16 *dst = p.o + r * D + lane * E;
+    if constexpr (W > 1) {
+        float *mine = sums[warp_id()] + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) mine[e] = acc[e];
+        __syncthreads();
+        if (w != 0) return;
+#pragma unroll
+        for (int u = 1; u < W; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += mine[u * D + e];
+    }
+    if (!there) return;
+    __nv_bfloat16 *dst = p.o + static_cast<size_t>(r) * D + lane * E;
     if constexpr (E == 4)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     else
