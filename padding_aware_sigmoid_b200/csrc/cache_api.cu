@@ -48,7 +48,7 @@ constexpr int kPagedMostBlocks = 3 * kPagedMostSms;  // of the tile kernel
 
 // Rows (over the batch, per key head) from which the prefix kernel takes the
 // prefix.
-constexpr int64_t kPrefixKernelRows = 32;
+constexpr int64_t kPrefixKernelRows = 64;
 
 struct PagedSizes {
     int prefix_warps, own_warps;
@@ -115,8 +115,8 @@ sigattn_status prefix_launch(const PagedMaps &m, const PagedParams &p, cudaStrea
                   FwdLayout<D, KS, VS>::SMEM_ALLOC, st, m.prefix_q, m.prefix_k, m.prefix_v, p);
 }
 #ifndef PAGED_W8
-#define PAGED_W8 512
-#define PAGED_W4 4096
+#define PAGED_W8 2048
+#define PAGED_W4 8192
 #define PAGED_W2 16384
 #endif
 template <int D, int SCORE>

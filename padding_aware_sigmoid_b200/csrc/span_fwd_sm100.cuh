@@ -37,9 +37,22 @@ struct SpanFwdParams {
 template <int D>
 struct SpanFwdLayout : FwdLayout<D, FwdStages<D>::K, FwdStages<D>::V> {
     using Base = FwdLayout<D, FwdStages<D>::K, FwdStages<D>::V>;
-    static constexpr int OFF_HULL = (Base::OFF_SAMPLE + 7) & ~7;   // 8 warps x {lo, hi}
+    static constexpr int OFF_HALF = (Base::OFF_SAMPLE + 7) & ~7;   // barriers per (part, tile): S ready, P ready
+    static constexpr int OFF_HULL = OFF_HALF + 8 * 8;              // 8 warps x {lo, hi}
     static constexpr int SMEM_ALLOC = OFF_HULL + 64 + 1024;
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+};
+
+// Parts that a 128-key tile's scores are handed over in.  Two halves let a sigma
+// warpgroup start as soon as its own 64 keys are there, and its scores of the
+// next tile be computed while the other warpgroup still works; but an N = 64
+// score MMA runs at 2/3 of the N = 128 rate (shared-memory reads).  That pays
+// where the MUFU is the bound: D = 64 packed documents 63.2 -> 59.8 us, D = 128
+// with a cap 224.7 -> 213.7 us, but causal L = 16384 at D = 128 without one 1066 ->
+// 1211 us.
+template <int D, int SCORE>
+struct SpanParts {
+    static constexpr int N = D == 64 || (SCORE & kScoreCap) ? 2 : 1;
 };
 
 template <int D, int MODE, int SCORE>
@@ -47,6 +60,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     span_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const SpanFwdParams p) {
     constexpr int KS = FwdStages<D>::K, VS = FwdStages<D>::V;
+    constexpr int NP = SpanParts<D, SCORE>::N, PK = 128 / NP;   // parts of a key tile, keys of a part
     using Lay = SpanFwdLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1k(smem_raw);
@@ -56,9 +70,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t *k_empty = k_full + KS;
     uint64_t *v_full = k_empty + KS;
     uint64_t *v_empty = v_full + VS;
-    uint64_t *s_full = v_empty + VS;
-    uint64_t *p_full = s_full + 2;
-    uint64_t *drain = p_full + 2;
+    uint64_t *drain = v_empty + VS;
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + Lay::OFF_HALF);   // [part][tile]
+    uint64_t *p_full = s_full + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
     int2 *hull = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
@@ -84,9 +98,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], 1);
         }
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 256);  // the two sigma warpgroups of tile t
+        for (int u = 0; u < 2 * NP; ++u) {
+            mbar_init(&s_full[u], 1);
+            mbar_init(&p_full[u], 256 / NP);  // the sigma warpgroups of this tile and part
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -188,42 +202,44 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         auto wt = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, wctx));
         };
-        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_s = idesc_bf16_f32(128, PK, false, false);
         const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
         const uint32_t sQ = smem_u32(smem + Lay::OFF_Q);
         const uint32_t sK = smem_u32(smem + Lay::OFF_K);
         const uint32_t sV = smem_u32(smem + Lay::OFF_V);
         constexpr uint32_t kDescHi = desc_hi(1024);
-        auto issue_s = [&](int t, uint32_t kbase) {
-            const uint32_t q_lo = desc_lo(sQ + t * Lay::TILE_BYTES, 16), k_lo = desc_lo(kbase, 16);
-            const uint32_t d_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0);
+        // scores of query tile t against part c of the key tile at kbase
+        auto issue_s = [&](int t, int c, uint32_t kbase) {
+            const uint32_t q_lo = desc_lo(sQ + t * Lay::TILE_BYTES, 16), k_lo = desc_lo(kbase + c * PK * 128, 16);
+            const uint32_t d_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0) + PK * c;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t koff = ((kk >> 2) * Lay::SUB_BYTES + (kk & 3) * 32) >> 4;
                 mma_ss_lhw(d_tmem, q_lo + koff, k_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
             }
-            mma_commit_w(&s_full[t]);
+            mma_commit_w(&s_full[2 * c + t]);
         };
-        auto issue_pv = [&](int t, uint32_t vbase, bool first) {
+        auto issue_pv = [&](int t, int c, uint32_t vbase, bool first) {
             const uint32_t d_tmem = tmem + (t ? Lay::COL_O1 : Lay::COL_O0);
             const uint32_t a_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0);
             const uint32_t v_lo = desc_lo(vbase, Lay::SUB_BYTES);
+            // 16 keys = 8 packed columns per step; keys 64-127 sit 32 columns further on
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
+            for (int kk = c * PK / 16; kk < (c + 1) * PK / 16; ++kk)
                 mma_ts_lhw(d_tmem, a_tmem + kk * 8 + (kk >= 4 ? 32 : 0), v_lo + kk * ((16 * 128) >> 4), kDescHi,
                            idesc_o, (!first || kk > 0) ? 1u : 0u);
         };
-        // Per key tile j: for each query tile that visits j, O_t += P_t V_j once
-        // its P is there, then S_t of j + 1 over it.  MMAs from one thread
-        // run in issue order, so P_t has been read before the next scores are
-        // written.  A key tile that neither visits (a gap between the two hulls)
-        // passes through the rings unread.
+        // Per key tile j and part c: for each query tile that visits j, O_t += P V
+        // over the part's keys once its P is there, then the same part's scores of
+        // j + 1 over it.  MMAs from one thread run in issue order, so P has been
+        // read before the next scores are written.  A key tile that neither visits
+        // (a gap between the two hulls) passes through the rings unread.
         bool ok = wt(q_full, 0) && wt(&k_full[0], 0);
         if (ok) {
             tc_fence_after();
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (j0[t] == J0 && J0 < j1[t]) issue_s(t, sK);
+            for (int u = 0; u < 2 * NP; ++u)
+                if (j0[u & 1] == J0 && J0 < j1[u & 1]) issue_s(u & 1, u >> 1, sK);
             mma_commit_w(&k_empty[0]);
         }
         for (int r = 0; ok && r < steps; ++r) {
@@ -236,18 +252,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_V + sv * Lay::TILE_BYTES, n & 127);
             bool have_k = false;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int u = 0; u < 2 * NP; ++u) {
+                const int t = u & 1, c = u >> 1;
                 if (j >= j0[t] && j < j1[t]) {
-                    if (!(ok = wt(&p_full[t], (j - j0[t]) & 1))) break;
+                    if (!(ok = wt(&p_full[u], (j - j0[t]) & 1))) break;
                     tc_fence_after();
-                    issue_pv(t, vbase, j == j0[t]);
+                    issue_pv(t, c, vbase, j == j0[t] && c == 0);
                 }
-                if (t == 1) mma_commit_w(&v_empty[sv]);
+                if (u == 2 * NP - 1) mma_commit_w(&v_empty[sv]);
                 if (more && j + 1 >= j0[t] && j + 1 < j1[t]) {
                     if (!have_k && !(ok = wt(&k_full[sk], ((r + 1) / KS) & 1))) break;
                     have_k = true;
                     tc_fence_after();
-                    issue_s(t, knext);
+                    issue_s(t, c, knext);
                 }
             }
             if (!ok) break;
@@ -265,6 +282,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // [64 c, 64 c + 64) of each key tile, c = g % 2
         const int g = (warp - 4) >> 2;
         const int t = g >> 1, c = g & 1;
+        const int part = 2 * (c * NP / 2) + t;   // barriers of this tile and part
         const int quarter = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
         const int row = (qtile0 + t) * 128 + quarter * 32 + lane;
@@ -277,7 +295,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const uint32_t tS = tmem + lane_bits + (t ? Lay::COL_S1 : Lay::COL_S0) + 64 * c;
             int pause = tail_pause(cf);
             for (int j = ja; j < jb; ++j) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (j - ja) & 1, wctx));
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[part], (j - ja) & 1, wctx));
                 if (!ok) break;
                 tc_fence_after();
                 const int key0 = j * 128 + 64 * c;   // first key of this half
@@ -297,7 +315,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&p_full[t]);
+                mbar_arrive(&p_full[part]);
             }
             // every MMA of this CTA has finished once the MMA warp's final commit lands
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
