@@ -65,6 +65,15 @@ SpanF32Params f32_params(const SpanArgs &a, int *status) {
     return p;
 }
 
+// Whether a kernel's blocks start tile by tile over all heads of a sample (the
+// tiles with the most work first) instead of head by head: when what they stream
+// (`tensors` of them, per key head) fits L2 with room to spare, so that nothing
+// is read twice from memory.
+constexpr int64_t kStreamMost = int64_t(64) << 20;
+bool heads_first(const SpanArgs &a, int tensors, int64_t tiles) {
+    return tiles <= 65535 && static_cast<int64_t>(tensors) * a.Z * a.L * a.Hk * a.D * 2 <= kStreamMost;
+}
+
 dim3 f32_grid(int64_t rows) { return dim3(static_cast<unsigned>((rows + 7) / 8)); }
 
 // The device's state, for a dtype the device can run.
@@ -188,8 +197,9 @@ sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, voi
     p.bias_z = bias_z;
     p.slopes = slopes;
     p.timeout_ns = g_timeout_ns.load();
-    const dim3 grid(static_cast<unsigned>((tiles_of(L) + 1) / 2), H, Z);
-    return launch_span_fwd(kind_of(a), grid, mq, mk, mv, p, st);
+    const unsigned pairs = static_cast<unsigned>((tiles_of(L) + 1) / 2);
+    p.heads_first = heads_first(a, 2, pairs);
+    return launch_span_fwd(kind_of(a), p.heads_first ? dim3(H, pairs, Z) : dim3(pairs, H, Z), mq, mk, mv, p, st);
 }
 
 size_t sigattn_bwd_span_workspace_bytes(int Z, int L, sigattn_dtype dtype) {
@@ -254,8 +264,11 @@ sigattn_status sigattn_bwd_span(const void *q, const void *k, const void *v, con
     p.hull = hull;
     p.timeout_ns = g_timeout_ns.load();
     if ((s = launch(span_prep_kernel, dim3(tiles, Z), dim3(128), 0, st, p.src, clean, hull)) != SIGATTN_OK) return s;
-    if ((s = launch_span_dq(kind_of(a), dim3(tiles, H, Z), mq, mk, mv, mdo, p, st)) != SIGATTN_OK) return s;
-    return launch_span_dkdv(kind_of(a), dim3(tiles, Hk, Z), mq, mk, mv, mdo, p, st);
+    p.heads_first = heads_first(a, 2, tiles);
+    s = launch_span_dq(kind_of(a), p.heads_first ? dim3(H, tiles, Z) : dim3(tiles, H, Z), mq, mk, mv, mdo, p, st);
+    if (s != SIGATTN_OK) return s;
+    p.heads_first = heads_first(a, 2 * p.group, tiles);
+    return launch_span_dkdv(kind_of(a), p.heads_first ? dim3(Hk, tiles, Z) : dim3(tiles, Hk, Z), mq, mk, mv, mdo, p, st);
 }
 
 sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix, const int32_t *docs, int causal,

@@ -27,6 +27,7 @@ struct SpanBwdParams {
     __nv_bfloat16 *dq, *dk, *dv;
     SpanSource src;
     int H, Hk, group;
+    int heads_first;       // grid (heads, tiles, samples) instead of (tiles, heads, samples)
     float alpha, bias, cap;
     const float *bias_z, *slopes;
     const int2 *clean;     // [Z][tiles * 128] clipped spans (span_prep_kernel)
@@ -83,13 +84,30 @@ __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_
     using SG = BwdSigma<D>;
     if (!__all_sync(0xffffffffu, mbar_wait(s_full, s_par, wctx))) return false;
     tc_fence_after();
+    const int first = key0 + SG::kCols * w;    // this warpgroup's first key
+    const bool whole = __all_sync(0xffffffffu, span.x <= first && span.y >= first + SG::kCols);
+    const bool some = whole || __any_sync(0xffffffffu, span.x < first + SG::kCols && span.y > first);
+    constexpr int kChunks = SG::kCols / 32;
+    if (!some) {
+        // none of the warp's rows sees any of these keys: dS = 0 without a score
+        tc_fence_before();
+        mbar_arrive(s_free);
+        if (!__all_sync(0xffffffffu, mbar_wait(dp_full, dp_par, wctx))) return false;
+        tc_fence_after();
+        uint32_t zero[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero[i] = 0u;
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) tmem_st16(trow + dcol + SG::kCols * w + 16 * ch, zero);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
+        return true;
+    }
     uint32_t r[SG::kCols];
     tmem_ld_cols(trow + col_s + SG::kCols * w, r);
     tc_fence_before();
     mbar_arrive(s_free);
-    const int first = key0 + SG::kCols * w;    // this warpgroup's first key
-    const bool whole = __all_sync(0xffffffffu, span.x <= first && span.y >= first + SG::kCols);
-    constexpr int kChunks = SG::kCols / 32;
     float2 g[16];
     auto gains = [&](int ch) {
         uint32_t unused[16];
@@ -122,7 +140,7 @@ __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_
 // dkdv_sigma_tile (bwd_sm100.cuh) with the masked score function: one query
 // tile of a dK/dV sigma warpgroup, whose columns are the queries from q_first
 // on.  `key` is this thread's key; `whole`: every row of the tile sees every
-// key of this CTA's tile; otherwise `clean` points at the spans of the columns.
+// key of this CTA's tile; otherwise `clean` points at the spans of the columns (lane i reads column i).
 template <int D, int MODE, int SCORE>
 __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_t *s_full, uint64_t *s_free,
                                                uint64_t *dp_full, uint64_t *p_ready, uint64_t *ds_ready,
@@ -133,19 +151,34 @@ __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_
     float2 g[SG::kPacked];
     uint32_t pk[SG::kPacked];
     uint32_t bits[W];
+    bool some = true;
     if (!whole) {
-        // two columns' spans per load, the same address in every lane
-        const int4 *pair = reinterpret_cast<const int4 *>(clean);
+        // lane i takes column i: the keys of this warp that it sees, as bits, turned
+        // round so that each key has its columns
+        const int key0 = key - static_cast<int>(threadIdx.x & 31);
+        some = false;
 #pragma unroll
         for (int u = 0; u < W; ++u) {
-            bits[u] = 0u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int4 s = __ldg(pair + 16 * u + i);
-                if (static_cast<unsigned>(key - s.x) < static_cast<unsigned>(s.y - s.x)) bits[u] |= 1u << (2 * i);
-                if (static_cast<unsigned>(key - s.z) < static_cast<unsigned>(s.w - s.z)) bits[u] |= 2u << (2 * i);
-            }
+            const int2 s = __ldg(clean + 32 * u + (threadIdx.x & 31));
+            bits[u] = warp_transpose(bit_range(s.x - key0, s.y - key0));
+            some |= __any_sync(0xffffffffu, bits[u] != 0u);
         }
+    }
+    if (!some) {
+        // no query of these columns sees a key of this warp: P^T = dS^T = 0
+        if (!__all_sync(0xffffffffu, mbar_wait(s_full, par, wctx))) return false;
+        mbar_arrive(s_free);
+        if (!__all_sync(0xffffffffu, mbar_wait(dp_full, par, wctx))) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < SG::kPacked; ++i) pk[i] = 0u;
+        tmem_st_cols(tD, pk);
+        tmem_st_cols(tD + SG::kPacked, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_ready);
+        mbar_arrive(ds_ready);
+        return true;
     }
     if (!__all_sync(0xffffffffu, mbar_wait(s_full, par, wctx))) return false;
     tc_fence_after();
@@ -247,11 +280,13 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
 
     const int warp = warp_id(), lane = lane_id();
-    const int z = blockIdx.z, h = blockIdx.y, kvh = h / p.group;
-    const int qtile = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), h = p.heads_first ? blockIdx.x : blockIdx.y;
+    const int kvh = h / p.group;
+    const int tiles = p.heads_first ? gridDim.y : gridDim.x;
+    const int qtile = tiles - 1 - static_cast<int>(p.heads_first ? blockIdx.y : blockIdx.x);
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
-    const int4 hull = p.hull[static_cast<size_t>(z) * gridDim.x + qtile];
+    const int4 hull = p.hull[static_cast<size_t>(z) * tiles + qtile];
     if (hull.y == 0) {
         // no row of this tile sees a key: zeros, written by every thread
         zero_rows<D>(p.dq, z, h, qtile * 128, min(128, L - qtile * 128), L, p.H);
@@ -452,8 +487,10 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
     int2 *met = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
 
     const int warp = warp_id(), lane = lane_id();
-    const int z = blockIdx.z, kvh = blockIdx.y, ktile = blockIdx.x;
-    const int L = p.src.L, tiles = gridDim.x;
+    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), kvh = p.heads_first ? blockIdx.x : blockIdx.y;
+    const int tiles = p.heads_first ? gridDim.y : gridDim.x;
+    const int ktile = p.heads_first ? blockIdx.y : blockIdx.x;
+    const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     const int k0 = ktile * 128, k1 = min(k0 + 128, n);
     // first and last query tile whose hull meets this key tile

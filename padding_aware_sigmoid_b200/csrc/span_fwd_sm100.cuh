@@ -6,11 +6,14 @@
 //    its rows' hull only, [j0_t, j1_t), and the rings stream the union of the
 //    two.  A pair of causal tiles so costs its visible tiles plus half a
 //    diagonal tile each, and packed documents cost what their own keys cost;
-//  - pairs are started from the last rows on: with causal spans those see the
-//    most keys, and the short ones fill in behind them;
+//  - long samples start first, and of a sample the last rows, which see the
+//    most keys under causal spans: the short blocks fill in behind.  Where all
+//    keys and values fit L2 this goes over all heads of a sample at once;
+//    otherwise head by head, so that the blocks running at one time share theirs;
 //  - query head h reads key head h / (H / Hk);
 //  - a warp masks a 64-key half only where one of its rows does not see all of
-//    it (the rows' bounds are in registers; whole tiles pay one vote);
+//    it, and writes zeros without a score where none sees any (the rows' bounds
+//    are in registers; whole tiles pay two votes);
 //  - the MMA warp zeroes the value rows at or beyond n of the last key tile
 //    while the sigma warps work on its scores, so that NaN in padding never
 //    meets the product.
@@ -31,6 +34,7 @@ struct SpanFwdParams {
     float alpha, bias, cap;
     const float *bias_z;   // device float[Z] or null
     const float *slopes;   // device float[H] or null
+    int heads_first;       // grid (heads, pairs, samples) instead of (pairs, heads, samples)
     uint64_t timeout_ns;
 };
 
@@ -78,8 +82,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     int2 *hull = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
 
     const int warp = warp_id(), lane = lane_id();
-    const int z = blockIdx.z, h = blockIdx.y, kvh = h / p.group;
-    const int qtile0 = static_cast<int>(gridDim.x - 1 - blockIdx.x) * 2;
+    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), h = p.heads_first ? blockIdx.x : blockIdx.y;
+    const int kvh = h / p.group;
+    const int qtile0 = 2 * static_cast<int>(p.heads_first ? gridDim.y - 1 - blockIdx.y : gridDim.x - 1 - blockIdx.x);
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     if (warp < 8) {
@@ -300,17 +305,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 tc_fence_after();
                 const int key0 = j * 128 + 64 * c;   // first key of this half
                 const bool whole = __all_sync(0xffffffffu, span.x <= key0 && span.y >= key0 + 64);
+                const bool some = whole || __any_sync(0xffffffffu, span.x < key0 + 64 && span.y > key0);
                 // two chunks of 32 scores per thread; P of chunk u lies over S
                 // columns [16 u, 16 u + 16) of this half, already read
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    uint32_t r[32];
-                    tmem_ld32(tS + 32 * u, r);
                     uint32_t pk[16];
-                    const float rel = static_cast<float>(row - key0 - 32 * u);
-                    score_chunk<MODE, SCORE, false>(r, cf, rel, pk, nullptr, pause);
-                    if (!whole)
-                        keep_bits(pk, bit_range(span.x - key0 - 32 * u, span.y - key0 - 32 * u));
+                    if (some) {
+                        uint32_t r[32];
+                        tmem_ld32(tS + 32 * u, r);
+                        score_chunk<MODE, SCORE, false>(r, cf, static_cast<float>(row - key0 - 32 * u), pk, nullptr,
+                                                        pause);
+                        if (!whole) keep_bits(pk, bit_range(span.x - key0 - 32 * u, span.y - key0 - 32 * u));
+                    } else {
+                        // none of the warp's rows sees any of the half
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                    }
                     tmem_st16(tS + 16 * u, pk);
                 }
                 tmem_wait_st();

@@ -190,6 +190,25 @@ __device__ __forceinline__ int span_tokens(const SpanSource &s, int z) {
     return n;
 }
 
+// The sample of grid position r: samples start by decreasing length (ranks_before,
+// up to kMaxRankedSamples of them; above that in index order).  Every warp finds it
+// by itself.
+__device__ __forceinline__ int span_sample(const int *seqlens, int Z, int r) {
+    if (Z > kMaxRankedSamples || Z == 1) return r;
+    const int lane = threadIdx.x & 31;
+    int w[2], rank[2] = {0, 0};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) w[c] = lane + 32 * c < Z ? seqlens[lane + 32 * c] : 0;
+    for (int j = 0; j < Z; ++j) {
+        const int wj = __shfl_sync(0xffffffffu, j < 32 ? w[0] : w[1], j & 31);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) rank[c] += ranks_before(wj, j, w[c], lane + 32 * c);
+    }
+    const unsigned a = __ballot_sync(0xffffffffu, lane < Z && rank[0] == r);
+    const unsigned b = __ballot_sync(0xffffffffu, lane + 32 < Z && rank[1] == r);
+    return a != 0 ? __ffs(a) - 1 : 31 + __ffs(b);
+}
+
 // Keys that row i of sample z (n tokens) sees; (0, 0) when there are none.
 __device__ __forceinline__ int2 row_span(const SpanSource &s, int z, int i, int n) {
     if (i >= n) return make_int2(0, 0);
@@ -209,16 +228,36 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
     return below_b & ~below_a;
 }
 
-// Keeps the packed bf16 pairs (columns 2 i, 2 i + 1) whose bit is set.
-template <int N>
-__device__ __forceinline__ void keep_bits(uint32_t (&pk)[N], uint32_t bits) {
-    static_assert(N <= 16, "one word of bits");
+// Keeps the packed bf16 pairs (columns 2 i, 2 i + 1) whose bit is set.  Bit k of
+// the word is the sign bit of a byte of bits << (7 - k % 8), and PRMT can spread
+// the sign of a byte: one PRMT makes a pair's mask out of two of the eight
+// shifted words, 39 instructions a chunk where selects by bit take about 110.
+__device__ __forceinline__ void keep_bits(uint32_t (&pk)[16], uint32_t bits) {
+    uint32_t t[8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint32_t lo = (bits >> (2 * i)) & 1u ? 0x0000FFFFu : 0u;
-        const uint32_t hi = (bits >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u;
-        pk[i] &= lo | hi;
+    for (int k = 0; k < 8; ++k) t[k] = bits << k;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int byte = i / 4, k = (2 * i) % 8;
+        // low half: sign of `byte` of the first word, high half: of the second
+        const uint32_t sel = (8u | byte) * 0x11u | (8u | 4u | byte) * 0x1100u;
+        uint32_t m;
+        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m) : "r"(t[7 - k]), "r"(t[6 - k]), "r"(sel));
+        pk[i] &= m;
     }
+}
+
+// Bit i of lane j's word against bit j of lane i's: the 32 x 32 bits of a warp
+// transposed.
+__device__ __forceinline__ uint32_t warp_transpose(uint32_t x) {
+    const int lane = threadIdx.x & 31;
+    uint32_t m = 0x0000FFFFu;
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1, m ^= m << j) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+        x = lane & j ? (x & ~m) | ((y & ~m) >> j) : (x & m) | ((y & m) << j);
+    }
+    return x;
 }
 
 // Zeroes rows [r0, 128) of a [128][64 NSUB] bf16 operand tile in shared memory
