@@ -197,7 +197,8 @@ sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, voi
     p.bias_z = bias_z;
     p.slopes = slopes;
     p.timeout_ns = g_timeout_ns.load();
-    const unsigned pairs = static_cast<unsigned>((tiles_of(L) + 1) / 2);
+    const int per = D == 64 ? SpanTiles<64>::N : SpanTiles<128>::N;
+    const unsigned pairs = static_cast<unsigned>((tiles_of(L) + per - 1) / per);
     p.heads_first = heads_first(a, 2, pairs);
     return launch_span_fwd(kind_of(a), p.heads_first ? dim3(H, pairs, Z) : dim3(pairs, H, Z), mq, mk, mv, p, st);
 }

@@ -38,13 +38,35 @@ struct SpanFwdParams {
     uint64_t timeout_ns;
 };
 
+// Query tiles of one CTA, and CTAs that share an SM.
 template <int D>
-struct SpanFwdLayout : FwdLayout<D, FwdStages<D>::K, FwdStages<D>::V> {
-    using Base = FwdLayout<D, FwdStages<D>::K, FwdStages<D>::V>;
-    static constexpr int OFF_HALF = (Base::OFF_SAMPLE + 7) & ~7;   // barriers per (part, tile): S ready, P ready
-    static constexpr int OFF_HULL = OFF_HALF + 8 * 8;              // 8 warps x {lo, hi}
-    static constexpr int SMEM_ALLOC = OFF_HULL + 64 + 1024;
-    static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+struct SpanTiles {
+    static constexpr int N = D == 64 ? 1 : 2, kPerSm = 2 / N;
+    static constexpr int kThreads = 128 + 256 * N;
+    static constexpr int KS = D == 64 ? 2 : FwdStages<D>::K, VS = D == 64 ? 3 : FwdStages<D>::V;
+};
+
+template <int D>
+struct SpanFwdLayout {
+    static constexpr int NT = SpanTiles<D>::N, KS = SpanTiles<D>::KS, VS = SpanTiles<D>::VS;
+    static constexpr int NSUB = D / 64;
+    static constexpr int SUB_BYTES = 128 * 64 * 2;
+    static constexpr int TILE_BYTES = NSUB * SUB_BYTES;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + NT * TILE_BYTES;
+    static constexpr int OFF_V = OFF_K + KS * TILE_BYTES;
+    static constexpr int OFF_BAR = OFF_V + VS * TILE_BYTES;
+    // q_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], drain, then per
+    // (part, tile): S ready, P ready
+    static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 4 * NT;
+    static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+    static constexpr int OFF_ABORT = OFF_TMEM + 8;
+    static constexpr int OFF_HULL = OFF_ABORT + 8;                 // {lo, hi} of each 32 rows
+    static constexpr int SMEM_ALLOC = OFF_HULL + 32 * NT + 1024;
+    static constexpr uint32_t COL_S = 0, COL_O = 128 * NT;         // S_t, then O_t
+    static constexpr uint32_t TMEM_COLS = NT * (128 + D) > 256 ? 512 : 256;
+    static_assert(NT * (128 + D) <= TMEM_COLS && SpanTiles<D>::kPerSm * TMEM_COLS <= 512, "TMEM budget");
+    static_assert(SpanTiles<D>::kPerSm * (SMEM_ALLOC + 1024) <= 228 * 1024, "shared memory budget");
 };
 
 // Parts that a 128-key tile's scores are handed over in.  Two halves let a sigma
@@ -60,12 +82,13 @@ struct SpanParts {
 };
 
 template <int D, int MODE, int SCORE>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
     span_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const SpanFwdParams p) {
-    constexpr int KS = FwdStages<D>::K, VS = FwdStages<D>::V;
-    constexpr int NP = SpanParts<D, SCORE>::N, PK = 128 / NP;   // parts of a key tile, keys of a part
     using Lay = SpanFwdLayout<D>;
+    constexpr int NT = Lay::NT, KS = Lay::KS, VS = Lay::VS;
+    constexpr int NP = SpanParts<D, SCORE>::N, PK = 128 / NP;   // parts of a key tile, keys of a part
+    constexpr int kThreads = SpanTiles<D>::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1k(smem_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
@@ -75,8 +98,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t *v_full = k_empty + KS;
     uint64_t *v_empty = v_full + VS;
     uint64_t *drain = v_empty + VS;
-    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + Lay::OFF_HALF);   // [part][tile]
-    uint64_t *p_full = s_full + 4;
+    uint64_t *s_full = drain + 1;              // [part][tile]
+    uint64_t *p_full = s_full + 2 * NT;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
     int2 *hull = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
@@ -84,10 +107,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int warp = warp_id(), lane = lane_id();
     const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), h = p.heads_first ? blockIdx.x : blockIdx.y;
     const int kvh = h / p.group;
-    const int qtile0 = 2 * static_cast<int>(p.heads_first ? gridDim.y - 1 - blockIdx.y : gridDim.x - 1 - blockIdx.x);
+    const int qtile0 = NT * static_cast<int>(p.heads_first ? gridDim.y - 1 - blockIdx.y : gridDim.x - 1 - blockIdx.x);
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
-    if (warp < 8) {
+    if (warp < 4 * NT) {
         const int2 r = row_span(p.src, z, qtile0 * 128 + static_cast<int>(threadIdx.x), n);
         const int lo = __reduce_min_sync(0xffffffffu, r.x < r.y ? r.x : INT_MAX);
         const int hi = __reduce_max_sync(0xffffffffu, r.y);
@@ -103,7 +126,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], 1);
         }
-        for (int u = 0; u < 2 * NP; ++u) {
+        for (int u = 0; u < NT * NP; ++u) {
             mbar_init(&s_full[u], 1);
             mbar_init(&p_full[u], 256 / NP);  // the sigma warpgroups of this tile and part
         }
@@ -112,10 +135,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         fence_barrier_init();
     }
     __syncthreads();
-    // key tiles [j0[t], j1[t]) of query tile t; an empty tile has j0 = j1 = 0
-    int j0[2], j1[2];
+    // key tiles [j0[t], j1[t]) of query tile t, and [J0, J1) of all; an empty tile
+    // has j0 = j1 = 0
+    int j0[NT], j1[NT], J0 = INT_MAX, J1 = 0, live = 0;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NT; ++t) {
         int lo = INT_MAX, hi = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -125,22 +149,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         j0[t] = hi > 0 ? lo / 128 : 0;
         j1[t] = (hi + 127) / 128;
+        if (hi > 0) {
+            J0 = min(J0, j0[t]);
+            J1 = max(J1, j1[t]);
+            ++live;
+        }
     }
-    const bool live0 = j1[0] > 0, live1 = j1[1] > 0;
     const size_t row_stride = static_cast<size_t>(p.H) * D;
-    if (!live0 && !live1) {
+    if (live == 0) {
         // no row sees a key: zeros, written by every thread
-        const int r0 = qtile0 * 128, rows = min(256, L - r0);
+        const int r0 = qtile0 * 128, rows = min(128 * NT, L - r0);
         constexpr int V4 = D / 8;
-        for (int e = threadIdx.x; e < rows * V4; e += kFwdThreads) {
+        for (int e = threadIdx.x; e < rows * V4; e += kThreads) {
             uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<size_t>(z) * L + r0 + e / V4) * row_stride +
                                                    static_cast<size_t>(h) * D);
             dst[e % V4] = make_uint4(0u, 0u, 0u, 0u);
         }
         return;
     }
-    const int J0 = live0 ? (live1 ? min(j0[0], j0[1]) : j0[0]) : j0[1];
-    const int J1 = max(j1[0], j1[1]);
     const int steps = J1 - J0;
     // the last key tile, when n ends inside it: its value rows are cleaned
     const bool ragged = (n & 127) != 0 && J1 == (n + 127) / 128;
@@ -163,10 +189,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (lane == 0) {
             uint8_t *sQ = smem + Lay::OFF_Q;
             uint8_t *sK = smem + Lay::OFF_K;
-            mbar_arrive_expect_tx(q_full, (live0 + live1) * Lay::TILE_BYTES);
+            mbar_arrive_expect_tx(q_full, live * Lay::TILE_BYTES);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (!(t ? live1 : live0)) continue;
+            for (int t = 0; t < NT; ++t) {
+                if (j1[t] == 0) continue;
                 for (int s = 0; s < Lay::NSUB; ++s)
                     tma_load_4d(&tmQ, q_full, sQ + t * Lay::TILE_BYTES + s * Lay::SUB_BYTES, 64 * s, h,
                                 (qtile0 + t) * 128, z);
@@ -216,17 +242,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // scores of query tile t against part c of the key tile at kbase
         auto issue_s = [&](int t, int c, uint32_t kbase) {
             const uint32_t q_lo = desc_lo(sQ + t * Lay::TILE_BYTES, 16), k_lo = desc_lo(kbase + c * PK * 128, 16);
-            const uint32_t d_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0) + PK * c;
+            const uint32_t d_tmem = tmem + Lay::COL_S + 128 * t + PK * c;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t koff = ((kk >> 2) * Lay::SUB_BYTES + (kk & 3) * 32) >> 4;
                 mma_ss_lhw(d_tmem, q_lo + koff, k_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
             }
-            mma_commit_w(&s_full[2 * c + t]);
+            mma_commit_w(&s_full[NT * c + t]);
         };
         auto issue_pv = [&](int t, int c, uint32_t vbase, bool first) {
-            const uint32_t d_tmem = tmem + (t ? Lay::COL_O1 : Lay::COL_O0);
-            const uint32_t a_tmem = tmem + (t ? Lay::COL_S1 : Lay::COL_S0);
+            const uint32_t d_tmem = tmem + Lay::COL_O + D * t;
+            const uint32_t a_tmem = tmem + Lay::COL_S + 128 * t;
             const uint32_t v_lo = desc_lo(vbase, Lay::SUB_BYTES);
             // 16 keys = 8 packed columns per step; keys 64-127 sit 32 columns further on
 #pragma unroll
@@ -243,8 +269,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (ok) {
             tc_fence_after();
 #pragma unroll
-            for (int u = 0; u < 2 * NP; ++u)
-                if (j0[u & 1] == J0 && J0 < j1[u & 1]) issue_s(u & 1, u >> 1, sK);
+            for (int u = 0; u < NT * NP; ++u)
+                if (j0[u % NT] == J0 && J0 < j1[u % NT]) issue_s(u % NT, u / NT, sK);
             mma_commit_w(&k_empty[0]);
         }
         for (int r = 0; ok && r < steps; ++r) {
@@ -257,14 +283,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_V + sv * Lay::TILE_BYTES, n & 127);
             bool have_k = false;
 #pragma unroll
-            for (int u = 0; u < 2 * NP; ++u) {
-                const int t = u & 1, c = u >> 1;
+            for (int u = 0; u < NT * NP; ++u) {
+                const int t = u % NT, c = u / NT;
                 if (j >= j0[t] && j < j1[t]) {
                     if (!(ok = wt(&p_full[u], (j - j0[t]) & 1))) break;
                     tc_fence_after();
                     issue_pv(t, c, vbase, j == j0[t] && c == 0);
                 }
-                if (u == 2 * NP - 1) mma_commit_w(&v_empty[sv]);
+                if (u == NT * NP - 1) mma_commit_w(&v_empty[sv]);
                 if (more && j + 1 >= j0[t] && j + 1 < j1[t]) {
                     if (!have_k && !(ok = wt(&k_full[sk], ((r + 1) / KS) & 1))) break;
                     have_k = true;
@@ -287,17 +313,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // [64 c, 64 c + 64) of each key tile, c = g % 2
         const int g = (warp - 4) >> 2;
         const int t = g >> 1, c = g & 1;
-        const int part = 2 * (c * NP / 2) + t;   // barriers of this tile and part
+        const int part = NT * (c * NP / 2) + t;   // barriers of this tile and part
         const int quarter = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
         const int row = (qtile0 + t) * 128 + quarter * 32 + lane;
         const int2 span = row_span(p.src, z, row, n);
-        const int ja = t ? j0[1] : j0[0], jb = t ? j1[1] : j1[0];
+        const int ja = t ? j0[NT - 1] : j0[0], jb = t ? j1[NT - 1] : j1[0];
         bool ok = true;
         if (jb > 0) {
             const ScoreCoef cf = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                                          SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
-            const uint32_t tS = tmem + lane_bits + (t ? Lay::COL_S1 : Lay::COL_S0) + 64 * c;
+            const uint32_t tS = tmem + lane_bits + Lay::COL_S + 128 * t + 64 * c;
             int pause = tail_pause(cf);
             for (int j = ja; j < jb; ++j) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&s_full[part], (j - ja) & 1, wctx));
@@ -338,7 +364,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (jb > 0) {
             if (ok) {
                 tc_fence_after();
-                const uint32_t tO = tmem + lane_bits + (t ? Lay::COL_O1 : Lay::COL_O0) + c * HALF;
+                const uint32_t tO = tmem + lane_bits + Lay::COL_O + D * t + c * HALF;
                 const bool valid = span.x < span.y;
 #pragma unroll
                 for (int cc = 0; cc < HALF / 32; ++cc) {
