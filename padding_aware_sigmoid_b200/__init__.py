@@ -138,6 +138,26 @@ def load_library():
         return lib
 
 
+_native = None
+
+
+def native():
+    """The compiled entry points (csrc/binding.cpp), bound to the library."""
+    global _native
+    if _native is None:
+        lib = load_library()
+        try:
+            from . import _calls as calls
+        except ImportError as e:
+            raise ImportError("_calls.so is not built for this PyTorch; run "
+                              "`python -m padding_aware_sigmoid_b200.build`") from e
+        names = ("sigattn_fwd_span", "sigattn_bwd_span", "sigattn_bwd_span_workspace_bytes",
+                 "sigattn_cache_append", "sigattn_fwd_paged", "sigattn_fwd_paged_workspace_bytes")
+        calls.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _check)
+        _native = calls
+    return _native
+
+
 def _check(code: int, where: str):
     if code != 0:
         detail = last_cuda_error() if code == 6 else ""
