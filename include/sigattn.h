@@ -261,7 +261,7 @@ size_t sigattn_dbias_workspace_bytes(int Z, int L, int H, sigattn_dtype dtype);
  * Errors: SIGATTN_ERR_INVALID_ARG (also: H not a multiple of Hk, a negative or
  * non-finite cap, a missing or small workspace), _UNSUPPORTED_HEADDIM,
  * _UNSUPPORTED_DTYPE, _UNSUPPORTED_DEVICE, _MISALIGNED (also: spans not 8-byte
- * aligned), _TOO_LARGE (fp32 beyond 2^34 rows), _CUDA.  On error nothing is
+ * aligned), _TOO_LARGE (fp32: 2^31 groups of four rows), _CUDA.  On error nothing is
  * launched. */
 sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, void *o,
                                 const int32_t *seqlens, const int32_t *spans, int Z, int L, int H,

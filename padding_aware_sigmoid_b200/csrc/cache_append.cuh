@@ -85,9 +85,10 @@ struct AppendVec<float> {
 // TOK tokens a block.  A head row is D / N vectors of 16 bytes, handled in
 // D / 2N units of two vectors each: with half-split pairs a unit of the rotated
 // part is (vector u, vector u + rot / 2N), otherwise two neighbours.  Every
-// thread reads its first UNR units before anything else is known about the
-// tokens (padded rows are there to be read, too), so the loads cover the
-// lookups and the angles.
+// thread reads its first UNR units before the lookups and the angles, which the
+// loads cover.  With one token a block (latency counts) nothing at all is known
+// about the token by then: a padded row is there to be read, too.  With several
+// (traffic counts) rows of padding are left out.
 template <typename T, int D, int TOK>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
     using Vec = AppendVec<T>;
@@ -130,6 +131,10 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
         }
         if (u.head >= p.H + p.Hk) u.pair = -1;    // a value
         return u;
+    };
+    auto is_live = [&](int t) {
+        const unsigned tok = static_cast<unsigned>(tok0) + t, z = tok / p.L;     // below 2^31
+        return static_cast<int>(tok - z * p.L) < __ldg(p.seqlens_new + z);
     };
     auto load = [&](const Unit &u, uint4 &a, uint4 &b) {
         const size_t tok = static_cast<size_t>(tok0 + u.t);
@@ -188,7 +193,10 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
         const int e = tid + u * kAppendThreads;
-        if (e < all) load(unit_of(e), a[u], b[u]);
+        if (e < all) {
+            const Unit un = unit_of(e);
+            if (TOK == 1 || is_live(un.t)) load(un, a[u], b[u]);
+        }
     }
 
     // where each token goes, by the last warp
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
     }
     for (int e = tid + UNR * kAppendThreads; e < all; e += kAppendThreads) {
         const Unit un = unit_of(e);
-        load(un, a[0], b[0]);
+        if (live[un.t]) load(un, a[0], b[0]);
         finish(un, a[0], b[0]);
     }
 }

@@ -35,8 +35,9 @@ sigattn_status check_span(const SpanArgs &a, bool *empty) {
     if (a.Hk == 0 || a.H % a.Hk != 0) return SIGATTN_ERR_INVALID_ARG;
     if (a.seqlens == nullptr) return SIGATTN_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(a.spans) & 7u) != 0) return SIGATTN_ERR_MISALIGNED;
-    // one warp per row: 8 rows a block
-    if (a.dtype == SIGATTN_FP32 && static_cast<int64_t>(a.Z) * a.L * (a.H + a.Hk) > (int64_t(INT_MAX) - 8) * 8)
+    // the grid of the fp32 path
+    if (a.dtype == SIGATTN_FP32 &&
+        (static_cast<int64_t>(a.L) + kF32Rows - 1) / kF32Rows * a.Z > int64_t(INT_MAX) / (a.H + a.Hk))
         return SIGATTN_ERR_TOO_LARGE;
     return SIGATTN_OK;
 }
@@ -74,7 +75,10 @@ bool heads_first(const SpanArgs &a, int tensors, int64_t tiles) {
     return tiles <= 65535 && static_cast<int64_t>(tensors) * a.Z * a.L * a.Hk * a.D * 2 <= kStreamMost;
 }
 
-dim3 f32_grid(int64_t rows) { return dim3(static_cast<unsigned>((rows + 7) / 8)); }
+// blocks of kF32Rows rows of one head
+unsigned f32_blocks(const SpanArgs &a, int heads) {
+    return static_cast<unsigned>((static_cast<int64_t>(a.L) + kF32Rows - 1) / kF32Rows * heads * a.Z);
+}
 
 // The device's state, for a dtype the device can run.
 sigattn_status span_device(const SpanArgs &a, int *dev, int **status) {
@@ -178,9 +182,9 @@ sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, voi
         p.k = static_cast<const float *>(k);
         p.v = static_cast<const float *>(v);
         p.o = static_cast<float *>(o);
-        const dim3 grid = f32_grid(static_cast<int64_t>(Z) * L * H);
-        return D == 64 ? launch(span_f32_fwd_kernel<64>, grid, dim3(256), 0, st, p)
-                       : launch(span_f32_fwd_kernel<128>, grid, dim3(256), 0, st, p);
+        const dim3 grid(f32_blocks(a, H)), block(32 * kF32Rows);
+        return D == 64 ? launch(span_f32_fwd_kernel<64>, grid, block, 0, st, p)
+                       : launch(span_f32_fwd_kernel<128>, grid, block, 0, st, p);
     }
     CUtensorMap mq, mk, mv;
     if ((s = encode_bf16_map_uncached(&mq, q, Z, L, H, D)) != SIGATTN_OK) return s;
@@ -236,9 +240,10 @@ sigattn_status sigattn_bwd_span(const void *q, const void *k, const void *v, con
         p.dq = static_cast<float *>(dq);
         p.dk = static_cast<float *>(dk);
         p.dv = static_cast<float *>(dv);
-        const dim3 gq = f32_grid(static_cast<int64_t>(Z) * L * H), gk = f32_grid(static_cast<int64_t>(Z) * L * Hk);
-        return D == 64 ? launch(span_f32_bwd_kernel<64>, dim3(gq.x + gk.x), dim3(256), 0, st, p, gq.x)
-                       : launch(span_f32_bwd_kernel<128>, dim3(gq.x + gk.x), dim3(256), 0, st, p, gq.x);
+        const unsigned rows = f32_blocks(a, H);
+        const dim3 grid(rows + f32_blocks(a, Hk)), block(32 * kF32Rows);
+        return D == 64 ? launch(span_f32_bwd_kernel<64>, grid, block, 0, st, p, rows)
+                       : launch(span_f32_bwd_kernel<128>, grid, block, 0, st, p, rows);
     }
     CUtensorMap mq, mk, mv, mdo;
     if ((s = encode_bf16_map_uncached(&mq, q, Z, L, H, D)) != SIGATTN_OK) return s;

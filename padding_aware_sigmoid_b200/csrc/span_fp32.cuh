@@ -1,8 +1,10 @@
 // fp32 accuracy path of the masked attention (span_score.cuh): one warp per
-// output row, fp32 arithmetic throughout, library expf and tanhf.  Lanes are
-// keys (or queries) while scores are formed, so that a weight is computed once and
-// no reduction is needed, and entries of the row while it is accumulated.
-// Bound by latency: meant for accuracy checks at small sizes.
+// output row, fp32 arithmetic throughout, library expf and tanhf.  The four rows
+// of a block share chunks of 32 rows of the other side in shared memory; lanes are
+// those rows while scores are formed, so that a weight is computed once and no
+// reduction is needed, and entries of the output row while it is accumulated.
+// Bound by latency and shared-memory reads: meant for accuracy checks at small
+// sizes.
 #pragma once
 
 #include "fp32_simt.cuh"
@@ -32,15 +34,41 @@ __device__ __forceinline__ void span_exact(float y, float cap, float add, float 
     g *= f;
 }
 
-// Dot products of the row `x` (D floats, the same address in every lane) with
-// this lane's rows a and b.
+// Rows of a block, one warp each, and rows of a chunk that all of them share in
+// shared memory, kF32Stride floats apart (16-byte reads of 32 rows then meet no
+// bank twice).
+constexpr int kF32Rows = 4, kF32Chunk = 32;
 template <int D>
-__device__ __forceinline__ float row_dot(const float *x, const float *a) {
+struct SpanF32Smem {
+    static constexpr int kStride = D + 4;
+    float a[kF32Chunk][kStride], b[kF32Chunk][kStride];   // K and V, or Q and dO, of a chunk
+    float x[kF32Rows][D], y[kF32Rows][D];                  // the block's own rows of the other side
+};
+
+// Rows r0 ... r0 + kF32Chunk - 1 below `end` of two tensors (row r at base + r *
+// stride) into a chunk; the others as zeros, whatever memory holds there.
+template <int D>
+__device__ __forceinline__ void span_f32_chunk(SpanF32Smem<D> &sm, const float *a, const float *b, int64_t stride,
+                                               int r0, int end) {
+    constexpr int V = D / 4;
+    for (int e = threadIdx.x; e < kF32Chunk * V; e += 32 * kF32Rows) {
+        const int r = e / V, c = 4 * (e % V);
+        float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
+        if (r0 + r < end) {
+            u = __ldg(reinterpret_cast<const float4 *>(a + (r0 + r) * stride + c));
+            v = __ldg(reinterpret_cast<const float4 *>(b + (r0 + r) * stride + c));
+        }
+        *reinterpret_cast<float4 *>(&sm.a[r][c]) = u;
+        *reinterpret_cast<float4 *>(&sm.b[r][c]) = v;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ float span_f32_dot(const float *x, const float *a) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float4 *x4 = reinterpret_cast<const float4 *>(x), *a4 = reinterpret_cast<const float4 *>(a);
 #pragma unroll
-    for (int e = 0; e < D / 4; ++e) {
-        const float4 u = __ldg(x4 + e), v = __ldg(a4 + e);
+    for (int e = 0; e < D; e += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(x + e), v = *reinterpret_cast<const float4 *>(a + e);
         s[0] = fmaf(u.x, v.x, s[0]);
         s[1] = fmaf(u.y, v.y, s[1]);
         s[2] = fmaf(u.z, v.z, s[2]);
@@ -49,124 +77,141 @@ __device__ __forceinline__ float row_dot(const float *x, const float *a) {
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// Forward (DQ false) or dQ (DQ true): one warp per (z, i, h).
+// Forward (DQ false) or dQ (DQ true) of query rows 4 g ... 4 g + 3 of one head.
 template <int D, bool DQ>
-__device__ __forceinline__ void span_f32_row(const SpanF32Params &p, int64_t r) {
+__device__ __forceinline__ void span_f32_rows(const SpanF32Params &p, SpanF32Smem<D> &sm, int64_t block) {
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, L = p.src.L;
-    if (r >= static_cast<int64_t>(p.Z) * L * p.H) return;
-    const int h = static_cast<int>(r % p.H);
-    const int i = static_cast<int>((r / p.H) % L);
-    const int z = static_cast<int>(r / (static_cast<int64_t>(p.H) * L));
+    const int lane = lane_id(), warp = warp_id(), L = p.src.L, groups = (L + kF32Rows - 1) / kF32Rows;
+    const int g = static_cast<int>(block % groups);
+    const int h = static_cast<int>((block / groups) % p.H);
+    const int z = static_cast<int>(block / (static_cast<int64_t>(groups) * p.H));
+    const int i = g * kF32Rows + warp;
     const int n = span_tokens(p.src, z);
     const int2 span = row_span(p.src, z, i, n);
     const float bias = bias_of(p.bias_z, p.bias, z), slope = p.slopes != nullptr ? p.slopes[h] : 0.0f;
     const int64_t krow = static_cast<int64_t>(p.Hk) * D;
     const int64_t kbase = static_cast<int64_t>(z) * L * krow + static_cast<int64_t>(h / p.group) * D;
+    const int64_t row = ((static_cast<int64_t>(z) * L + i) * p.H + h) * D;
+    int lo = INT_MAX, hi = 0;            // keys that any row of the block sees
+#pragma unroll
+    for (int w = 0; w < kF32Rows; ++w) {
+        const int2 s = row_span(p.src, z, g * kF32Rows + w, n);
+        if (s.x < s.y) {
+            lo = min(lo, s.x);
+            hi = max(hi, s.y);
+        }
+    }
     float acc[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int j0 = span.x; j0 < span.y; j0 += 32) {
+    for (int e = 0; e < E; ++e) {
+        acc[e] = 0.0f;
+        if (i < L) {
+            sm.x[warp][lane + 32 * e] = p.q[row + lane + 32 * e];
+            if (DQ) sm.y[warp][lane + 32 * e] = p.dout[row + lane + 32 * e];
+        }
+    }
+    for (int j0 = lo; j0 < hi; j0 += kF32Chunk) {
+        __syncthreads();
+        span_f32_chunk<D>(sm, p.k + kbase, p.v + kbase, krow, j0, hi);
+        __syncthreads();
         const int j = j0 + lane;
         float w = 0.0f;
-        if (j < span.y) {
-            const int64_t at = kbase + j * krow;
-            float pr, g;
-            span_exact(p.alpha * row_dot<D>(p.q + r * D, p.k + at), p.cap,
-                       fmaf(-slope, fabsf(static_cast<float>(i - j)), bias), pr, g);
-            w = DQ ? g * row_dot<D>(p.dout + r * D, p.v + at) : pr;
+        if (j >= span.x && j < span.y) {
+            float pr, gr;
+            span_exact(p.alpha * span_f32_dot<D>(sm.x[warp], sm.a[lane]), p.cap,
+                       fmaf(-slope, fabsf(static_cast<float>(i - j)), bias), pr, gr);
+            w = DQ ? gr * span_f32_dot<D>(sm.y[warp], sm.b[lane]) : pr;
         }
-        const float *src = (DQ ? p.k : p.v) + kbase + j0 * krow + lane;
-        const int m = min(32, span.y - j0);
-        if (m == 32) {
-#pragma unroll 8
-            for (int u = 0; u < 32; ++u) {
+        if (__any_sync(0xffffffffu, w != 0.0f)) {
+#pragma unroll
+            for (int u = 0; u < kF32Chunk; ++u) {
                 const float wu = __shfl_sync(0xffffffffu, w, u);
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wu, __ldg(src + u * krow + 32 * e), acc[e]);
-            }
-        } else {
-            for (int u = 0; u < m; ++u) {
-                const float wu = __shfl_sync(0xffffffffu, w, u);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wu, __ldg(src + u * krow + 32 * e), acc[e]);
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(wu, (DQ ? sm.a : sm.b)[u][lane + 32 * e], acc[e]);
             }
         }
     }
-    float *out = (DQ ? p.dq : p.o) + r * D + lane;
+    if (i < L) {
+        float *out = (DQ ? p.dq : p.o) + row + lane;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[32 * e] = DQ ? p.alpha * acc[e] : acc[e];
+        for (int e = 0; e < E; ++e) out[32 * e] = DQ ? p.alpha * acc[e] : acc[e];
+    }
 }
 
-// dK and dV: one warp per (z, j, key head), over the queries of its heads.
+// dK and dV of keys 4 g ... 4 g + 3 of one key head, over the queries of its heads.
 template <int D>
-__device__ __forceinline__ void span_f32_key(const SpanF32Params &p, int64_t r) {
+__device__ __forceinline__ void span_f32_keys(const SpanF32Params &p, SpanF32Smem<D> &sm, int64_t block) {
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, L = p.src.L;
-    if (r >= static_cast<int64_t>(p.Z) * L * p.Hk) return;
-    const int kvh = static_cast<int>(r % p.Hk);
-    const int j = static_cast<int>((r / p.Hk) % L);
-    const int z = static_cast<int>(r / (static_cast<int64_t>(p.Hk) * L));
+    const int lane = lane_id(), warp = warp_id(), L = p.src.L, groups = (L + kF32Rows - 1) / kF32Rows;
+    const int g = static_cast<int>(block % groups);
+    const int kvh = static_cast<int>((block / groups) % p.Hk);
+    const int z = static_cast<int>(block / (static_cast<int64_t>(groups) * p.Hk));
+    const int j = g * kF32Rows + warp;
     const int n = span_tokens(p.src, z);
     const float bias = bias_of(p.bias_z, p.bias, z);
     const int64_t qrow = static_cast<int64_t>(p.H) * D;
+    const int64_t row = ((static_cast<int64_t>(z) * L + j) * p.Hk + kvh) * D;
     float ak[E], av[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) ak[e] = av[e] = 0.0f;
-    for (int h = kvh * p.group; j < n && h < (kvh + 1) * p.group; ++h) {
-        const float slope = p.slopes != nullptr ? p.slopes[h] : 0.0f;
-        const int64_t base = static_cast<int64_t>(z) * L * qrow + static_cast<int64_t>(h) * D;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane;
-            const int2 sp = row_span(p.src, z, i, n);
-            const bool sees = j >= sp.x && j < sp.y;
-            unsigned who = __ballot_sync(0xffffffffu, sees);
-            if (who == 0) continue;
-            float pr = 0.0f, g = 0.0f;
+    for (int e = 0; e < E; ++e) {
+        ak[e] = av[e] = 0.0f;
+        if (j < L) {
+            sm.x[warp][lane + 32 * e] = p.k[row + lane + 32 * e];
+            sm.y[warp][lane + 32 * e] = p.v[row + lane + 32 * e];
+        }
+    }
+    for (int i0 = 0; i0 < n; i0 += kF32Chunk) {
+        // does any row of the chunk see a key of the block?
+        const int i = i0 + lane;
+        const int2 sp = row_span(p.src, z, i, n);
+        if (!__any_sync(0xffffffffu, sp.x < (g + 1) * kF32Rows && sp.y > g * kF32Rows)) continue;   // alike in all warps
+        const bool sees = j >= sp.x && j < sp.y;
+        for (int h = kvh * p.group; h < (kvh + 1) * p.group; ++h) {
+            const int64_t base = static_cast<int64_t>(z) * L * qrow + static_cast<int64_t>(h) * D;
+            __syncthreads();
+            span_f32_chunk<D>(sm, p.q + base, p.dout + base, qrow, i0, n);
+            __syncthreads();
+            float pr = 0.0f, gr = 0.0f;
             if (sees) {
-                const int64_t at = base + i * qrow;
-                span_exact(p.alpha * row_dot<D>(p.k + r * D, p.q + at), p.cap,
-                           fmaf(-slope, fabsf(static_cast<float>(i - j)), bias), pr, g);
-                g *= row_dot<D>(p.v + r * D, p.dout + at);
+                span_exact(p.alpha * span_f32_dot<D>(sm.x[warp], sm.a[lane]), p.cap,
+                           fmaf(p.slopes != nullptr ? -p.slopes[h] : 0.0f, fabsf(static_cast<float>(i - j)), bias), pr, gr);
+                gr *= span_f32_dot<D>(sm.y[warp], sm.b[lane]);
             }
-            // only rows that see the key are read: the others may be padding
-            const int64_t at = base + i0 * qrow + lane;
-            auto add = [&](int u) {
-                const float pu = __shfl_sync(0xffffffffu, pr, u), gu = __shfl_sync(0xffffffffu, g, u);
+            if (__any_sync(0xffffffffu, sees)) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    ak[e] = fmaf(gu, __ldg(p.q + at + u * qrow + 32 * e), ak[e]);
-                    av[e] = fmaf(pu, __ldg(p.dout + at + u * qrow + 32 * e), av[e]);
+                for (int u = 0; u < kF32Chunk; ++u) {
+                    const float pu = __shfl_sync(0xffffffffu, pr, u), gu = __shfl_sync(0xffffffffu, gr, u);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        ak[e] = fmaf(gu, sm.a[u][lane + 32 * e], ak[e]);
+                        av[e] = fmaf(pu, sm.b[u][lane + 32 * e], av[e]);
+                    }
                 }
-            };
-            if (who == 0xffffffffu) {
-#pragma unroll 8
-                for (int u = 0; u < 32; ++u) add(u);
-            } else {
-                for (; who != 0; who &= who - 1) add(__ffs(who) - 1);
             }
         }
     }
+    if (j < L) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        p.dk[r * D + lane + 32 * e] = p.alpha * ak[e];
-        p.dv[r * D + lane + 32 * e] = av[e];
+        for (int e = 0; e < E; ++e) {
+            p.dk[row + lane + 32 * e] = p.alpha * ak[e];
+            p.dv[row + lane + 32 * e] = av[e];
+        }
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) span_f32_fwd_kernel(const SpanF32Params p) {
-    span_f32_row<D, false>(p, static_cast<int64_t>(blockIdx.x) * 8 + warp_id());
+__global__ void __launch_bounds__(32 * kF32Rows) span_f32_fwd_kernel(const SpanF32Params p) {
+    __shared__ __align__(16) SpanF32Smem<D> sm;
+    span_f32_rows<D, false>(p, sm, blockIdx.x);
 }
 
 // Both halves of the backward in one launch: blocks [0, row_blocks) take rows of
 // dQ, the others keys.
 template <int D>
-__global__ void __launch_bounds__(256) span_f32_bwd_kernel(const SpanF32Params p, unsigned row_blocks) {
-    if (blockIdx.x < row_blocks)
-        span_f32_row<D, true>(p, static_cast<int64_t>(blockIdx.x) * 8 + warp_id());
-    else
-        span_f32_key<D>(p, static_cast<int64_t>(blockIdx.x - row_blocks) * 8 + warp_id());
+__global__ void __launch_bounds__(32 * kF32Rows) span_f32_bwd_kernel(const SpanF32Params p, unsigned row_blocks) {
+    __shared__ __align__(16) SpanF32Smem<D> sm;
+    if (blockIdx.x < row_blocks) span_f32_rows<D, true>(p, sm, blockIdx.x);
+    else span_f32_keys<D>(p, sm, blockIdx.x - row_blocks);
 }
 
 }  // namespace sigattn
