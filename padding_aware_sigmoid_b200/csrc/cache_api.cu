@@ -156,13 +156,14 @@ sigattn_status paged_score(int score, const PagedMaps &m, const PagedParams &p, 
 
 template <typename T, int D>
 sigattn_status append_launch(const AppendParams &p, int sms, cudaStream_t st) {
+    // Few tokens (a decoding step): eight warps share one, a block, and read ahead.
+    // Many: a warp each.
     const int64_t tokens = static_cast<int64_t>(p.Z) * p.L;
-    // Four tokens a block keep three units in flight per thread; below two
-    // blocks an SM one token a block spreads a decoding step over more SMs.
-    if (tokens >= int64_t(8) * sms)
-        return launch(cache_append_kernel<T, D, 4>, dim3(static_cast<unsigned>((tokens + 3) / 4)),
-                      dim3(kAppendThreads), 0, st, p);
-    return launch(cache_append_kernel<T, D, 1>, dim3(static_cast<unsigned>(tokens)), dim3(kAppendThreads), 0, st, p);
+    const bool few = tokens <= int64_t(4) * sms;
+    const int share = few ? kAppendThreads / 32 : 1;
+    const int64_t blocks = (tokens * share + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+    return launch(cache_append_kernel<T, D>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0, st, p, share,
+                  few);
 }
 
 }  // namespace

@@ -7,9 +7,12 @@
 // turns by the angle p * inv_freq[i].  Values are copied, queries rotated out.
 //
 // Pure traffic: every row is read once and written once, 16 bytes a thread and
-// access.  The angles of a token (rot / 2 of them) are shared by all its heads:
-// a block holds a few tokens, issues its loads first, forms the angles of its
-// tokens while they fly, and rotates and stores after one barrier.
+// access.  One warp takes a token (or a share of its heads, when tokens are few).
+// Its lanes keep their place within a head, so that each holds the angles of its
+// pairs in registers for all heads of the token; what is left per head is the
+// loads, two FMAs an entry and the stores.  (One thread per unit of any head with the
+// angles in shared memory spent its time on instructions: 40 us for 4 x 4096 prompt
+// tokens, 16 + 4 heads of 128.)
 #pragma once
 
 #include <stdint.h>
@@ -48,6 +51,12 @@ __device__ __forceinline__ float2 position_angle(double p, float f) {
     return make_float2(c, s);
 }
 
+__device__ __forceinline__ void turn_pair(float &a, float &b, float c, float s) {
+    const float a0 = a;
+    a = a0 * c - b * s;
+    b = b * c + a0 * s;
+}
+
 template <typename T>
 struct AppendVec;
 template <>
@@ -82,169 +91,132 @@ struct AppendVec<float> {
     }
 };
 
-// TOK tokens a block.  A head row is D / N vectors of 16 bytes, handled in
-// D / 2N units of two vectors each: with half-split pairs a unit of the rotated
-// part is (vector u, vector u + rot / 2N), otherwise two neighbours.  Every
-// thread reads its first UNR units before the lookups and the angles, which the
-// loads cover.  With one token a block (latency counts) nothing at all is known
-// about the token by then: a padded row is there to be read, too.  With several
-// (traffic counts) rows of padding are left out.
-template <typename T, int D, int TOK>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
+// A head row is D / N vectors of 16 bytes, handled in UNITS units of two vectors
+// each: with half-split pairs a unit of the rotated part is (vector u, vector u +
+// rot / 2N), otherwise two neighbours.  32 / UNITS heads make one pass of a warp;
+// `share` warps split a token's passes.
+//
+// With `ahead` the first rows are read before anything is known about the token
+// (a padded row is there to be read, too), which hides the lookups of a decoding
+// step; without it rows of padding cost nothing.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const AppendParams p, int share, bool ahead) {
     using Vec = AppendVec<T>;
-    constexpr int N = Vec::N, VECS = D / N, UNITS = VECS / 2;
-    constexpr int UNR = 3;
-    __shared__ float2 turn[TOK][kAppendPairs];
-    __shared__ int64_t dest[TOK];      // cache row (page * page_size + slot) times Hk, or < 0
-    __shared__ int live[TOK];          // 1: a token of its sample, 0: padding
-    __shared__ int after[TOK];         // its sample's new length, < 0: written by another token
-    const int64_t tokens = static_cast<int64_t>(p.Z) * p.L;
-    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * TOK;
-    const int here = static_cast<int>(min(static_cast<int64_t>(TOK), tokens - tok0));
+    constexpr int N = Vec::N, VECS = D / N, UNITS = VECS / 2, HEADS = 32 / UNITS;
+    constexpr int UNR = 2;        // passes whose rows are in flight together
+    __shared__ __align__(16) float2 turns[kAppendThreads / 32][kAppendPairs];
+    const int lane = lane_id();
+    const unsigned id = blockIdx.x * (kAppendThreads / 32) + warp_id();
+    const unsigned tok = id / share, sub = id % share;     // Z L tokens, below 2^31
+    if (tok >= static_cast<unsigned>(p.Z) * p.L) return;
+    const unsigned z = tok / p.L;
+    const int l = static_cast<int>(tok - z * p.L);
     const int capacity = p.max_pages << p.page_shift;     // checked on the host to fit
-    const int tid = threadIdx.x;
-    const int pairs = p.rot / 2;
-    const int heads = p.H + 2 * p.Hk;       // queries, keys, values
-    const int per_token = heads * UNITS, all = here * per_token;
-    const int half_units = pairs / N;       // rotated units with half-split pairs
-    const uint4 *q = static_cast<const uint4 *>(p.q), *k = static_cast<const uint4 *>(p.k),
-                *v = static_cast<const uint4 *>(p.v);
+    const int un = lane % UNITS, pairs = p.rot / 2, half_units = pairs / N;
+    const int heads = p.H + 2 * p.Hk;                      // queries, keys, values
+    // this lane's vectors, and its first pair (-1: not rotated)
+    const bool neighbours = p.interleaved || un >= half_units;
+    const int va = !neighbours ? un : p.interleaved ? 2 * un : 2 * half_units + 2 * (un - half_units);
+    const int vb = !neighbours ? un + half_units : va + 1;
+    const int pair = !neighbours ? un * N : p.interleaved && va * N < p.rot ? va * N / 2 : -1;
 
-    // one unit: its token and head, its vectors, its first pair (-1: not rotated)
-    struct Unit {
-        int t, head, va, vb, pair;
+    const int keys = p.H, values = p.H + p.Hk;     // first head of each
+    const uint4 *qrow = static_cast<const uint4 *>(p.q) + static_cast<size_t>(tok) * p.H * VECS;
+    const uint4 *krow = static_cast<const uint4 *>(p.k) + (static_cast<size_t>(tok) * p.Hk - keys) * VECS;
+    const uint4 *vrow = static_cast<const uint4 *>(p.v) + (static_cast<size_t>(tok) * p.Hk - values) * VECS;
+    auto load = [&](int head, uint4 &a, uint4 &b) {
+        const uint4 *row = (head < keys ? qrow : head < values ? krow : vrow) + head * VECS;
+        a = __ldg(row + va);
+        b = __ldg(row + vb);
     };
-    auto unit_of = [&](int e) {
-        Unit u;
-        u.t = TOK == 1 ? 0 : e / per_token;
-        const int w = e - u.t * per_token, un = w % UNITS;
-        u.head = w / UNITS;
-        u.pair = -1;
-        if (p.interleaved || un >= half_units) {
-            u.va = p.interleaved ? 2 * un : 2 * half_units + 2 * (un - half_units);
-            u.vb = u.va + 1;
-            if (p.interleaved && u.va * N < p.rot) u.pair = u.va * N / 2;
-        } else {
-            u.va = un;
-            u.vb = un + half_units;
-            u.pair = un * N;
+    const int first = static_cast<int>(sub) * HEADS + lane / UNITS, step = share * HEADS;
+    uint4 a[UNR], b[UNR];
+    if (ahead) {
+#pragma unroll
+        for (int u = 0; u < UNR; ++u)
+            if (first + u * step < heads) load(first + u * step, a[u], b[u]);
+    }
+
+    int have = p.cache_lens[z], add = p.seqlens_new[z];
+    const int base = p.prefix_len != nullptr ? max(*p.prefix_len, 0) : 0;
+    if (have < 0 || have > capacity || add < 0 || add > p.L || add > capacity - have) {
+        record_status(p.status, kStatusSeqlenRange);
+        have = min(max(have, 0), capacity);
+        add = min(max(add, 0), p.L);
+    }
+    // lens_out may be cache_lens when L is 1: then the token's warps all have to have
+    // read it, and they are one warp, or one block that meets here
+    if (share > 1) __syncthreads();
+    if (l == 0 && sub == 0 && lane == 0) p.lens_out[z] = min(have + min(add, capacity - have), capacity);
+    const bool live = l < add;
+    int64_t dest = -1;       // cache row (page * page_size + slot) times Hk
+    const int64_t place = static_cast<int64_t>(have) + l;
+    if (live && place < capacity) {
+        const int page = p.page_table[static_cast<size_t>(z) * p.max_pages + (place >> p.page_shift)];
+        if (page < 0 || page >= p.pages)
+            record_status(p.status, kStatusPageRange);
+        else
+            dest = ((static_cast<int64_t>(page) << p.page_shift) + (place & ((1 << p.page_shift) - 1))) * p.Hk;
+    }
+    if (live && !ahead) {
+#pragma unroll
+        for (int u = 0; u < UNR; ++u)
+            if (first + u * step < heads) load(first + u * step, a[u], b[u]);
+    }
+    float2 *turn = turns[warp_id()];     // cos, sin of the token's pairs
+    if (live && pairs > 0) {
+        for (int i = lane; i < pairs; i += 32)
+            turn[i] = position_angle(static_cast<double>(base) + place, p.inv_freq[i]);
+        __syncwarp();
+    }
+    uint4 *qto = static_cast<uint4 *>(p.q_out) + static_cast<size_t>(tok) * p.H * VECS;
+    uint4 *kto = static_cast<uint4 *>(p.k_pages) + (dest - keys) * VECS;
+    uint4 *vto = static_cast<uint4 *>(p.v_pages) + (dest - values) * VECS;
+    const float4 *cs = reinterpret_cast<const float4 *>(turn + max(pair, 0));
+    auto finish = [&](int head, uint4 x16, uint4 y16) {
+        if (head < keys) {
+            if (!live) x16 = y16 = make_uint4(0u, 0u, 0u, 0u);      // a padded query row
+        } else if (dest < 0) {
+            return;
         }
-        if (u.head >= p.H + p.Hk) u.pair = -1;    // a value
-        return u;
-    };
-    auto is_live = [&](int t) {
-        const unsigned tok = static_cast<unsigned>(tok0) + t, z = tok / p.L;     // below 2^31
-        return static_cast<int>(tok - z * p.L) < __ldg(p.seqlens_new + z);
-    };
-    auto load = [&](const Unit &u, uint4 &a, uint4 &b) {
-        const size_t tok = static_cast<size_t>(tok0 + u.t);
-        const uint4 *row = u.head < p.H ? q + (tok * p.H + u.head) * VECS
-                           : u.head < p.H + p.Hk ? k + (tok * p.Hk + (u.head - p.H)) * VECS
-                                                 : v + (tok * p.Hk + (u.head - p.H - p.Hk)) * VECS;
-        a = __ldg(row + u.va);
-        b = __ldg(row + u.vb);
-    };
-    auto finish = [&](const Unit &u, uint4 a, uint4 b) {
-        uint4 *to;
-        if (u.head < p.H) {
-            to = static_cast<uint4 *>(p.q_out) + (static_cast<size_t>(tok0 + u.t) * p.H + u.head) * VECS;
-            if (!live[u.t]) {      // a padded query row
-                to[u.va] = to[u.vb] = make_uint4(0u, 0u, 0u, 0u);
-                return;
-            }
-        } else {
-            if (dest[u.t] < 0) return;
-            const bool key = u.head < p.H + p.Hk;
-            to = static_cast<uint4 *>(key ? p.k_pages : p.v_pages) +
-                 (static_cast<size_t>(dest[u.t]) + u.head - p.H - (key ? 0 : p.Hk)) * VECS;
-        }
-        if (u.pair >= 0) {
+        uint4 *to = (head < keys ? qto : head < values ? kto : vto) + head * VECS;
+        if (pair >= 0 && live && head < values) {
             float x[N], y[N];
-            Vec::open(a, x);
-            Vec::open(b, y);
-            const float2 *cs = &turn[u.t][u.pair];
+            Vec::open(x16, x);
+            Vec::open(y16, y);
             if (p.interleaved) {
 #pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const float2 c = cs[i / 2], d = cs[N / 2 + i / 2];
-                    const float x0 = x[i], y0 = y[i];
-                    x[i] = x0 * c.x - x[i + 1] * c.y;
-                    x[i + 1] = x[i + 1] * c.x + x0 * c.y;
-                    y[i] = y0 * d.x - y[i + 1] * d.y;
-                    y[i + 1] = y[i + 1] * d.x + y0 * d.y;
+                for (int i = 0; i < N; i += 4) {
+                    const float4 c = cs[i / 4], d = cs[N / 4 + i / 4];      // two pairs each
+                    turn_pair(x[i], x[i + 1], c.x, c.y);
+                    turn_pair(x[i + 2], x[i + 3], c.z, c.w);
+                    turn_pair(y[i], y[i + 1], d.x, d.y);
+                    turn_pair(y[i + 2], y[i + 3], d.z, d.w);
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float2 c = cs[i];
-                    const float x0 = x[i];
-                    x[i] = x0 * c.x - y[i] * c.y;
-                    y[i] = y[i] * c.x + x0 * c.y;
+                for (int i = 0; i < N; i += 2) {
+                    const float4 c = cs[i / 2];
+                    turn_pair(x[i], y[i], c.x, c.y);
+                    turn_pair(x[i + 1], y[i + 1], c.z, c.w);
                 }
             }
-            a = Vec::close(x);
-            b = Vec::close(y);
+            x16 = Vec::close(x);
+            y16 = Vec::close(y);
         }
-        to[u.va] = a;
-        to[u.vb] = b;
+        to[va] = x16;
+        to[vb] = y16;
     };
-
-    uint4 a[UNR], b[UNR];
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-        const int e = tid + u * kAppendThreads;
-        if (e < all) {
-            const Unit un = unit_of(e);
-            if (TOK == 1 || is_live(un.t)) load(un, a[u], b[u]);
-        }
-    }
-
-    // where each token goes, by the last warp
-    if (tid >= kAppendThreads - 32 && tid - (kAppendThreads - 32) < here) {
-        const int t = tid - (kAppendThreads - 32);
-        const int64_t tok = tok0 + t;
-        const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
-        int have = p.cache_lens[z], add = p.seqlens_new[z];
-        if (have < 0 || have > capacity || add < 0 || add > p.L || add > capacity - have) {
-            record_status(p.status, kStatusSeqlenRange);
-            have = min(max(have, 0), capacity);
-            add = min(max(add, 0), p.L);
-        }
-        after[t] = l == 0 ? min(have + min(add, capacity - have), capacity) : -1;
-        live[t] = l < add;
-        const int64_t at = static_cast<int64_t>(have) + l;
-        int64_t to = -1;
-        if (l < add && at < capacity) {
-            const int page = p.page_table[static_cast<size_t>(z) * p.max_pages + (at >> p.page_shift)];
-            if (page < 0 || page >= p.pages)
-                record_status(p.status, kStatusPageRange);
-            else
-                to = ((static_cast<int64_t>(page) << p.page_shift) + (at & ((1 << p.page_shift) - 1))) * p.Hk;
-        }
-        dest[t] = to;
-    }
-    // the tokens' angles
-    const int base = p.prefix_len != nullptr ? max(*p.prefix_len, 0) : 0;
-    for (int e = tid; e < here * pairs; e += kAppendThreads) {
-        const int t = TOK == 1 ? 0 : e / pairs, i = e - t * pairs;
-        const int64_t tok = tok0 + t;
-        const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
-        const int have = min(max(p.cache_lens[z], 0), capacity);
-        if (l < p.seqlens_new[z]) turn[t][i] = position_angle(static_cast<double>(base) + have + l, p.inv_freq[i]);
-    }
-    __syncthreads();
-    // not before the barrier: with single tokens lens_out may be cache_lens
-    if (tid < here && after[tid] >= 0) p.lens_out[(tok0 + tid) / p.L] = after[tid];
-
+    for (int u = 0; u < UNR; ++u)
+        if (first + u * step < heads) finish(first + u * step, a[u], b[u]);
+    for (int h0 = first + UNR * step; h0 < heads; h0 += UNR * step) {
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-        const int e = tid + u * kAppendThreads;
-        if (e < all) finish(unit_of(e), a[u], b[u]);
-    }
-    for (int e = tid + UNR * kAppendThreads; e < all; e += kAppendThreads) {
-        const Unit un = unit_of(e);
-        if (live[un.t]) load(un, a[0], b[0]);
-        finish(un, a[0], b[0]);
+        for (int u = 0; u < UNR; ++u)
+            if (live && h0 + u * step < heads) load(h0 + u * step, a[u], b[u]);
+#pragma unroll
+        for (int u = 0; u < UNR; ++u)
+            if (h0 + u * step < heads) finish(h0 + u * step, a[u], b[u]);
     }
 }
 
