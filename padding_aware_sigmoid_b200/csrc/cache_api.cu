@@ -53,7 +53,7 @@ constexpr int64_t kPrefixKernelRows = 64;
 struct PagedSizes {
     int prefix_warps, own_warps;
     int64_t prefix_rt, own_rt;     // row tiles per key head: of the prefix, of a sample
-    int64_t items;
+    int64_t items;                 // of a key head
     int tile_tokens;      // tokens of a row tile of the prefix kernel; 0: it does not run
     int64_t pairs;        // its pairs of row tiles
 };
@@ -64,7 +64,7 @@ PagedSizes paged_sizes(int Z, int L, int H, int Hk) {
     s.own_warps = row_warps(own);
     s.prefix_rt = (all + 16 * s.prefix_warps - 1) / (16 * s.prefix_warps);
     s.own_rt = (own + 16 * s.own_warps - 1) / (16 * s.own_warps);
-    s.items = Hk * (s.prefix_rt + Z * s.own_rt);
+    s.items = s.prefix_rt + Z * s.own_rt;
     s.tile_tokens = 0;
     s.pairs = 0;
     if (H / Hk <= 128 && all > kPrefixKernelRows) {
@@ -74,14 +74,18 @@ PagedSizes paged_sizes(int Z, int L, int H, int Hk) {
     return s;
 }
 
-size_t part_bytes(const PagedSizes &s, int D) {
-    return static_cast<size_t>(kPagedMostBlocks + s.items) * kPagedPartRows * D * sizeof(float);
+// a head has as many partials as groups and items; the groups' blocks are at most
+// the grid's, or one a head
+size_t part_bytes(const PagedSizes &s, int Hk, int D) {
+    return (static_cast<size_t>(std::max(kPagedMostBlocks, Hk)) + s.items * Hk) * kPagedPartRows * D * sizeof(float);
 }
 // the splits are chosen so that all blocks of the prefix kernel fit the SMs once
 size_t prefix_part_bytes(const PagedSizes &s, int Hk, int D) {
     return s.pairs == 0 ? 0 : (kPagedMostSms + static_cast<size_t>(s.pairs) * Hk) * 256 * D * sizeof(float);
 }
-size_t blocks_bytes(const PagedSizes &s) { return (static_cast<size_t>(s.items) * sizeof(int2) + 255) & ~size_t(255); }
+size_t groups_bytes(const PagedSizes &s, int Hk) {
+    return (static_cast<size_t>(s.items) * Hk * sizeof(int2) + 255) & ~size_t(255);
+}
 
 // A bf16 tensor of four dimensions (innermost first, 128-byte swizzle).
 sigattn_status encode_box(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
@@ -120,7 +124,7 @@ sigattn_status prefix_launch(const PagedMaps &m, const PagedParams &p, cudaStrea
 #define PAGED_W2 16384
 #endif
 template <int D, int SCORE>
-sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, int blocks, cudaStream_t st) {
+sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
     using Lay = PagedLayout<D>;
     sigattn_status s = SIGATTN_OK;
     if (p.splits > 0) {
@@ -130,7 +134,7 @@ sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, int blocks
     }
     // The tile kernel needs nothing of the prefix kernel's, and the join reads
     // its lengths before it waits: both may start early.
-    s = launch_with(paged_tiles_kernel<D, SCORE>, dim3(blocks), dim3(kPagedThreads), Lay::bytes(SIGATTN_PAGED_MAX_Z),
+    s = launch_with(paged_tiles_kernel<D, SCORE>, dim3(p.groups * p.heads_wide), dim3(kPagedThreads), Lay::bytes(SIGATTN_PAGED_MAX_Z),
                     Lay::bytes(p.Z), p.splits > 0, st, m.k, m.v, p);
     if (s != SIGATTN_OK) return s;
     // Few rows: a block each, its warps sharing the row's partials.
@@ -145,12 +149,12 @@ sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, int blocks
     return join(paged_join_kernel<D, 1>, 8);
 }
 template <int D>
-sigattn_status paged_score(int score, const PagedMaps &m, const PagedParams &p, int blocks, cudaStream_t st) {
+sigattn_status paged_score(int score, const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
     switch (score) {
-        case 0: return paged_launch<D, 0>(m, p, blocks, st);
-        case kScoreCap: return paged_launch<D, kScoreCap>(m, p, blocks, st);
-        case kScoreSlope: return paged_launch<D, kScoreSlope>(m, p, blocks, st);
-        default: return paged_launch<D, kScoreCap | kScoreSlope>(m, p, blocks, st);
+        case 0: return paged_launch<D, 0>(m, p, st);
+        case kScoreCap: return paged_launch<D, kScoreCap>(m, p, st);
+        case kScoreSlope: return paged_launch<D, kScoreSlope>(m, p, st);
+        default: return paged_launch<D, kScoreCap | kScoreSlope>(m, p, st);
     }
 }
 
@@ -227,7 +231,7 @@ size_t sigattn_fwd_paged_workspace_bytes(int Z, int L, int H, int Hk, int D, sig
     if (Z <= 0 || L <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || (D != 64 && D != 128) || dtype != SIGATTN_BF16)
         return 0;
     const PagedSizes s = paged_sizes(Z, L, H, Hk);
-    return blocks_bytes(s) + part_bytes(s, D) + prefix_part_bytes(s, Hk, D);
+    return groups_bytes(s, Hk) + part_bytes(s, Hk, D) + prefix_part_bytes(s, Hk, D);
 }
 
 sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void *v_pages, void *o,
@@ -262,7 +266,7 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
     if ((s = device_state(&dev, &cc, &status)) != SIGATTN_OK) return s;
     if (dtype == SIGATTN_BF16 && cc != 100) return SIGATTN_ERR_UNSUPPORTED_DEVICE;
     const PagedSizes z = paged_sizes(Z, L, H, Hk);
-    if (z.items > INT_MAX - 2 * kPagedMostBlocks || z.pairs > 65535 || Hk > 65535) return SIGATTN_ERR_TOO_LARGE;
+    if (z.items * Hk > INT_MAX - 2 * kPagedMostBlocks || z.pairs > 65535 || Hk > 65535) return SIGATTN_ERR_TOO_LARGE;
     PagedParams p = {};
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.o = static_cast<__nv_bfloat16 *>(o);
@@ -297,21 +301,24 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
     }
     if ((s = get_encoder()) != SIGATTN_OK) return s;
     char *ws = static_cast<char *>(workspace);
-    p.blocks_of = reinterpret_cast<int2 *>(ws);
-    p.part = reinterpret_cast<float *>(ws + blocks_bytes(z));
+    p.groups_of = reinterpret_cast<int2 *>(ws);
+    p.part = reinterpret_cast<float *>(ws + groups_bytes(z, Hk));
     p.prefix_rt = static_cast<int>(z.prefix_rt);
     p.own_rt = static_cast<int>(z.own_rt);
     p.prefix_warps = z.prefix_warps;
     p.own_warps = z.own_warps;
     const int sms = std::min(g_sm_count[dev], kPagedMostSms);
     const int blocks = sms * (D == 64 ? PagedLayout<64>::kBlocksPerSm : PagedLayout<128>::kBlocksPerSm);
+    p.heads_wide = std::min(Hk, blocks);
+    p.groups = blocks / p.heads_wide;
+    p.items = static_cast<int>(z.items);
     p.timeout_ns = g_timeout_ns.load();
     PagedMaps m;
     const int own_box = std::min(page_size, kPagedTile);
     if ((s = encode_pages(&m.k, k_pages, c, own_box)) != SIGATTN_OK) return s;
     if ((s = encode_pages(&m.v, v_pages, c, own_box)) != SIGATTN_OK) return s;
     if (z.tile_tokens > 0 && prefix_len != nullptr && prefix_pages > 0) {
-        p.prefix_part = reinterpret_cast<float *>(ws + blocks_bytes(z) + part_bytes(z, D));
+        p.prefix_part = reinterpret_cast<float *>(ws + groups_bytes(z, Hk) + part_bytes(z, Hk, D));
         p.tile_tokens = z.tile_tokens;
         p.pairs = static_cast<int>(z.pairs);
         p.splits = static_cast<int>(std::max<int64_t>(1, sms / (z.pairs * Hk)));
@@ -324,7 +331,7 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
             return s;
     }
     const int score = (cap > 0.0f ? kScoreCap : 0) | (slopes != nullptr ? kScoreSlope : 0);
-    return D == 64 ? paged_score<64>(score, m, p, blocks, st) : paged_score<128>(score, m, p, blocks, st);
+    return D == 64 ? paged_score<64>(score, m, p, st) : paged_score<128>(score, m, p, st);
 }
 
 }  // extern "C"

@@ -17,15 +17,19 @@
 //    prefix is read once per 256 rows and not once per sample.  The key range is
 //    split over blocks until they fill the device.
 //  paged_tiles_kernel (mma.sync): the samples' own keys, and the prefix where the
-//    batch has few rows.  Work is a list of items, each a run of 64-key tiles:
-//      prefix items: (key head, tile of the rows above);
-//      own items:    (sample, key head, tile of its query rows).
-//    The tiles of all items form one sequence that is cut evenly over the grid
-//    (block b of B <= T takes [b T / B, (b + 1) T / B)), whatever the lengths; a
-//    producer warp walks a block's range with TMA, across item borders, and the
-//    consumer warps write one fp32 partial per item that they touch.  Walking on
-//    either starts a new block or a new item, so (block + item) numbers the
-//    partials without a table.
+//    batch has few rows.  Work is a list of items, each a run of 64-key tiles,
+//    alike for every key head:
+//      prefix items: a tile of the rows above;
+//      own items:    (sample, tile of its query rows).
+//    The tiles of a head's items form one sequence that is cut evenly over groups
+//    of blocks (group g of B <= T takes [g T / B, (g + 1) T / B)), whatever the
+//    lengths; the blocks of a group each take a head, so that the heads' rows of
+//    one place, which lie side by side in memory, are read at about the same time
+//    (block by block over one head's keys after the other's, 128-byte rows came in at
+//    4.4 TB/s).  A producer warp walks a block's range with TMA, across item
+//    borders, and the consumer warps write one fp32 partial per item that they
+//    touch.  Walking on either starts a new group or a new item, so (group + item)
+//    numbers a head's partials without a table.
 //  paged_join_kernel adds the partials of each row in a fixed order (the result
 //    does not depend on scheduling) and rounds once.
 //
@@ -49,8 +53,10 @@ struct PagedParams {
     int pages, page_shift, max_pages, prefix_pages;
     float alpha, bias, cap;
     const float *bias_z, *slopes;
-    float *part;          // [block + item][kPagedPartRows][D]
-    int2 *blocks_of;      // [item] first and last block of each item that has tiles
+    float *part;          // [key head][group + item][kPagedPartRows][D]
+    int2 *groups_of;      // [key head][item] first and last group of each item that has tiles
+    int heads_wide;       // blocks of a group: the key heads, or the grid where it has fewer
+    int groups, items;    // groups of the grid; items of a head
     int prefix_warps, own_warps;   // warps along the rows (1, 2, 4): row tiles of 16 times that
     int prefix_rt, own_rt;         // row tiles of the prefix and of a sample, per key head
     // the prefix kernel, when it runs (splits > 0; the tile kernel then leaves the prefix out)
@@ -113,9 +119,9 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 
 // The shape of the item list.
 struct PagedPlan {
-    int prefix_tiles, prefix_rows, prefix_rt, prefix_items;   // tiles of the prefix; rows per tile; row tiles; items
+    int prefix_tiles, prefix_rows, prefix_rt;   // tiles of the prefix; rows of a row tile; row tiles, an item each
     int own_rows, own_rt;
-    int64_t own_first;        // tiles of all prefix items: where own items begin
+    int64_t own_first;        // tiles of a head's prefix items: where own items begin
 };
 __device__ __forceinline__ PagedPlan paged_plan(const PagedParams &p, int prefix) {
     PagedPlan a;
@@ -123,36 +129,32 @@ __device__ __forceinline__ PagedPlan paged_plan(const PagedParams &p, int prefix
     a.prefix_tiles = (prefix + kPagedTile - 1) / kPagedTile;
     a.prefix_rows = 16 * p.prefix_warps;
     a.prefix_rt = p.prefix_rt;
-    a.prefix_items = a.prefix_rt * p.Hk;
     a.own_rows = 16 * p.own_warps;
     a.own_rt = p.own_rt;
-    a.own_first = static_cast<int64_t>(a.prefix_tiles) * a.prefix_items;
+    a.own_first = static_cast<int64_t>(a.prefix_tiles) * a.prefix_rt;
     return a;
 }
 
-// A place in the tile sequence.
+// A place in the tile sequence of key head kvh.
 struct PagedCursor {
-    int item;             // number of the item
+    int item;             // number of the item among the head's
     int z;                // sample of an own item, -1 for a prefix item
     int kvh, rt, tile, tiles;
 };
 
-__device__ __forceinline__ PagedCursor paged_locate(const PagedParams &p, const PagedPlan &a, const int *before,
-                                                    int64_t t) {
+__device__ __forceinline__ PagedCursor paged_locate(const PagedPlan &a, int Z, const int *before, int kvh, int64_t t) {
     PagedCursor c;
+    c.kvh = kvh;
     if (t < a.own_first) {
-        c.item = static_cast<int>(t / a.prefix_tiles);
+        c.item = c.rt = static_cast<int>(t / a.prefix_tiles);
         c.z = -1;
-        c.kvh = c.item / a.prefix_rt;
-        c.rt = c.item % a.prefix_rt;
         c.tile = static_cast<int>(t % a.prefix_tiles);
         c.tiles = a.prefix_tiles;
         return c;
     }
-    const int per = p.Hk * a.own_rt;    // items of a sample
     const int64_t u = t - a.own_first;
-    const int at = static_cast<int>(u / per);
-    int lo = 0, hi = p.Z - 1;           // the last sample with before[z] <= at
+    const int at = static_cast<int>(u / a.own_rt);
+    int lo = 0, hi = Z - 1;             // the last sample with before[z] <= at
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (before[mid] <= at) lo = mid;
@@ -160,29 +162,24 @@ __device__ __forceinline__ PagedCursor paged_locate(const PagedParams &p, const 
     }
     c.z = lo;
     c.tiles = before[lo + 1] - before[lo];
-    const int64_t in = u - static_cast<int64_t>(before[lo]) * per;
-    const int i = static_cast<int>(in / c.tiles);
+    const int64_t in = u - static_cast<int64_t>(before[lo]) * a.own_rt;
+    c.rt = static_cast<int>(in / c.tiles);
     c.tile = static_cast<int>(in % c.tiles);
-    c.kvh = i / a.own_rt;
-    c.rt = i % a.own_rt;
-    c.item = a.prefix_items + lo * per + i;
+    c.item = a.prefix_rt + lo * a.own_rt + c.rt;
     return c;
 }
 
 // The next tile; the caller knows that there is one.
-__device__ __forceinline__ void paged_next(const PagedParams &p, const PagedPlan &a, const int *before,
-                                           PagedCursor &c) {
+__device__ __forceinline__ void paged_next(const PagedPlan &a, const int *before, PagedCursor &c) {
     if (++c.tile < c.tiles) return;
     c.tile = 0;
     ++c.item;
     if (++c.rt < (c.z < 0 ? a.prefix_rt : a.own_rt)) return;
     c.rt = 0;
-    if (++c.kvh < p.Hk) return;
-    c.kvh = 0;
     do {
         ++c.z;            // from -1: the first sample
-        c.tiles = c.z < p.Z ? before[c.z + 1] - before[c.z] : 1;
-        c.item = a.prefix_items + c.z * p.Hk * a.own_rt;
+        c.tiles = before[c.z + 1] - before[c.z];
+        c.item = a.prefix_rt + c.z * a.own_rt;
     } while (c.tiles == 0);
 }
 
@@ -406,15 +403,29 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
     __syncthreads();
     const int prefix = paged_prefix(p);
     const PagedPlan a = paged_plan(p, prefix);
-    const int64_t total = a.own_first + static_cast<int64_t>(carry) * p.Hk * a.own_rt;
-    const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);   // each has at least one tile
-    if (blockIdx.x >= blocks) {
+    const int64_t total = a.own_first + static_cast<int64_t>(carry) * a.own_rt;
+    const int64_t groups = min(static_cast<int64_t>(p.groups), total);   // each has at least one tile
+    const int group = blockIdx.x / p.heads_wide, head0 = blockIdx.x % p.heads_wide;
+    if (group >= groups) {
         grid_wait();
         return;
     }
-    const int64_t t0 = total * blockIdx.x / blocks;
-    const int count = static_cast<int>(total * (blockIdx.x + 1) / blocks - t0);
-    PagedCursor now = paged_locate(p, a, before, t0);
+    // this block's range, the same for each of its heads
+    const int64_t t0 = total * group / groups;
+    const int range = static_cast<int>(total * (group + 1) / groups - t0);
+    const int count = range * ((p.Hk - 1 - head0) / p.heads_wide + 1);
+    const PagedCursor start = paged_locate(a, p.Z, before, head0, t0);
+    PagedCursor now = start;
+    // tile `done` of the block's; the caller knows that there is one
+    auto advance = [&](int done) {
+        if (done % range != 0) {
+            paged_next(a, before, now);
+        } else {
+            const int kvh = now.kvh + p.heads_wide;
+            now = start;
+            now.kvh = kvh;
+        }
+    };
     auto keys_of = [&](const PagedCursor &c) { return c.z < 0 ? prefix : paged_lengths(p, c.z).x; };
     const WaitCtx wctx{abort_flag, p.status, p.timeout_ns};
 
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
         int keys = 0, issued = 0;
         const int *table = nullptr;
         for (int t = 0; t < count; ++t) {
-            if (t == 0 || now.tile == 0) {
+            if (t % range == 0 || now.tile == 0) {
                 keys = keys_of(now);
                 table = now.z < 0 ? p.prefix_table : p.page_table + static_cast<size_t>(now.z) * p.max_pages;
                 // the query rows that the consumers will want for this item, a line per lane
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
             }
             __syncwarp();
             issued = t + 1;
-            if (issued < count) paged_next(p, a, before, now);
+            if (issued < count) advance(issued);
         }
         // every issued load must land before the block's shared memory is released
         for (int t = (issued > S ? issued - S : 0); t < issued; ++t)
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
         PagedItem<D, SCORE, WM> it;
         const PagedCursor c = now;
         const int keys = keys_of(c);
-        if (tid == 0 && c.tile == 0) p.blocks_of[c.item].x = blockIdx.x;
+        if (tid == 0 && c.tile == 0) p.groups_of[c.kvh * p.items + c.item].x = group;
         it.begin(p, c, prefix);
         for (;;) {
             const int s = t % S;
@@ -489,12 +500,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedLayout<D>::kBlocksPerSm)
             it.tile(smem_u32(st), smem_u32(st + Lay::kOperand), now.tile * kPagedTile);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
-            if (tid == 0 && now.tile == now.tiles - 1) p.blocks_of[c.item].y = blockIdx.x;
+            if (tid == 0 && now.tile == now.tiles - 1) p.groups_of[c.kvh * p.items + c.item].y = group;
             if (++t >= count) break;
-            paged_next(p, a, before, now);
-            if (now.item != c.item) break;
+            advance(t);
+            if (now.item != c.item || now.kvh != c.kvh) break;
         }
-        it.end(p.part + (static_cast<size_t>(blockIdx.x) + c.item) * kPagedPartRows * D);
+        it.end(p.part + (static_cast<size_t>(c.kvh) * (p.groups + p.items) + group + c.item) * kPagedPartRows * D);
     };
     while (t < count) {
         const int w = now.z < 0 ? p.prefix_warps : p.own_warps;
@@ -774,7 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const unsigned kvh = h / p.group, g = h % p.group;
     const unsigned own_row = l * p.group + g;
     const unsigned own_rows = 16 * p.own_warps, prefix_rows = 16 * p.prefix_warps;
-    const unsigned own_item = p.prefix_rt * p.Hk + (z * p.Hk + kvh) * p.own_rt + own_row / own_rows;
+    const unsigned own_item = p.prefix_rt + z * p.own_rt + own_row / own_rows;
     const int2 n = paged_lengths(p, z);
     const int prefix = paged_prefix(p);
     const bool live = there && static_cast<int>(l) < n.y;
@@ -802,10 +813,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         }
     };
     // partials of row `row` of an item's `rows`: the warps along the keys lie `rows`
-    // rows apart, the blocks kPagedPartRows
+    // rows apart, the groups kPagedPartRows
     auto add = [&](unsigned item, unsigned row, unsigned rows) {
-        const int2 b = __ldcg(&p.blocks_of[item]);
-        sum(p.part + (static_cast<size_t>(b.x + item) * kPagedPartRows + row) * D + lane * E,
+        const int2 b = __ldcg(&p.groups_of[kvh * p.items + item]);
+        const size_t slot = static_cast<size_t>(kvh) * (p.groups + p.items) + b.x + item;
+        sum(p.part + (slot * kPagedPartRows + row) * D + lane * E,
             static_cast<size_t>(rows) * D, (b.y - b.x + 1) * static_cast<int>(kPagedPartRows / rows));
     };
     grid_wait();
@@ -818,7 +830,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
                 static_cast<size_t>(p.Hk) * p.pairs * 256 * D, S);
         } else if (prefix > 0) {
             const unsigned row = tok * p.group + g;
-            add(kvh * p.prefix_rt + row / prefix_rows, row % prefix_rows, prefix_rows);
+            add(row / prefix_rows, row % prefix_rows, prefix_rows);
         }
         add(own_item, own_row % own_rows, own_rows);     // a live row has at least its own key
     }
