@@ -321,7 +321,12 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
         p.prefix_part = reinterpret_cast<float *>(ws + groups_bytes(z, Hk) + part_bytes(z, Hk, D));
         p.tile_tokens = z.tile_tokens;
         p.pairs = static_cast<int>(z.pairs);
-        p.splits = static_cast<int>(std::max<int64_t>(1, sms / (z.pairs * Hk)));
+        // as many splits as SMs allow, but no more than a full prefix needs to give each
+        // the same number of tiles: the others would only add partials
+        const int64_t most = std::max<int64_t>(1, sms / (z.pairs * Hk));
+        const int64_t tiles = ((static_cast<int64_t>(prefix_pages) << p.page_shift) + 127) / 128;
+        const int64_t each = (tiles + most - 1) / most;
+        p.splits = static_cast<int>((tiles + each - 1) / each);
         const int box = std::min(page_size, 128);
         if ((s = encode_pages(&m.prefix_k, k_pages, c, box)) != SIGATTN_OK) return s;
         if ((s = encode_pages(&m.prefix_v, v_pages, c, box)) != SIGATTN_OK) return s;

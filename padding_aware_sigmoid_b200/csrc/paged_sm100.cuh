@@ -112,11 +112,6 @@ __device__ __forceinline__ int2 paged_lengths(const PagedParams &p, int z) {
     return make_int2(nk, nq);
 }
 
-// Lets the next kernel of the stream start, and waits until the one before has
-// finished (both do nothing where the launch did not ask for it).
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The shape of the item list.
 struct PagedPlan {
     int prefix_tiles, prefix_rows, prefix_rt;   // tiles of the prefix; rows of a row tile; row tiles, an item each
@@ -550,9 +545,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     grid_release();     // the tile kernel reads nothing of this one's
     const int prefix = paged_prefix(p);
     const int T = (prefix + 127) / 128, S = min(p.splits, T);
-    if (split >= S) return;
-    const int J0 = static_cast<int>(static_cast<int64_t>(T) * split / S);
-    const int steps = static_cast<int>(static_cast<int64_t>(T) * (split + 1) / S) - J0;
+    const int J0 = split < S ? static_cast<int>(static_cast<int64_t>(T) * split / S) : 0;
+    const int steps = split < S ? static_cast<int>(static_cast<int64_t>(T) * (split + 1) / S) - J0 : 0;
     const bool ragged = (prefix & 127) != 0 && J0 + steps == T;
     const int64_t tokens = static_cast<int64_t>(p.Z) * p.L;
     const int64_t tok0 = static_cast<int64_t>(pair) * 2 * p.tile_tokens;
@@ -590,6 +584,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx wctx{abort_flag, p.status, p.timeout_ns};
+    if (steps == 0) {
+        // more splits than tiles (the prefix's length was not needed before this point, so
+        // that its load overlaps the set-up)
+        if (warp == 1) tmem_dealloc(tmem, Lay::TMEM_COLS);
+        return;
+    }
 
     if (warp == 0) {
         if (lane == 0) {

@@ -270,11 +270,13 @@ sigattn_status sigattn_bwd_span(const void *q, const void *k, const void *v, con
     p.hull = hull;
     p.timeout_ns = g_timeout_ns.load();
     if ((s = launch(span_prep_kernel, dim3(tiles, Z), dim3(128), 0, st, p.src, clean, hull)) != SIGATTN_OK) return s;
-    p.heads_first = heads_first(a, 2, tiles);
-    s = launch_span_dq(kind_of(a), p.heads_first ? dim3(H, tiles, Z) : dim3(tiles, H, Z), mq, mk, mv, mdo, p, st);
-    if (s != SIGATTN_OK) return s;
+    // dK/dV first: its blocks are the longer ones (a key head's queries of all its
+    // heads), and dQ's fill in behind them
     p.heads_first = heads_first(a, 2 * p.group, tiles);
-    return launch_span_dkdv(kind_of(a), p.heads_first ? dim3(Hk, tiles, Z) : dim3(tiles, Hk, Z), mq, mk, mv, mdo, p, st);
+    s = launch_span_dkdv(kind_of(a), p.heads_first ? dim3(Hk, tiles, Z) : dim3(tiles, Hk, Z), mq, mk, mv, mdo, p, st);
+    if (s != SIGATTN_OK) return s;
+    p.heads_first = heads_first(a, 2, tiles);
+    return launch_span_dq(kind_of(a), p.heads_first ? dim3(H, tiles, Z) : dim3(tiles, H, Z), mq, mk, mv, mdo, p, st);
 }
 
 sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix, const int32_t *docs, int causal,

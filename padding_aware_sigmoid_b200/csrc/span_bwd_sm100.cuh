@@ -14,6 +14,13 @@
 //    the contraction side (K in dQ; Q and dO in dK/dV), so that NaN in padding
 //    never meets a weight of zero.
 //
+//  - the three kernels overlap (programmatic dependent launch): dK/dV starts
+//    beside the table kernel and waits for it, dQ beside dK/dV's last blocks,
+//    which its shorter blocks fill in behind.  Against dQ first and one kernel
+//    after the other: packed capped D = 64 documents 157.6 -> 134.2 us, capped prefix
+//    D = 128 638 -> 547 us, documents of 4096 rows at D = 128 252.5 -> 197 us, causal 8K at
+//    D = 128 1860 -> 1840 us.
+//
 // Bound: dQ issues 6 D and dK/dV 8 D tensor FLOP per pair against one MUFU op
 // (two with a cap): tensor-bound at D = 128, near the MUFU's rate at D = 64.
 #pragma once
@@ -42,6 +49,7 @@ struct SpanBwdParams {
 // greatest lo <= k0 and least hi >= k1.
 static __global__ void __launch_bounds__(128) span_prep_kernel(const SpanSource src, int2 *clean, int4 *hull) {
     __shared__ int4 part[4];
+    grid_release();
     const int z = blockIdx.y, i = blockIdx.x * 128 + threadIdx.x;
     const int n = span_tokens(src, z);
     const int2 r = row_span(src, z, i, n);
@@ -286,10 +294,12 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
     const int qtile = tiles - 1 - static_cast<int>(p.heads_first ? blockIdx.y : blockIdx.x);
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
-    const int4 hull = p.hull[static_cast<size_t>(z) * tiles + qtile];
+    const bool last = blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
+    const int4 hull = __ldg(&p.hull[static_cast<size_t>(z) * tiles + qtile]);
     if (hull.y == 0) {
         // no row of this tile sees a key: zeros, written by every thread
         zero_rows<D>(p.dq, z, h, qtile * 128, min(128, L - qtile * 128), L, p.H);
+        if (last) grid_wait();
         return;
     }
     const int J0 = hull.x / 128, steps = (hull.y + 127) / 128 - J0;
@@ -313,12 +323,13 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
-    }
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmQ);
-        prefetch_tensormap(&tmK);
-        prefetch_tensormap(&tmV);
-        prefetch_tensormap(&tmDO);
+        // the resident tiles fly while the rest of the block sets up
+        uint8_t *sQ = smem + Lay::OFF_A, *sDO = smem + Lay::OFF_B;
+        mbar_arrive_expect_tx(res_full, 2 * Lay::TILE_BYTES);
+        for (int s = 0; s < Lay::NSUB; ++s) {
+            tma_load_4d(&tmQ, res_full, sQ + s * Lay::SUB_BYTES, 64 * s, h, qtile * 128, z);
+            tma_load_4d(&tmDO, res_full, sDO + s * Lay::SUB_BYTES, 64 * s, h, qtile * 128, z);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Lay::TMEM_COLS);
@@ -332,12 +343,6 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            uint8_t *sQ = smem + Lay::OFF_A, *sDO = smem + Lay::OFF_B;
-            mbar_arrive_expect_tx(res_full, 2 * Lay::TILE_BYTES);
-            for (int s = 0; s < Lay::NSUB; ++s) {
-                tma_load_4d(&tmQ, res_full, sQ + s * Lay::SUB_BYTES, 64 * s, h, qtile * 128, z);
-                tma_load_4d(&tmDO, res_full, sDO + s * Lay::SUB_BYTES, 64 * s, h, qtile * 128, z);
-            }
             int ix = 0;
             for (int r = 0; r < steps; ++r) {
                 if (!span_ring_load<SX, Lay::NSUB>(&tmK, x_full, x_empty, smem + Lay::OFF_X, Lay::TILE_BYTES, r,
@@ -454,6 +459,9 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, Lay::TMEM_COLS);
     }
+    // whatever follows on the stream waits for this kernel alone: it has to end after
+    // the dK/dV kernel, beside whose last blocks it may have started
+    if (last) grid_wait();
 }
 
 // dK/dV: one CTA per 128-key tile of a key head; streams the query tiles that
@@ -493,6 +501,8 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     const int k0 = ktile * 128, k1 = min(k0 + 128, n);
+    grid_wait();        // span_prep_kernel's tables
+    grid_release();     // dQ needs nothing else of this kernel
     // first and last query tile whose hull meets this key tile
     const int4 *hull = p.hull + static_cast<size_t>(z) * tiles;
     {
@@ -542,12 +552,13 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
-    }
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmQ);
-        prefetch_tensormap(&tmK);
-        prefetch_tensormap(&tmV);
-        prefetch_tensormap(&tmDO);
+        // the resident tiles fly while the rest of the block sets up
+        uint8_t *sK = smem + Lay::OFF_A, *sV = smem + Lay::OFF_B;
+        mbar_arrive_expect_tx(res_full, 2 * Lay::TILE_BYTES);
+        for (int s = 0; s < Lay::NSUB; ++s) {
+            tma_load_4d(&tmK, res_full, sK + s * Lay::SUB_BYTES, 64 * s, kvh, k0, z);
+            tma_load_4d(&tmV, res_full, sV + s * Lay::SUB_BYTES, 64 * s, kvh, k0, z);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Lay::TMEM_COLS);
@@ -561,12 +572,6 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            uint8_t *sK = smem + Lay::OFF_A, *sV = smem + Lay::OFF_B;
-            mbar_arrive_expect_tx(res_full, 2 * Lay::TILE_BYTES);
-            for (int s = 0; s < Lay::NSUB; ++s) {
-                tma_load_4d(&tmK, res_full, sK + s * Lay::SUB_BYTES, 64 * s, kvh, k0, z);
-                tma_load_4d(&tmV, res_full, sV + s * Lay::SUB_BYTES, 64 * s, kvh, k0, z);
-            }
             int ix = 0, i = I0, h = kvh * p.group;
             for (int r = 0; r < steps; ++r) {
                 if (!span_ring_load<SX, Lay::NSUB>(&tmQ, x_full, x_empty, smem + Lay::OFF_X, Lay::TILE_BYTES, r,

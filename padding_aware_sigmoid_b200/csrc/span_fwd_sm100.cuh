@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
     const int qtile0 = NT * static_cast<int>(p.heads_first ? gridDim.y - 1 - blockIdx.y : gridDim.x - 1 - blockIdx.x);
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
+    const int loads = min(max((n + 127) / 128 - qtile0, 0), NT);     // query tiles below n
     if (warp < 4 * NT) {
         const int2 r = row_span(p.src, z, qtile0 * 128 + static_cast<int>(threadIdx.x), n);
         const int lo = __reduce_min_sync(0xffffffffu, r.x < r.y ? r.x : INT_MAX);
@@ -133,6 +134,12 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
+        // the query tiles fly while the rest of the block sets up
+        if (loads > 0) mbar_arrive_expect_tx(q_full, loads * Lay::TILE_BYTES);
+        for (int t = 0; t < loads; ++t)
+            for (int s = 0; s < Lay::NSUB; ++s)
+                tma_load_4d(&tmQ, q_full, smem + Lay::OFF_Q + t * Lay::TILE_BYTES + s * Lay::SUB_BYTES, 64 * s, h,
+                            (qtile0 + t) * 128, z);
     }
     __syncthreads();
     // key tiles [j0[t], j1[t]) of query tile t, and [J0, J1) of all; an empty tile
@@ -165,13 +172,13 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
                                                    static_cast<size_t>(h) * D);
             dst[e % V4] = make_uint4(0u, 0u, 0u, 0u);
         }
+        if (threadIdx.x == 0 && loads > 0) mbar_wait_drain(q_full, 0, p.timeout_ns);
         return;
     }
     const int steps = J1 - J0;
     // the last key tile, when n ends inside it: its value rows are cleaned
     const bool ragged = (n & 127) != 0 && J1 == (n + 127) / 128;
     if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
@@ -187,16 +194,7 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
 
     if (warp == 0) {
         if (lane == 0) {
-            uint8_t *sQ = smem + Lay::OFF_Q;
             uint8_t *sK = smem + Lay::OFF_K;
-            mbar_arrive_expect_tx(q_full, live * Lay::TILE_BYTES);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (j1[t] == 0) continue;
-                for (int s = 0; s < Lay::NSUB; ++s)
-                    tma_load_4d(&tmQ, q_full, sQ + t * Lay::TILE_BYTES + s * Lay::SUB_BYTES, 64 * s, h,
-                                (qtile0 + t) * 128, z);
-            }
             int issued = 0;
             for (int r = 0; r < steps; ++r) {
                 const int sk = r % KS;

@@ -169,6 +169,11 @@ __device__ __forceinline__ float2 score_p2(float s0, float s1, const ScoreCoef &
     return sigma2<kSigmoidExp>(score_arg2<kSigmoidExp, SCORE, false>(s0, s1, cf, rel, f));
 }
 
+// Lets the next kernel of the stream start, and waits until the one before has
+// finished (both do nothing where the launch did not ask for it).
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ spans
 
 // Where the kernels take a batch's masks from.  spans null: every row of a
