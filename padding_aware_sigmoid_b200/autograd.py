@@ -51,6 +51,29 @@ class _SigmoidAttentionBiasFn(torch.autograd.Function):
         return dq, dk, dv, None, None, None, db
 
 
+class _SpanAttentionFn(torch.autograd.Function):
+    """The masked attention (``fwd_span`` / ``bwd_span``).  Gradients for q, k and
+    v; the bias and the slopes are constants here."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, seqlens, spans, slopes, alpha, bias, cap):
+        from . import fwd_span
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        out = fwd_span(q, k, v, seqlens, alpha, bias, spans=spans, cap=cap, slopes=slopes)
+        bias_z = bias if isinstance(bias, torch.Tensor) else None
+        ctx.save_for_backward(q, k, v, seqlens, spans, slopes, bias_z)
+        ctx.alpha, ctx.bias, ctx.cap = alpha, None if bias_z is not None else bias, cap
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        from . import bwd_span
+        q, k, v, n, spans, slopes, bias_z = ctx.saved_tensors
+        grads = bwd_span(q, k, v, dout.contiguous(), n, ctx.alpha, ctx.bias if bias_z is None else bias_z,
+                         spans=spans, cap=ctx.cap, slopes=slopes)
+        return (*grads, None, None, None, None, None, None)
+
+
 class SigmoidAttention(torch.nn.Module):
     """sigma(alpha Q K^T + b) V over padded [Z, L, H, D] batches.
 
@@ -64,12 +87,27 @@ class SigmoidAttention(torch.nn.Module):
       db = sum_z db_z, created here with the initial value ``bias``, or -ln
       ``max_len`` (the padded length the module will see) when ``bias`` is not
       given, so that an optimiser built from ``parameters()`` before the first
-      call already holds it."""
+      call already holds it.
+
+    ``cap`` > 0 caps the scores, cap tanh(alpha q . k / cap), and ``slopes`` (one
+    number per head) takes slopes[h] |i - j| off them; both are constants.  A call
+    with ``spans`` (``mask_spans``: causal, prefix, document and window masks), or
+    with k and v of fewer heads, which groups of query heads share, runs the
+    masked attention as well; it needs one length per sample for queries and
+    keys, and a bias that is not learned."""
 
     def __init__(self, alpha: float | None = None, bias: float | None = None,
                  per_sample_bias: bool = False, learnable_bias: bool = False,
-                 max_len: int | None = None):
+                 max_len: int | None = None, cap: float = 0.0, slopes=None):
         super().__init__()
+        if learnable_bias and (cap or slopes is not None):
+            raise ValueError("a learned bias goes with neither cap nor slopes")
+        self.cap = float(cap)
+        if self.cap < 0 or not math.isfinite(self.cap):
+            raise ValueError("cap must be 0 or a positive finite number")
+        self.register_buffer("slopes", None if slopes is None else
+                             torch.as_tensor(slopes, dtype=torch.float32).detach().clone().reshape(-1),
+                             persistent=False)
         if per_sample_bias and learnable_bias:
             raise ValueError("choose per_sample_bias or learnable_bias, not both")
         self.alpha, self.bias = alpha, bias
@@ -83,7 +121,9 @@ class SigmoidAttention(torch.nn.Module):
             init = float(bias) if bias is not None else -math.log(max_len)
             self.b = torch.nn.Parameter(torch.tensor(init))
 
-    def forward(self, q, k, v, seqlens_q, seqlens_k=None):
+    def forward(self, q, k, v, seqlens_q, seqlens_k=None, spans=None):
+        if spans is not None or self.cap or self.slopes is not None or k.shape[2] != q.shape[2]:
+            return self._masked(q, k, v, seqlens_q, seqlens_k, spans)
         if seqlens_k is None:
             seqlens_k = seqlens_q
         Z, L, D = q.shape[0], q.shape[1], q.shape[-1]
@@ -97,3 +137,17 @@ class SigmoidAttention(torch.nn.Module):
             return _SigmoidAttentionBiasFn.apply(q, k, v, seqlens_q, seqlens_k, alpha, bias_z)
         bias = -math.log(L) if self.bias is None else self.bias
         return _SigmoidAttentionFn.apply(q, k, v, seqlens_q, seqlens_k, alpha, float(bias))
+
+    def _masked(self, q, k, v, seqlens, seqlens_k, spans):
+        if seqlens_k is not None and seqlens_k is not seqlens:
+            raise ValueError("the masked attention takes one length per sample, for queries and keys")
+        if self.learnable_bias:
+            raise ValueError("the masked attention has no gradient for a learned bias")
+        alpha = float(1.0 / math.sqrt(q.shape[-1]) if self.alpha is None else self.alpha)
+        if self.per_sample_bias:
+            from . import log_length_bias
+            bias = log_length_bias(seqlens)
+        else:
+            bias = float(-math.log(q.shape[1]) if self.bias is None else self.bias)
+        slopes = None if self.slopes is None else self.slopes.to(q.device)
+        return _SpanAttentionFn.apply(q, k, v, seqlens, spans, slopes, alpha, bias, self.cap)

@@ -302,3 +302,73 @@ def test_mask_spans(dev, L):
         got = sa.mask_spans(seq, L, causal=causal, prefix=None if prefix is None else pd,
                             docs=None if doc is None else dd, window=window)
         assert np.array_equal(got.cpu().numpy(), _by_rule(n, L, causal, prefix, doc, min(window, L)))
+
+
+@pytest.mark.parametrize("per_sample", [False, True])
+def test_module_runs_the_masked_attention_with_its_gradients(dev, per_sample):
+    """The autograd module's outputs and gradients are the calls' own, for strided inputs and a strided output gradient too."""
+    Z, L, H, Hk, D = 2, 200, 6, 2, 64
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 61)
+    seq = torch.as_tensor(np.asarray([200, 91], np.int32), device=dev)
+    spans = sa.mask_spans(seq, L, causal=True)
+    slopes = torch.linspace(0.4, 0.01, H)
+    attn = sa.SigmoidAttention(per_sample_bias=per_sample, bias=None if per_sample else -3.0, cap=25.0, slopes=slopes)
+    leaves = [t.transpose(1, 2).contiguous().requires_grad_() for t in (q, k, v)]
+    out = attn(*(t.transpose(1, 2) for t in leaves), seq, spans=spans)
+    out.backward(do.transpose(1, 2).contiguous().transpose(1, 2))
+    bias = sa.log_length_bias(seq) if per_sample else -3.0
+    args = dict(spans=spans, cap=25.0, slopes=slopes.to(dev))
+    assert torch.equal(out, sa.fwd_span(q, k, v, seq, D ** -0.5, bias, **args))
+    for leaf, want in zip(leaves, sa.bwd_span(q, k, v, do, seq, D ** -0.5, bias, **args)):
+        assert torch.equal(leaf.grad.transpose(1, 2), want)
+
+
+def test_module_shares_key_heads_without_a_mask(dev):
+    Z, L, H, Hk, D = 2, 130, 4, 1, 128
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 62)
+    seq = torch.as_tensor(np.asarray([130, 7], np.int32), device=dev)
+    out = sa.SigmoidAttention(bias=-2.0)(q, k, v, seq)
+    assert torch.equal(out, sa.fwd_span(q, k, v, seq, D ** -0.5, -2.0))
+
+
+def test_calls_refuse_what_does_not_fit(dev):
+    Z, L, H, Hk, D = 2, 40, 4, 2, 64
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 63)
+    seq = torch.as_tensor(np.asarray([40, 7], np.int32), device=dev)
+    ok = lambda **a: sa.fwd_span(a.pop("q", q), a.pop("k", k), a.pop("v", v), a.pop("n", seq), 0.1, a.pop("b", 0.0), **a)  # noqa: E731
+    ok()
+    bad = [dict(q=q.float()), dict(k=k[:, :20]), dict(v=v[..., :32]), dict(q=q.transpose(1, 2)), dict(k=k.cpu()),
+           dict(n=seq.long()), dict(n=seq[:1]), dict(spans=torch.zeros(Z, L, 2, device=dev)),
+           dict(spans=torch.zeros(Z, L, 1, dtype=torch.int32, device=dev)), dict(slopes=torch.zeros(H - 1, device=dev)),
+           dict(slopes=torch.zeros(H, device=dev, dtype=torch.float64)), dict(b=torch.zeros(Z + 1, device=dev)),
+           dict(out=torch.empty_like(q).float()), dict(out=torch.empty_like(k)), dict(k=k[:, :, :1].expand(-1, -1, 3, -1).contiguous())]
+    for args in bad:
+        with pytest.raises(ValueError):
+            ok(**args)
+    with pytest.raises(TypeError):
+        sa.fwd_span(q.half(), k.half(), v.half(), seq, 0.1, 0.0)
+    for cap in (-1.0, float("nan"), float("inf")):
+        with pytest.raises(sa.SigattnError):
+            ok(cap=cap)
+    with pytest.raises(sa.SigattnError):
+        sa.bwd_span(q, k, v, do, seq, 0.1, 0.0, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
+    with pytest.raises(ValueError):
+        sa.mask_spans(seq, L, prefix=seq, window=3)
+    with pytest.raises(ValueError):
+        sa.SigmoidAttention()(q, k, v, seq, seq.clone())
+    assert sa.last_device_status() == 0
+
+
+def test_long_rows_pass_the_tail_of_the_grid(dev):
+    """More 128-row tiles than a grid's y and z sizes were chosen for, one head: the last rows count what they see."""
+    Z, L, D = 1, 70000, 64
+    n = np.asarray([L - 5], np.int32)
+    seq = torch.as_tensor(n, device=dev)
+    spans = sa.mask_spans(seq, L, causal=True, window=200)
+    q = torch.zeros(Z, L, 1, D, device=dev, dtype=torch.bfloat16)
+    v = torch.zeros_like(q)
+    v[..., 0] = 2.0
+    o = sa.fwd_span(q, q, v, seq, 1.0, 0.0, spans=spans)[0, :, 0, 0].float().cpu()
+    want = torch.clamp(torch.arange(L) + 1, max=200).float()
+    want[L - 5:] = 0
+    assert torch.equal(o, want.to(torch.bfloat16).float())

@@ -76,3 +76,19 @@ def test_binding_refuses_cpu_tensors_and_uneven_heads(sa):
         sa.bwd_span(t(2), t(2), t(2), t(2), n, 1.0, 0.0)
     with pytest.raises(ValueError, match="CUDA"):
         sa.mask_spans(n, 8)
+
+
+def test_masked_module_refuses_what_has_no_gradient(sa):
+    with pytest.raises(ValueError, match="learned bias"):
+        sa.SigmoidAttention(learnable_bias=True, bias=-1.0, cap=20.0)
+    with pytest.raises(ValueError, match="cap"):
+        sa.SigmoidAttention(cap=-1.0)
+    m = sa.SigmoidAttention(learnable_bias=True, bias=-1.0)
+    x = torch.zeros(1, 4, 2, 64)
+    n = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="learned bias"):
+        m(x, x[:, :, :1], x[:, :, :1], n)
+    with pytest.raises(ValueError, match="one length"):
+        sa.SigmoidAttention()(x, x[:, :, :1], x[:, :, :1], n, n.clone())
+    assert sa.SigmoidAttention(slopes=[0.5, 0.25]).slopes.tolist() == [0.5, 0.25]
+    assert not sa.SigmoidAttention(slopes=[0.5]).state_dict()
