@@ -72,12 +72,52 @@ static __global__ void __launch_bounds__(128) span_prep_kernel(const SpanSource 
     }
 }
 
-template <int D>
-struct SpanBwdLayout : BwdLayout<D, BwdStages<D>::X, BwdStages<D>::Y> {
-    using Base = BwdLayout<D, BwdStages<D>::X, BwdStages<D>::Y>;
-    static constexpr int OFF_HULL = (Base::OFF_SAMPLE + 7) & ~7;   // {first, last} of each warp
-    static constexpr int SMEM_ALLOC = OFF_HULL + 32 * 8 + 1024;
-    static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+// Shape of the backward blocks.  A step is kStep columns of a streamed 128-row
+// tile (keys in dQ, queries in dK/dV): the whole tile, but half of it in dQ at D =
+// 64, so that scores and accumulator take 256 columns of tensor memory and two
+// blocks share an SM; one's start and end, most of a short document's time, pass
+// while the other computes.  Whole backward, against one block an SM: packed capped
+// documents 133.6 -> 119.1 us, documents 130.7 -> 128.2 us, window 8K 202 -> 200 us;
+// causal 8K 431 -> 440 us, full capped 4K 620 -> 648 us (half steps hand over twice as
+// often).  The same in dK/dV, whose threads hold more, spilled at 80 registers and
+// lost 6 to 25%.
+template <int D, bool DQ>
+struct SpanBwdShape {
+    static constexpr bool kHalf = DQ && D == 64;
+    static constexpr int kPerSm = kHalf ? 2 : 1;
+    static constexpr int kStep = kHalf ? 64 : 128, kParts = 128 / kStep;
+    static constexpr int NG = D == 64 && !kHalf ? 4 : 2;     // sigma warpgroups, kCols columns of a step each
+    static constexpr int kThreads = 128 + 128 * NG, kArrivals = 128 * NG;
+    static constexpr int kCols = kStep / NG, kPacked = kCols / 2;
+    static constexpr int SX = kHalf ? 2 : BwdStages<D>::X, SY = kHalf ? 2 : BwdStages<D>::Y;
+    // TMEM column (relative to the buffer) of the packed bf16 values of K step kk
+    // (columns 16 kk ... of the step), over the first kPacked of their warpgroup's
+    static __device__ __forceinline__ uint32_t packed_col(int kk) {
+        return kCols * ((16 * kk) / kCols) + ((16 * kk) % kCols) / 2;
+    }
+};
+
+template <int D, bool DQ>
+struct SpanBwdLayout {
+    using SG = SpanBwdShape<D, DQ>;
+    static constexpr int NSUB = D / 64;
+    static constexpr int SUB_BYTES = 128 * 64 * 2;
+    static constexpr int TILE_BYTES = NSUB * SUB_BYTES;
+    static constexpr int PART_BYTES = SG::kStep * 128;             // a part's rows in one 64-column atom
+    static constexpr int OFF_A = 0;                                // resident tiles (dQ: Q, dO; dK/dV: K, V)
+    static constexpr int OFF_B = TILE_BYTES;
+    static constexpr int OFF_X = 2 * TILE_BYTES;                   // ring (dQ: K; dK/dV: Q)
+    static constexpr int OFF_Y = OFF_X + SG::SX * TILE_BYTES;      // ring (dQ: V; dK/dV: dO)
+    static constexpr int OFF_BAR = OFF_Y + SG::SY * TILE_BYTES;
+    static constexpr int MAX_HANDOFF = 8;
+    static constexpr int NBAR = 1 + 2 * SG::SX + 2 * SG::SY + MAX_HANDOFF;
+    static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+    static constexpr int OFF_ABORT = OFF_TMEM + 8;
+    static constexpr int OFF_HULL = OFF_ABORT + 8;                 // {first, last} of each warp
+    static constexpr int SMEM_ALLOC = OFF_HULL + 8 * (SG::kThreads / 32) + 1024;
+    static constexpr uint32_t TMEM_COLS = SG::kHalf ? 256 : 512;
+    static_assert((DQ ? 3 * SG::kStep + D : 2 * SG::kStep + 2 * D) <= TMEM_COLS, "TMEM budget");
+    static_assert(SG::kPerSm * TMEM_COLS <= 512 && SG::kPerSm * (SMEM_ALLOC + 1024) <= 228 * 1024, "SM budget");
 };
 
 // dq_sigma_tile (bwd_sm100.cuh) with the masked score function: one key tile
@@ -89,7 +129,7 @@ __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_
                                              uint64_t *dp_full, uint32_t dp_par, uint64_t *ds_ready,
                                              const ScoreCoef &cf, int row, int key0, int2 span, int &pause,
                                              const WaitCtx &wctx) {
-    using SG = BwdSigma<D>;
+    using SG = SpanBwdShape<D, true>;
     if (!__all_sync(0xffffffffu, mbar_wait(s_full, s_par, wctx))) return false;
     tc_fence_after();
     const int first = key0 + SG::kCols * w;    // this warpgroup's first key
@@ -154,7 +194,7 @@ __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_
                                                uint64_t *dp_full, uint64_t *p_ready, uint64_t *ds_ready,
                                                uint32_t par, const ScoreCoef &cf, int key, int q_first,
                                                bool whole, const int2 *clean, int &pause, const WaitCtx &wctx) {
-    using SG = BwdSigma<D>;
+    using SG = SpanBwdShape<D, false>;
     constexpr int W = SG::kPacked / 16;   // words of 32 columns
     float2 g[SG::kPacked];
     uint32_t pk[SG::kPacked];
@@ -258,18 +298,17 @@ __device__ __forceinline__ bool span_ring_load(const CUtensorMap *map, uint64_t 
 }
 
 // dQ: one CTA per 128-row query tile (the last rows' tiles first).  Tensor
-// memory as bwd_dq_kernel: [0,128) S, [128,256) and [256,384) dP of even / odd
-// steps, [384,384+D) dQ.
+// memory as bwd_dq_kernel, in steps of kStep keys: S, dP of even and of odd steps,
+// dQ.
 template <int D, int MODE, int SCORE>
-__global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
+__global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<D, true>::kPerSm)
     span_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                    const SpanBwdParams p) {
-    constexpr int SX = BwdStages<D>::X, SY = BwdStages<D>::Y;
-    using Lay = SpanBwdLayout<D>;
-    using SG = BwdSigma<D>;
-    constexpr uint32_t kColS = 0, kColDP0 = 128, kColDP1 = 256, kColDQ = 384;
-    static_assert(kColDQ + D <= Lay::TMEM_COLS, "TMEM budget");
+    using Lay = SpanBwdLayout<D, true>;
+    using SG = SpanBwdShape<D, true>;
+    constexpr int SX = SG::SX, SY = SG::SY, NP = SG::kParts;
+    constexpr uint32_t kColS = 0, kColDP0 = SG::kStep, kColDP1 = 2 * SG::kStep, kColDQ = 3 * SG::kStep;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1k(smem_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
@@ -302,7 +341,7 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         if (last) grid_wait();
         return;
     }
-    const int J0 = hull.x / 128, steps = (hull.y + 127) / 128 - J0;
+    const int J0 = hull.x / 128, steps = (hull.y + 127) / 128 - J0;     // key tiles
     const bool ragged = (n & 127) != 0 && J0 + steps == (n + 127) / 128;
     if (threadIdx.x == 0) {
         mbar_init(res_full, 1);
@@ -369,14 +408,15 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, wctx));
         };
-        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_s = idesc_bf16_f32(128, SG::kStep, false, false);
         const uint32_t idesc_q = idesc_bf16_f32(128, D, false, true);
         const uint32_t sQ = smem_u32(smem + Lay::OFF_A), sDO = smem_u32(smem + Lay::OFF_B);
         const uint32_t xring = smem_u32(smem + Lay::OFF_X), yring = smem_u32(smem + Lay::OFF_Y);
         constexpr uint32_t kDescHi = desc_hi(1024);
-        auto kslot = [&](int r) { return xring + (r % SX) * Lay::TILE_BYTES; };
-        auto vslot = [&](int r) { return yring + (r % SY) * Lay::TILE_BYTES; };
-        // X (128 rows of Q or dO) times Y^T (128 rows of K or V) into TMEM column `col`
+        // rows of step r (part r % NP of tile r / NP) in its slot
+        auto krows = [&](int r) { return xring + (r / NP % SX) * Lay::TILE_BYTES + (r % NP) * Lay::PART_BYTES; };
+        auto vrows = [&](int r) { return yring + (r / NP % SY) * Lay::TILE_BYTES + (r % NP) * Lay::PART_BYTES; };
+        // X (128 rows of Q or dO) times Y^T (a step's rows of K or V) into TMEM column `col`
         auto issue_xyT = [&](uint32_t col, uint32_t xbase, uint32_t ybase) {
             const uint32_t x_lo = desc_lo(xbase, 16), y_lo = desc_lo(ybase, 16);
 #pragma unroll
@@ -385,42 +425,45 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
                 mma_ss_lhw(tmem + col, x_lo + koff, y_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
             }
         };
+        const int all = steps * NP;
         bool ok = wait(res_full, 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
         if (ok) {
             tc_fence_after();
-            issue_xyT(kColS, sQ, kslot(0));
+            issue_xyT(kColS, sQ, krows(0));
             mma_commit_w(s_full);
-            issue_xyT(kColDP0, sDO, vslot(0));
+            issue_xyT(kColDP0, sDO, vrows(0));
             mma_commit_w(&dp_full[0]);
-            mma_commit_w(&y_empty[0]);
+            if (NP == 1) mma_commit_w(&y_empty[0]);
         }
-        for (int r = 0; ok && r < steps; ++r) {
-            const bool more = r + 1 < steps;
+        for (int r = 0; ok && r < all; ++r) {
+            const bool more = r + 1 < all;
             if (more) {
-                if (!(ok = wait(&x_full[(r + 1) % SX], ((r + 1) / SX) & 1))) break;
+                const int t = (r + 1) / NP;      // tile of the next step
+                const bool opens = NP == 1 || (r + 1) % NP == 0, closes = (r + 1) % NP == NP - 1;
+                if (opens && !(ok = wait(&x_full[t % SX], (t / SX) & 1))) break;
                 if (!(ok = wait(s_free, r & 1))) break;
                 tc_fence_after();
-                issue_xyT(kColS, sQ, kslot(r + 1));
+                issue_xyT(kColS, sQ, krows(r + 1));
                 mma_commit_w(s_full);
-                if (!(ok = wait(&y_full[(r + 1) % SY], ((r + 1) / SY) & 1))) break;
+                if (opens && !(ok = wait(&y_full[t % SY], (t / SY) & 1))) break;
                 // buffer (r+1) % 2 still holds dS_{r-1}: dQ += dS_{r-1} K_{r-1} was issued
                 // earlier by this thread and MMAs run in issue order
                 tc_fence_after();
-                issue_xyT((r + 1) & 1 ? kColDP1 : kColDP0, sDO, vslot(r + 1));
+                issue_xyT((r + 1) & 1 ? kColDP1 : kColDP0, sDO, vrows(r + 1));
                 mma_commit_w(&dp_full[(r + 1) & 1]);
-                mma_commit_w(&y_empty[(r + 1) % SY]);
+                if (closes) mma_commit_w(&y_empty[t % SY]);
             }
-            if (!more && ragged)
-                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_X + (r % SX) * Lay::TILE_BYTES, n & 127);
+            if (ragged && r == all - NP)
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_X + (r / NP % SX) * Lay::TILE_BYTES, n & 127);
             if (!(ok = wait(&ds_ready[r & 1], (r >> 1) & 1))) break;
             tc_fence_after();
             const uint32_t dcol = r & 1 ? kColDP1 : kColDP0;
-            const uint32_t k_lo = desc_lo(kslot(r), Lay::SUB_BYTES);
+            const uint32_t k_lo = desc_lo(krows(r), Lay::SUB_BYTES);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
+            for (int kk = 0; kk < SG::kStep / 16; ++kk)
                 mma_ts_lhw(tmem + kColDQ, tmem + dcol + SG::packed_col(kk), k_lo + kk * ((16 * 128) >> 4), kDescHi,
                            idesc_q, (r > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_w(&x_empty[r % SX]);
+            if (r % NP == NP - 1) mma_commit_w(&x_empty[r / NP % SX]);
         }
         mma_commit_w(drain);
         mbar_wait_drain(drain, 0, p.timeout_ns);
@@ -437,16 +480,16 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
                                                      SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         bool ok = true;
         int pause = tail_pause(cf);
-        for (int r = 0; r < steps; ++r) {
+        for (int r = 0; r < steps * NP; ++r) {
             ok = span_dq_tile<D, MODE, SCORE>(tmem + lane_bits, w, kColS, r & 1 ? kColDP1 : kColDP0, s_full, r & 1,
                                               s_free, &dp_full[r & 1], (r >> 1) & 1, &ds_ready[r & 1], cf, row,
-                                              (J0 + r) * 128, span, pause, wctx);
+                                              J0 * 128 + r * SG::kStep, span, pause, wctx);
             if (!ok) break;
         }
         // every MMA of this CTA has finished once the MMA warp's final commit lands
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
-        constexpr int kEpi = D / SG::NG >= 32 ? D / SG::NG : 32;
-        if (ok && w * kEpi < D) {
+        constexpr int kEpi = D / SG::NG;
+        if (ok) {
             tc_fence_after();
             store_row_from_tmem<D>(tmem + lane_bits + kColDQ, drow, row < L, span.x < span.y, p.alpha, w * kEpi,
                                    kEpi);
@@ -465,16 +508,17 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
 }
 
 // dK/dV: one CTA per 128-key tile of a key head; streams the query tiles that
-// meet it, head after head of its group.  Tensor memory as bwd_dkdv_kernel:
-// [0,128) S^T, [128,256) dP^T then P^T and dS^T over it, dV, dK.
+// meet it, head after head of its group.  Tensor memory as bwd_dkdv_kernel, in
+// steps of kStep queries: S^T, dP^T then P^T and dS^T over it, dV, dK.
 template <int D, int MODE, int SCORE>
-__global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
+__global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape<D, false>::kPerSm)
     span_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                      const SpanBwdParams p) {
-    constexpr int SX = BwdStages<D>::X, SY = BwdStages<D>::Y;
-    using Lay = SpanBwdLayout<D>;
-    using SG = BwdSigma<D>;
+    using Lay = SpanBwdLayout<D, false>;
+    using SG = SpanBwdShape<D, false>;
+    constexpr int SX = SG::SX, SY = SG::SY, NP = SG::kParts;
+    constexpr uint32_t kColS = 0, kColDP = SG::kStep, kColDV = 2 * SG::kStep, kColDK = 2 * SG::kStep + D;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_1k(smem_raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
@@ -532,7 +576,7 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         zero_rows<D>(p.dv, z, kvh, k0, rows, L, p.Hk);
         return;
     }
-    const int per_head = I1 - I0 + 1, steps = per_head * p.group;
+    const int per_head = I1 - I0 + 1, steps = per_head * p.group;     // query tiles
     const bool ragged = (n & 127) != 0 && I1 == n / 128;
     if (threadIdx.x == 0) {
         mbar_init(res_full, 1);
@@ -606,12 +650,13 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, wctx));
         };
-        const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t idesc_s = idesc_bf16_f32(128, SG::kStep, false, false);
         const uint32_t idesc_kv = idesc_bf16_f32(128, D, false, true);
         const uint32_t sK = smem_u32(smem + Lay::OFF_A), sV = smem_u32(smem + Lay::OFF_B);
         const uint32_t xring = smem_u32(smem + Lay::OFF_X), yring = smem_u32(smem + Lay::OFF_Y);
-        auto qslot = [&](int r) { return xring + (r % SX) * Lay::TILE_BYTES; };
-        auto doslot = [&](int r) { return yring + (r % SY) * Lay::TILE_BYTES; };
+        // rows of step r (part r % NP of tile r / NP) in its slot
+        auto qrows = [&](int r) { return xring + (r / NP % SX) * Lay::TILE_BYTES + (r % NP) * Lay::PART_BYTES; };
+        auto dorows = [&](int r) { return yring + (r / NP % SY) * Lay::TILE_BYTES + (r % NP) * Lay::PART_BYTES; };
         constexpr uint32_t kDescHi = desc_hi(1024);
         auto issue_xyT = [&](uint32_t col, uint32_t xbase, uint32_t ybase) {
             const uint32_t x_lo = desc_lo(xbase, 16), y_lo = desc_lo(ybase, 16);
@@ -621,54 +666,60 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
                 mma_ss_lhw(tmem + col, x_lo + koff, y_lo + koff, kDescHi, idesc_s, kk > 0 ? 1u : 0u);
             }
         };
-        // acc += A(TMEM, packed over `acol`) * B (128 query rows, MN-major)
+        // acc += A(TMEM, packed over `acol`) * B (a step's query rows, MN-major)
         auto issue_acc = [&](uint32_t acc, uint32_t acol, uint32_t bbase, bool first) {
             const uint32_t b_lo = desc_lo(bbase, Lay::SUB_BYTES);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
+            for (int kk = 0; kk < SG::kStep / 16; ++kk)
                 mma_ts_lhw(tmem + acc, tmem + acol + SG::packed_col(kk), b_lo + kk * ((16 * 128) >> 4), kDescHi,
                            idesc_kv, (!first || kk > 0) ? 1u : 0u);
         };
+        const int all = steps * NP;
         bool ok = wait(res_full, 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
         if (ok) {
             tc_fence_after();
-            issue_xyT(Lay::COL_S, sK, qslot(0));
+            issue_xyT(kColS, sK, qrows(0));
             mma_commit_w(s_full);
-            issue_xyT(Lay::COL_DP, sV, doslot(0));
+            issue_xyT(kColDP, sV, dorows(0));
             mma_commit_w(dp_full);
         }
         int left = per_head;          // query tiles left of this head
-        for (int r = 0; ok && r < steps; ++r) {
-            const bool more = r + 1 < steps;
+        for (int r = 0; ok && r < all; ++r) {
+            const bool more = r + 1 < all;
+            const int t = r / NP, t1 = (r + 1) / NP;      // tiles of this step and the next
+            const bool opens = NP == 1 || (r + 1) % NP == 0, closes = r % NP == NP - 1;
             if (more) {
-                if (!(ok = wait(&x_full[(r + 1) % SX], ((r + 1) / SX) & 1))) break;
+                if (opens && !(ok = wait(&x_full[t1 % SX], (t1 / SX) & 1))) break;
                 if (!(ok = wait(s_free, r & 1))) break;
                 tc_fence_after();
-                issue_xyT(Lay::COL_S, sK, qslot(r + 1));
+                issue_xyT(kColS, sK, qrows(r + 1));
                 mma_commit_w(s_full);
             }
-            if (ragged && left == 1) {
+            if (ragged && left == 1 && r % NP == 0) {
                 // S^T and dP^T may still be reading these rows: as columns that are masked
-                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_Y + (r % SY) * Lay::TILE_BYTES, n & 127);
-                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_X + (r % SX) * Lay::TILE_BYTES, n & 127);
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_Y + (t % SY) * Lay::TILE_BYTES, n & 127);
+                zero_tile_rows<Lay::NSUB>(smem + Lay::OFF_X + (t % SX) * Lay::TILE_BYTES, n & 127);
             }
             if (!(ok = wait(p_ready, r & 1))) break;
             tc_fence_after();
-            issue_acc(Lay::COL_ACC0, Lay::COL_DP, doslot(r), r == 0);       // dV += P^T dO
-            mma_commit_w(&y_empty[r % SY]);
+            issue_acc(kColDV, kColDP, dorows(r), r == 0);       // dV += P^T dO
+            if (NP == 1) mma_commit_w(&y_empty[t % SY]);
             if (!(ok = wait(ds_ready, r & 1))) break;
             tc_fence_after();
-            issue_acc(Lay::COL_ACC1, Lay::COL_DP + SG::kPacked, qslot(r), r == 0);  // dK += dS^T Q
-            mma_commit_w(&x_empty[r % SX]);
+            issue_acc(kColDK, kColDP + SG::kPacked, qrows(r), r == 0);  // dK += dS^T Q
+            if (closes) {
+                if (NP > 1) mma_commit_w(&y_empty[t % SY]);
+                mma_commit_w(&x_empty[t % SX]);
+                if (--left == 0) left = per_head;
+            }
             if (more) {
                 // dP^T of r + 1 overwrites P^T and dS^T of r, read by the two MMAs just
                 // issued (MMAs run in issue order)
-                if (!(ok = wait(&y_full[(r + 1) % SY], ((r + 1) / SY) & 1))) break;
+                if (opens && !(ok = wait(&y_full[t1 % SY], (t1 / SY) & 1))) break;
                 tc_fence_after();
-                issue_xyT(Lay::COL_DP, sV, doslot(r + 1));
+                issue_xyT(kColDP, sV, dorows(r + 1));
                 mma_commit_w(dp_full);
             }
-            if (--left == 0) left = per_head;
         }
         mma_commit_w(drain);
         mbar_wait_drain(drain, 0, p.timeout_ns);
@@ -680,28 +731,30 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
         const size_t roff = (static_cast<size_t>(z) * L + key) * (static_cast<size_t>(p.Hk) * D) +
                             static_cast<size_t>(kvh) * D;
-        constexpr int kOut = SG::NG / 2;
+        constexpr int kOut = SG::NG / 2;      // warpgroups to an output
         const bool is_dv = w < kOut;
         __nv_bfloat16 *dst = (is_dv ? p.dv : p.dk) + roff;
         const int2 *clean = p.clean + static_cast<size_t>(z) * tiles * 128 + SG::kCols * w;
-        const uint32_t tS = tmem + lane_bits + Lay::COL_S + SG::kCols * w;
-        const uint32_t tD = tmem + lane_bits + Lay::COL_DP + SG::kCols * w;
+        const uint32_t tS = tmem + lane_bits + kColS + SG::kCols * w;
+        const uint32_t tD = tmem + lane_bits + kColDP + SG::kCols * w;
         const float bias = bias_of(p.bias_z, p.bias, z);
-        int i = I0, h = kvh * p.group;
+        int i = I0, h = kvh * p.group, part = 0;
         ScoreCoef cf = make_score<SCORE>(p.alpha, bias, p.cap, SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         bool ok = true;
         int pause = tail_pause(cf);
-        for (int r = 0; r < steps; ++r) {
+        for (int r = 0; r < steps * NP; ++r) {
             const int4 t = __ldg(hull + i);
             const bool whole = t.z <= k0 && t.w >= k1;
+            const int row0 = i * 128 + part * SG::kStep;
             ok = span_dkdv_tile<D, MODE, SCORE>(tS, tD, s_full, s_free, dp_full, p_ready, ds_ready, r & 1, cf, key,
-                                                i * 128 + SG::kCols * w, whole, clean + i * 128, pause,
-                                                wctx);
+                                                row0 + SG::kCols * w, whole, clean + row0, pause, wctx);
             if (!ok) break;
+            if (++part < NP) continue;
+            part = 0;
             if (++i > I1) {
                 i = I0;
                 ++h;
-                if (SCORE & kScoreSlope && r + 1 < steps)
+                if (SCORE & kScoreSlope && r + 1 < steps * NP)
                     cf = make_score<SCORE>(p.alpha, bias, p.cap, p.slopes[h]);
             }
         }
@@ -709,7 +762,7 @@ __global__ void __launch_bounds__(BwdSigma<D>::kThreads, 1)
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
         if (ok) {
             tc_fence_after();
-            store_row_from_tmem<D>(tmem + lane_bits + (is_dv ? Lay::COL_ACC0 : Lay::COL_ACC1), dst, key < L, key < n,
+            store_row_from_tmem<D>(tmem + lane_bits + (is_dv ? kColDV : kColDK), dst, key < L, key < n,
                                    is_dv ? 1.0f : p.alpha, (w % kOut) * (D / kOut), D / kOut);
         }
     }

@@ -5,8 +5,8 @@ namespace sigattn {
 sigattn_status launch_span_dq(const SpanKind &kind, dim3 grid, const CUtensorMap &mq, const CUtensorMap &mk,
                                const CUtensorMap &mv, const CUtensorMap &mdo, const SpanBwdParams &p, cudaStream_t st) {
     return with_kind(kind, [&]<int D, int MODE, int SCORE>() {
-        constexpr int kSmem = SpanBwdLayout<D>::SMEM_ALLOC;
-        return launch_with(span_dq_kernel<D, MODE, SCORE>, grid, dim3(BwdSigma<D>::kThreads), kSmem, kSmem, true, st, mq, mk, mv, mdo, p);
+        constexpr int kSmem = SpanBwdLayout<D, true>::SMEM_ALLOC;
+        return launch_with(span_dq_kernel<D, MODE, SCORE>, grid, dim3(SpanBwdShape<D, true>::kThreads), kSmem, kSmem, true, st, mq, mk, mv, mdo, p);
     });
 }
 
