@@ -68,7 +68,7 @@ typedef enum {
     SIGATTN_ERR_CUDA = 6,                 /* a CUDA runtime/driver call failed */
     SIGATTN_ERR_TIMEOUT = 7,              /* device: a bounded wait ran out */
     SIGATTN_ERR_SEQLEN_RANGE = 8,         /* device: a length was outside [0, L] */
-    SIGATTN_ERR_TOO_LARGE = 9,            /* a size exceeds a fixed limit (sigattn_fwd_noalloc) */
+    SIGATTN_ERR_TOO_LARGE = 9,            /* a size exceeds a fixed limit */
     SIGATTN_ERR_PAGE_RANGE = 10           /* device: a page number was outside [0, pages) */
 } sigattn_status;
 
@@ -254,12 +254,13 @@ size_t sigattn_dbias_workspace_bytes(int Z, int L, int H, sigattn_dtype dtype);
  * a result.  Within a sample a masked key or query must still be finite (it is
  * multiplied by a weight of zero).
  *
+ * Outputs must not overlap inputs (the kernels of one call run side by side).
  * sigattn_bwd_span writes dq, dk, dv in full and needs neither O nor any saved
  * statistic.  Its workspace (device memory, 16-byte aligned, at least
  * sigattn_bwd_span_workspace_bytes(Z, L, dtype) bytes; 0 for fp32) is
  * overwritten; calls that may overlap, captured graphs included, need one each.
- * Errors: SIGATTN_ERR_INVALID_ARG (also: H not a multiple of Hk, a negative or
- * non-finite cap, a missing or small workspace), _UNSUPPORTED_HEADDIM,
+ * Errors: SIGATTN_ERR_INVALID_ARG (also: H not a multiple of Hk or H = 0 with
+ * Hk > 0, a negative or non-finite cap, a missing or small workspace), _UNSUPPORTED_HEADDIM,
  * _UNSUPPORTED_DTYPE, _UNSUPPORTED_DEVICE, _MISALIGNED (also: spans not 8-byte
  * aligned), _TOO_LARGE (fp32: 2^31 groups of four rows), _CUDA.  On error nothing is
  * launched. */
@@ -330,7 +331,8 @@ sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix,
  * need one each.  Results do not depend on scheduling.  Z is at most
  * SIGATTN_PAGED_MAX_Z.
  *
- * Errors of both: SIGATTN_ERR_INVALID_ARG, _UNSUPPORTED_HEADDIM,
+ * Errors of both: SIGATTN_ERR_INVALID_ARG (sigattn_cache_append: also L = 0;
+ * sigattn_fwd_paged: also pages = 0), _UNSUPPORTED_HEADDIM,
  * _UNSUPPORTED_DTYPE, _UNSUPPORTED_DEVICE, _MISALIGNED, _TOO_LARGE (2^31 places,
  * tokens, rows or, over all samples of sigattn_fwd_paged, 64-place tiles), _CUDA.  On error nothing is launched. */
 #define SIGATTN_PAGED_MAX_Z 4096

@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
@@ -188,10 +189,8 @@ PyObject *guarded(Py_ssize_t given, Py_ssize_t wanted, F &&f) {
         return f();
     } catch (const Refusal &r) {
         if (r.type != nullptr) PyErr_SetString(r.type, r.what.c_str());
-    } catch (const c10::OutOfMemoryError &e) {
-        PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

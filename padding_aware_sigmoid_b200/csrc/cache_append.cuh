@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const A
 
     int have = p.cache_lens[z], add = p.seqlens_new[z];
     const int base = p.prefix_len != nullptr ? max(*p.prefix_len, 0) : 0;
-    if (have < 0 || have > capacity || add < 0 || add > p.L || add > capacity - have) {
+    if (have < 0 || have > capacity || add < 0 || add > p.L || add > capacity - have ||
+        (p.prefix_len != nullptr && *p.prefix_len < 0)) {
         record_status(p.status, kStatusSeqlenRange);
         have = min(max(have, 0), capacity);
         add = min(max(add, 0), p.L);

@@ -30,6 +30,7 @@ sigattn_status check_span(const SpanArgs &a, bool *empty) {
     if (!(a.cap >= 0.0f) || !std::isfinite(a.cap) ||
         (a.cap > 0.0f && !std::isfinite(a.alpha / a.cap)))
         return SIGATTN_ERR_INVALID_ARG;
+    if (a.H == 0 && a.Hk != 0) return SIGATTN_ERR_INVALID_ARG;    // dK, dV would have no query
     *empty = a.Z == 0 || a.L == 0 || a.H == 0;
     if (*empty) return SIGATTN_OK;
     if (a.Hk == 0 || a.H % a.Hk != 0) return SIGATTN_ERR_INVALID_ARG;
@@ -150,10 +151,10 @@ __global__ void __launch_bounds__(kSpanThreads)
         }
         if (i >= L) continue;
         int lo = row[i].x, hi = end;
-        if (causal) hi = min(hi, max(i + 1, prefix != nullptr ? min(lo + pre, L) : 0));
+        if (causal) hi = min(hi, max(i + 1, prefix != nullptr ? lo + min(pre, L - lo) : 0));
         if (window > 0) {
             lo = max(lo, i - window + 1);
-            if (!causal) hi = min(hi, i + window);
+            if (!causal) hi = min(hi, i + min(window, L - i));
         }
         row[i] = i < n && lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
     }

@@ -161,12 +161,15 @@ __device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &
     }
 }
 
-// P of two neighbouring columns with the accurate forms, for kernels whose
-// scores are few.
+// P of two neighbouring columns to about 2^-20, for kernels whose scores are few:
+// one ex2 and one reciprocal, e^-|x| keeping both tails.
 template <int SCORE>
 __device__ __forceinline__ float2 score_p2(float s0, float s1, const ScoreCoef &cf, float rel) {
     float2 f;
-    return sigma2<kSigmoidExp>(score_arg2<kSigmoidExp, SCORE, false>(s0, s1, cf, rel, f));
+    const float2 y = score_arg2<kSigmoidExp, SCORE, false>(s0, s1, cf, rel, f);
+    const float2 u = f2(ex2_approx(-fabsf(y.x)), ex2_approx(-fabsf(y.y)));
+    const float2 g = f2(rcp_approx(1.0f + u.x), rcp_approx(1.0f + u.y));
+    return mul2(g, f2(y.x >= 0.0f ? 1.0f : u.x, y.y >= 0.0f ? 1.0f : u.y));
 }
 
 // Lets the next kernel of the stream start, and waits until the one before has

@@ -35,6 +35,7 @@ def test_forward_refusals(sa):
     assert _fwd(lib, D=96) == 2
     assert _fwd(lib, dtype=3) == 3
     assert _fwd(lib, Z=-1) == 1 and _fwd(lib, L=-1) == 1 and _fwd(lib, H=65536, Hk=1) == 1
+    assert _fwd(lib, H=0, Hk=2) == 1
     assert _fwd(lib, H=4, Hk=3) == 1 and _fwd(lib, H=4, Hk=0) == 1 and _fwd(lib, H=2, Hk=4) == 1
     assert _fwd(lib, q=None) == 1 and _fwd(lib, seqlens=None) == 1
     assert _fwd(lib, q=ctypes.c_void_p(18)) == 5 and _fwd(lib, spans=ctypes.c_void_p(20)) == 5
