@@ -228,7 +228,7 @@ struct PagedItem {
             rows.q[i] = nullptr;
             rows.pos[i] = 0.0f;
             rows.limit[i] = 0;
-            cf[i] = ScoreCoef{0.0f, 0.0f, 0.0f, 0.0f};
+            cf[i] = ScoreCoef{};
             if (!in) continue;
             const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
             const int2 n = paged_lengths(p, z);
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // the token and head of this row
             const int64_t tok = tok0 + static_cast<int64_t>(t) * p.tile_tokens + row / p.group;
             const int h = kvh * p.group + row % p.group;
-            ScoreCoef cf = {0.0f, -64.0f, 0.0f, 0.0f};    // of rows that are not there: sigma of almost nothing
+            ScoreCoef cf = {0.0f, -64.0f};    // of rows that are not there: sigma of almost nothing
             bool live = row < p.tile_tokens * p.group && tok < tokens;
             float pos = 0.0f;
             if (live) {
@@ -720,7 +720,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                        SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
             }
             // the same choice in the whole warp
-            int pause = __all_sync(0xffffffffu, !live || tail_pause(cf) == 0) ? 0 : 1 << 30;
+            ScorePause pause = score_pause(cf);
+            pause.tail = __all_sync(0xffffffffu, !live || pause.tail == 0) ? 0 : kNever;
+            pause.poly = __all_sync(0xffffffffu, !live || pause.poly == 0) ? 0 : kNever;
             bool ok = true;
             const uint32_t tS = tmem + lane_bits + (t ? Lay::COL_S1 : Lay::COL_S0) + 64 * c;
             for (int r = 0; r < steps; ++r) {
@@ -732,7 +734,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int u = 0; u < 2; ++u) {
                     uint32_t x[32], pk[16];
                     tmem_ld32(tS + 32 * u, x);
-                    score_chunk<MODE, SCORE, false>(x, cf, pos - static_cast<float>(key0 + 32 * u), pk, nullptr, pause);
+                    score_chunk<MODE, SCORE, false, true>(x, cf, pos - static_cast<float>(key0 + 32 * u), pk, nullptr, pause);
                     if (prefix - key0 < 64) keep_bits(pk, bit_range(0, prefix - key0 - 32 * u));
                     tmem_st16(tS + 16 * u, pk);
                 }

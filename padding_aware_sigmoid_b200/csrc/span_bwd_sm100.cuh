@@ -127,7 +127,7 @@ template <int D, int MODE, int SCORE>
 __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_s, uint32_t dcol,
                                              uint64_t *s_full, uint32_t s_par, uint64_t *s_free,
                                              uint64_t *dp_full, uint32_t dp_par, uint64_t *ds_ready,
-                                             const ScoreCoef &cf, int row, int key0, int2 span, int &pause,
+                                             const ScoreCoef &cf, int row, int key0, int2 span, ScorePause &pause,
                                              const WaitCtx &wctx) {
     using SG = SpanBwdShape<D, true>;
     if (!__all_sync(0xffffffffu, mbar_wait(s_full, s_par, wctx))) return false;
@@ -193,7 +193,7 @@ template <int D, int MODE, int SCORE>
 __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_t *s_full, uint64_t *s_free,
                                                uint64_t *dp_full, uint64_t *p_ready, uint64_t *ds_ready,
                                                uint32_t par, const ScoreCoef &cf, int key, int q_first,
-                                               bool whole, const int2 *clean, int &pause, const WaitCtx &wctx) {
+                                               bool whole, const int2 *clean, ScorePause &pause, const WaitCtx &wctx) {
     using SG = SpanBwdShape<D, false>;
     constexpr int W = SG::kPacked / 16;   // words of 32 columns
     float2 g[SG::kPacked];
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
         const ScoreCoef cf = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                                      SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         bool ok = true;
-        int pause = tail_pause(cf);
+        ScorePause pause = score_pause(cf);
         for (int r = 0; r < steps * NP; ++r) {
             ok = span_dq_tile<D, MODE, SCORE>(tmem + lane_bits, w, kColS, r & 1 ? kColDP1 : kColDP0, s_full, r & 1,
                                               s_free, &dp_full[r & 1], (r >> 1) & 1, &ds_ready[r & 1], cf, row,
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
         int i = I0, h = kvh * p.group, part = 0;
         ScoreCoef cf = make_score<SCORE>(p.alpha, bias, p.cap, SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         bool ok = true;
-        int pause = tail_pause(cf);
+        ScorePause pause = score_pause(cf);
         for (int r = 0; r < steps * NP; ++r) {
             const int4 t = __ldg(hull + i);
             const bool whole = t.z <= k0 && t.w >= k1;

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
             const ScoreCoef cf = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                                          SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
             const uint32_t tS = tmem + lane_bits + Lay::COL_S + 128 * t + 64 * c;
-            int pause = tail_pause(cf);
+            ScorePause pause = score_pause(cf);
             for (int j = ja; j < jb; ++j) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&s_full[part], (j - ja) & 1, wctx));
                 if (!ok) break;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
                     if (some) {
                         uint32_t r[32];
                         tmem_ld32(tS + 32 * u, r);
-                        score_chunk<MODE, SCORE, false>(r, cf, static_cast<float>(row - key0 - 32 * u), pk, nullptr,
+                        score_chunk<MODE, SCORE, false, true>(r, cf, static_cast<float>(row - key0 - 32 * u), pk, nullptr,
                                                         pause);
                         if (!whole) keep_bits(pk, bit_range(span.x - key0 - 32 * u, span.y - key0 - 32 * u));
                     } else {

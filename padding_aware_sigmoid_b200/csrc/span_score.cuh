@@ -35,7 +35,14 @@ struct ScoreCoef {
     float c;    // b log2 e
     float cap;  // cap log2 e
     float m;    // -m_h log2 e
+    // the cap as a polynomial of the raw product s (see cap_poly2)
+    float k0, k1, k2;
+    int most;   // s^2 up to which it holds, as bits
 };
+// tanh(y) / y as a0 + a1 y^2 + a2 y^4 on |y| <= 3/4: minimax fit in relative error,
+// fitted for this library by iteratively reweighted least squares (maximum 2.2e-4;
+// the hardware tanh has 4.9e-4).
+constexpr float kCapA0 = 0.9997852f, kCapA1 = -0.32629665f, kCapA2 = 0.09735532f, kCapMost = 0.75f;
 
 template <int SCORE>
 __device__ __forceinline__ ScoreCoef make_score(float alpha, float bias, float cap, float slope) {
@@ -44,11 +51,22 @@ __device__ __forceinline__ ScoreCoef make_score(float alpha, float bias, float c
     r.c = kLog2e * bias;
     r.cap = kLog2e * cap;
     r.m = -kLog2e * slope;
+    r.k0 = r.k1 = r.k2 = 0.0f;
+    r.most = 0;
+    if constexpr (SCORE & kScoreCap) {
+        const float a2 = r.a * r.a, k = kLog2e * alpha, most = kCapMost / r.a;
+        r.k0 = k * kCapA0;
+        r.k1 = k * kCapA1 * a2;
+        r.k2 = k * kCapA2 * a2 * a2;
+        r.most = __float_as_int(most * most);
+    }
     return r;
 }
 
 // Additive part of the arguments of two neighbouring columns; `rel` is this
-// row's position less the first column's.
+// row's position less the first column's.  (A second copy of the loops with the
+// straight line that |i - j| is away from the diagonal, one FMA in place of five
+// operations, ran 5 to 9% slower: the code no longer fits the instruction cache.)
 template <int SCORE>
 __device__ __forceinline__ float2 score_addend(const ScoreCoef &cf, float rel) {
     if constexpr (SCORE & kScoreSlope)
@@ -76,11 +94,10 @@ __device__ __forceinline__ float2 cap_tanh2(float2 y, float2 &f) {
     }
 }
 
-// x log2 e of two neighbouring columns from their raw products; with GRAD and
-// a cap also the cap's derivative.
+// x log2 e of two neighbouring columns from their raw products and the additive
+// part; with GRAD and a cap also the cap's derivative.
 template <int MODE, int SCORE, bool GRAD>
-__device__ __forceinline__ float2 score_arg2(float s0, float s1, const ScoreCoef &cf, float rel, float2 &f) {
-    const float2 add = score_addend<SCORE>(cf, rel);
+__device__ __forceinline__ float2 score_arg2(float s0, float s1, const ScoreCoef &cf, float2 add, float2 &f) {
     if constexpr (SCORE & kScoreCap) {
         const float2 t = cap_tanh2<MODE, GRAD>(mul2(f2(s0, s1), f2(cf.a, cf.a)), f);
         return fma2(t, f2(cf.cap, cf.cap), add);
@@ -89,84 +106,144 @@ __device__ __forceinline__ float2 score_arg2(float s0, float s1, const ScoreCoef
     }
 }
 
-// P (packed bf16) of 32 neighbouring columns of this thread's row, and with
-// GRAD g = dP/d(alpha s); `rel` is the row's position less the first column's.
-//
-// In TANH mode a chunk whose 32 x 32 weights all lie in the left tail, u = e^x <=
-// 1/32, takes sigma = u - u^2 and sigma' = u - 2 u^2 (+ O(u^3)) from one ex2: as
-// many MUFU and FMA operations as the tanh form, but a relative error of at most
-// u^2 <= 1e-3 where 0.5 + 0.5 tanh cancels (up to 1.4%).  With b = -ln n nearly
-// every chunk of a long row does.  Chunks that hold a larger weight keep the
-// tanh: there the weights that cancel are the small ones.
-//
-// The tail form is tried first and its largest u looked at afterwards (as
-// integers, which order like positive floats); after a chunk that did not fit,
-// the next kTailPause chunks of the warp go straight to the tanh (`pause` counts
-// them), so that rows of large scores do not pay twice.  Biases above
-// kTailBias never try: there the tanh is accurate enough (2-norm error of O 2.4e-3
-// at n = 2048, against 3.3e-3 at n = 16384 and 2.3e-3 with the tail form), and
-// the look costs 5% (causal forward, H = 16, L = 16384, D = 128: 1003 us with the
-// tanh alone, 1054 us so; with a degree-2 polynomial and a look at the arguments
-// first 1178 us).
-constexpr int kTailMost = 0x3D000000;    // 1/32 as bits
-constexpr int kTailPause = 31;
-constexpr float kTailBias = -11.5f;      // b log2 e: rows of about 2900 tokens
-__device__ __forceinline__ int tail_pause(const ScoreCoef &cf) { return cf.c <= kTailBias ? 0 : 1 << 30; }
+// The same with the cap as a polynomial: four FMA operations more than without a
+// cap, where a tanh doubles the MUFU's work.
+//   q = k alpha (a0 + a1 (a s)^2 + a2 (a s)^4),  x = s q + ..
+__device__ __forceinline__ float2 cap_poly2(float s0, float s1, const ScoreCoef &cf, float2 add, int &largest) {
+    const float2 s = f2(s0, s1), z = mul2(s, s);
+    largest = __vimax3_s32(largest, __float_as_int(z.x), __float_as_int(z.y));
+    const float2 q = fma2(z, fma2(z, f2(cf.k2, cf.k2), f2(cf.k1, cf.k1)), f2(cf.k0, cf.k0));
+    return fma2(s, q, add);
+}
 
-template <int MODE, int SCORE, bool GRAD>
-__device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk,
-                                            float2 *g, int &pause) {
-    if (MODE == kSigmoidTanh && pause == 0) {
-        int top = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float2 f;
-            const float2 y = score_arg2<MODE, SCORE, GRAD>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]),
-                                                           cf, rel - static_cast<float>(2 * i), f);
-            const float2 u = f2(ex2_approx(y.x), ex2_approx(y.y));
-            top = __vimax3_s32(top, __float_as_int(u.x), __float_as_int(u.y));
-            const float2 n = f2(-u.x, -u.y);
-            const float2 p = fma2(n, u, u);
-            pk[i] = pack_bf16x2(p.x, p.y);
-            if constexpr (GRAD) {
-                g[i] = fma2(n, u, p);
-                if constexpr (SCORE & kScoreCap) g[i] = mul2(g[i], f);
-            }
-        }
-        if (__all_sync(0xffffffffu, top <= kTailMost)) return;
-        pause = kTailPause + 1;
-    }
-    if (MODE == kSigmoidTanh) --pause;
+// How the chunks of a warp are evaluated in TANH mode: counts of chunks that skip a
+// form which did not fit before.
+struct ScorePause {
+    int tail, poly;
+};
+constexpr int kPause = 31, kNever = 1 << 30;
+constexpr int kTailMost = 0x3D000000;    // u = 1/32 as bits
+constexpr float kTailBias = -11.5f;      // b log2 e: rows of about 2900 tokens
+__device__ __forceinline__ ScorePause score_pause(const ScoreCoef &cf) {
+    // the polynomial's coefficients stay in range for any sane alpha / cap
+    return ScorePause{cf.c <= kTailBias ? 0 : kNever, fabsf(cf.a) < 1e4f ? 0 : kNever};
+}
+
+// P (packed bf16) of 32 neighbouring columns of this thread's row, and with GRAD g
+// = dP/d(alpha s), in TANH mode with the forms POLY (of the cap) and TAIL (of
+// sigma); returns whether both hold for all 32 x 32 scores of the warp (bit 0: the
+// cap's does not, bit 1: the tail's).
+//
+// TAIL: in the left tail, u = e^x <= 1/32, sigma = u - u^2 and sigma' = u - 2 u^2 (+
+// O(u^3)) from one ex2: as many MUFU and FMA operations as the tanh form, but a
+// relative error of at most u^2 <= 1e-3 where 0.5 + 0.5 tanh cancels (up to 1.4%).
+template <int SCORE, bool GRAD, bool POLY, bool TAIL>
+__device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk, float2 *g) {
     ScoreCoef cx = cf;
-    if constexpr (MODE == kSigmoidTanh) {     // tanh wants x / 2
+    if constexpr (!TAIL) {     // tanh wants x / 2
         constexpr float kHalfLn2 = 0.34657359f;
         if constexpr (!(SCORE & kScoreCap)) cx.a *= kHalfLn2;
         cx.c *= kHalfLn2;
         cx.cap *= kHalfLn2;
         cx.m *= kHalfLn2;
+        cx.k0 *= kHalfLn2;
+        cx.k1 *= kHalfLn2;
+        cx.k2 *= kHalfLn2;
     }
+    int largest = 0, top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float2 p, d, f;
-        const float2 x = score_arg2<MODE, SCORE, GRAD>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), cx,
-                                                       rel - static_cast<float>(2 * i), f);
-        if constexpr (GRAD) {
-            sigma_grad2<MODE>(x, p, d);
-            if constexpr (SCORE & kScoreCap) d = mul2(d, f);
-            g[i] = d;
+        const float s0 = __uint_as_float(r[2 * i]), s1 = __uint_as_float(r[2 * i + 1]);
+        const float2 add = score_addend<SCORE>(cx, rel - static_cast<float>(2 * i));
+        float2 f, p, y;
+        if constexpr (POLY) y = cap_poly2(s0, s1, cx, add, largest);
+        else y = score_arg2<kSigmoidTanh, SCORE, GRAD>(s0, s1, cx, add, f);
+        if constexpr (TAIL) {
+            const float2 u = f2(ex2_approx(y.x), ex2_approx(y.y)), n = f2(-u.x, -u.y);
+            top = __vimax3_s32(top, __float_as_int(u.x), __float_as_int(u.y));
+            p = fma2(n, u, u);
+            if constexpr (GRAD) g[i] = fma2(n, u, p);
+        } else if constexpr (GRAD) {
+            sigma_grad2<kSigmoidTanh>(y, p, g[i]);
         } else {
-            p = sigma2<MODE>(x);
+            p = sigma2<kSigmoidTanh>(y);
         }
+        if constexpr (GRAD && (SCORE & kScoreCap)) g[i] = mul2(g[i], f);
         pk[i] = pack_bf16x2(p.x, p.y);
     }
+    int bad = 0;
+    if constexpr (POLY) bad |= __any_sync(0xffffffffu, largest > cf.most) ? 1 : 0;
+    if constexpr (TAIL) bad |= __any_sync(0xffffffffu, top > kTailMost) ? 2 : 0;
+    return bad;
 }
 
+// P (packed bf16) of 32 neighbouring columns of this thread's row, and with GRAD g
+// = dP/d(alpha s); `rel` is the row's position less the first column's.
+//
+// In TANH mode a chunk is tried with the forms that usually hold and looked at
+// afterwards (the largest s^2 and u, as integers, which order like positive
+// floats); where one does not hold, the chunk is done again without it, and the
+// next kPause chunks of the warp skip it, so that rows of large scores do not pay
+// twice.
+//
+// The tail form is for b = -ln n of long rows, where nearly every chunk fits:
+// 2-norm error of O 3.3e-3 -> 2.3e-3 at n = 16384 (at n = 2048 the tanh alone has
+// 2.4e-3: biases above kTailBias do not try), for 5% of the time (causal forward, H =
+// 16, L = 16384, D = 128: 1003 us with the tanh alone, 1054 us so; with a degree-2
+// polynomial and a look at the arguments first 1178 us).  Chunks that hold a
+// larger weight keep the tanh: there the weights that cancel are the small ones.
+//
+// FWD: the cap as a polynomial, in the forward and without slopes (D = 64, full 4K:
+// 280 -> 222 us).  With slopes the FMA and ALU pipes are the bound already (D = 128
+// 193 -> 194 us, D = 64 packed 56 -> 62 us), and the backward's registers do not hold
+// its operands (D = 128 547 -> 663 us).
+template <int MODE, int SCORE, bool GRAD, bool FWD = false>
+__device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk,
+                                            float2 *g, ScorePause &pause) {
+    if constexpr (MODE == kSigmoidExp) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float2 p, f;
+            const float2 y =
+                score_arg2<MODE, SCORE, GRAD>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), cf,
+                                              score_addend<SCORE>(cf, rel - static_cast<float>(2 * i)), f);
+            if constexpr (GRAD) {
+                sigma_grad2<MODE>(y, p, g[i]);
+                if constexpr (SCORE & kScoreCap) g[i] = mul2(g[i], f);
+            } else {
+                p = sigma2<MODE>(y);
+            }
+            pk[i] = pack_bf16x2(p.x, p.y);
+        }
+    } else if constexpr (FWD && SCORE == kScoreCap) {
+        if (pause.poly == 0) {
+            int bad = 2;
+            if (pause.tail == 0) {
+                if ((bad = score_form<SCORE, GRAD, true, true>(r, cf, rel, pk, g)) == 0) return;
+                pause.tail = kPause + 1;
+            }
+            --pause.tail;
+            if (!(bad & 1) && score_form<SCORE, GRAD, true, false>(r, cf, rel, pk, g) == 0) return;
+            pause.poly = kPause + 1;
+        }
+        --pause.poly;
+        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g);
+    } else {
+        if (pause.tail == 0) {
+            if (score_form<SCORE, GRAD, false, true>(r, cf, rel, pk, g) == 0) return;
+            pause.tail = kPause + 1;
+        }
+        --pause.tail;
+        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g);
+    }
+}
 // P of two neighbouring columns to about 2^-20, for kernels whose scores are few:
 // one ex2 and one reciprocal, e^-|x| keeping both tails.
 template <int SCORE>
 __device__ __forceinline__ float2 score_p2(float s0, float s1, const ScoreCoef &cf, float rel) {
     float2 f;
-    const float2 y = score_arg2<kSigmoidExp, SCORE, false>(s0, s1, cf, rel, f);
+    const float2 y = score_arg2<kSigmoidExp, SCORE, false>(
+        s0, s1, cf, score_addend<SCORE>(cf, rel), f);
     const float2 u = f2(ex2_approx(-fabsf(y.x)), ex2_approx(-fabsf(y.y)));
     const float2 g = f2(rcp_approx(1.0f + u.x), rcp_approx(1.0f + u.y));
     return mul2(g, f2(y.x >= 0.0f ? 1.0f : u.x, y.y >= 0.0f ? 1.0f : u.y));

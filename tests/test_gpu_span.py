@@ -136,6 +136,27 @@ def test_parity_tanh(dev, case):
     _run_case(case, dev, torch.bfloat16, True)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,bias", [(1.5, -1.0), (6.0, -9.5), (15.0, -9.5), (40.0, -9.5), (40.0, -2.0), (1e6, 0.5)])
+def test_forms_of_capped_scores(dev, D, cap, bias):
+    """Scores far below the cap, around it and far beyond, within the same rows, in sigma's left tail and outside it: every form
+    of the hardware-tanh mode, and the steps between them."""
+    Z, L, H, Hk = 1, 1300, 2, 1
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 77)
+    # keys of one stretch score large, queries of one stretch small
+    k[:, 300:420] *= 4.0
+    q[:, 700:1000] *= 0.1
+    seq = torch.as_tensor(np.asarray([1290], np.int32), device=dev)
+    spans = _spans("causal", [1290], L, dev)
+    alpha = D ** -0.5
+    args = dict(spans=spans, cap=cap)
+    sees = R.visible(spans, [1290], L)
+    ref, _ = R.reference(q, k, v, do, sees, alpha, [bias], cap, None)
+    got = (sa.fwd_span(q, k, v, seq, alpha, bias, **args), *sa.bwd_span(q, k, v, do, seq, alpha, bias, **args))
+    for name, x in zip(("O", "dQ", "dK", "dV"), got):
+        C.assert_close(x.float().cpu().numpy(), ref[name].numpy(), "bf16", f"{name} at cap {cap}")
+
+
 @pytest.mark.parametrize("case", CASES)
 def test_parity_fp32(dev, case):
     _run_case(case, dev, torch.float32, False)
