@@ -66,7 +66,7 @@ __device__ __forceinline__ ScoreCoef make_score(float alpha, float bias, float c
 // Additive part of the arguments of two neighbouring columns; `rel` is this
 // row's position less the first column's.  (A second copy of the loops with the
 // straight line that |i - j| is away from the diagonal, one FMA in place of five
-// operations, ran 5 to 9% slower: the code no longer fits the instruction cache.)
+// operations, ran 3 to 9% slower in five of six cases.)
 template <int SCORE>
 __device__ __forceinline__ float2 score_addend(const ScoreCoef &cf, float rel) {
     if constexpr (SCORE & kScoreSlope)
