@@ -53,7 +53,8 @@ class _SigmoidAttentionBiasFn(torch.autograd.Function):
 
 class _SpanAttentionFn(torch.autograd.Function):
     """The masked attention (``fwd_span`` / ``bwd_span``).  Gradients for q, k and
-    v; the bias and the slopes are constants here."""
+    v; the bias and the slopes are constants here.  A gradient of the gradient is
+    refused: it would leave out how dQ, dK and dV depend on q, k and v."""
 
     @staticmethod
     def forward(ctx, q, k, v, seqlens, spans, slopes, alpha, bias, cap):
@@ -66,6 +67,7 @@ class _SpanAttentionFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         from . import bwd_span
         q, k, v, n, spans, slopes, bias_z = ctx.saved_tensors
@@ -94,7 +96,13 @@ class SigmoidAttention(torch.nn.Module):
     with ``spans`` (``mask_spans``: causal, prefix, document and window masks), or
     with k and v of fewer heads, which groups of query heads share, runs the
     masked attention as well; it needs one length per sample for queries and
-    keys, and a bias that is not learned."""
+    keys, and a bias that is not learned.
+
+    To capture a forward and backward in a CUDA graph, warm up on a side stream
+    and drop every output of an eager pass over the same leaves before the
+    capture: PyTorch keeps a leaf's gradient node, and the stream it was made on,
+    for as long as such an output lives, and a captured backward must not wait
+    on a stream outside the capture."""
 
     def __init__(self, alpha: float | None = None, bias: float | None = None,
                  per_sample_bias: bool = False, learnable_bias: bool = False,

@@ -46,9 +46,20 @@ int row_warps(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 constexpr int kPagedMostSms = 256;                   // more than any device has
 constexpr int kPagedMostBlocks = 3 * kPagedMostSms;  // of the tile kernel
 
-// Rows (over the batch, per key head) from which the prefix kernel takes the
-// prefix.
+// Rows (over the batch, per key head) above which the prefix kernel takes the
+// prefix. The tile kernel's row tile is 64 rows, the prefix kernel's 256: up to 64
+// rows the tile kernel reads the prefix once as well and needs no further launch
+// (whole call, a prefix of 16K tokens: 32 rows 18.1 us against 21.7 with the prefix
+// kernel, 64 rows 24.7 against 25.6); above, it would read the prefix again for every
+// 64 rows (128 rows 33.6 us against 27.4, 256 rows 57.0 against 39.3).
 constexpr int64_t kPrefixKernelRows = 64;
+
+// Rows of the output up to which a row's partials are added by 8, 4 or 2 warps.
+// Few rows leave most of the SMs empty with a warp a row (1024 rows, whole call:
+// 8 warps 35.6 us, 4 warps 37.2, 2 warps 40.9, 1 warp 44.5); many rows fill them
+// without the exchange through shared memory. Each limit is about 1, 2 and 2
+// waves of such blocks on 148 SMs.
+constexpr int64_t kJoin8Rows = 2048, kJoin4Rows = 8192, kJoin2Rows = 16384;
 
 struct PagedSizes {
     int prefix_warps, own_warps;
@@ -118,11 +129,7 @@ sigattn_status prefix_launch(const PagedMaps &m, const PagedParams &p, cudaStrea
     return launch(paged_prefix_kernel<D, MODE, SCORE>, dim3(p.splits, p.pairs, p.Hk), dim3(kFwdThreads),
                   FwdLayout<D, KS, VS>::SMEM_ALLOC, st, m.prefix_q, m.prefix_k, m.prefix_v, p);
 }
-#ifndef PAGED_W8
-#define PAGED_W8 2048
-#define PAGED_W4 8192
-#define PAGED_W2 16384
-#endif
+
 template <int D, int SCORE>
 sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream_t st) {
     using Lay = PagedLayout<D>;
@@ -137,15 +144,14 @@ sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream
     s = launch_with(paged_tiles_kernel<D, SCORE>, dim3(p.groups * p.heads_wide), dim3(kPagedThreads), Lay::bytes(SIGATTN_PAGED_MAX_Z),
                     Lay::bytes(p.Z), p.splits > 0, st, m.k, m.v, p);
     if (s != SIGATTN_OK) return s;
-    // Few rows: a block each, its warps sharing the row's partials.
     const int64_t rows = static_cast<int64_t>(p.Z) * p.L * p.H;
     auto join = [&](auto kernel, int per_block) {
         return launch_with(kernel, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)), dim3(kJoinThreads),
                            0, 0, true, st, p);
     };
-    if (rows <= PAGED_W8) return join(paged_join_kernel<D, 8>, 1);
-    if (rows <= PAGED_W4) return join(paged_join_kernel<D, 4>, 2);
-    if (rows <= PAGED_W2) return join(paged_join_kernel<D, 2>, 4);
+    if (rows <= kJoin8Rows) return join(paged_join_kernel<D, 8>, 1);
+    if (rows <= kJoin4Rows) return join(paged_join_kernel<D, 4>, 2);
+    if (rows <= kJoin2Rows) return join(paged_join_kernel<D, 2>, 4);
     return join(paged_join_kernel<D, 1>, 8);
 }
 template <int D>

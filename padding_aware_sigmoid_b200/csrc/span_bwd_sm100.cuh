@@ -83,11 +83,12 @@ static __global__ void __launch_bounds__(128) span_prep_kernel(const SpanSource 
 // lost 6 to 25%.
 template <int D, bool DQ>
 struct SpanBwdShape {
-    static constexpr bool kHalf = DQ && D == 64;
+    static constexpr bool kHalf = D == 64;
     static constexpr int kPerSm = kHalf ? 2 : 1;
     static constexpr int kStep = kHalf ? 64 : 128, kParts = 128 / kStep;
     static constexpr int NG = D == 64 && !kHalf ? 4 : 2;     // sigma warpgroups, kCols columns of a step each
-    static constexpr int kThreads = 128 + 128 * NG, kArrivals = 128 * NG;
+    static constexpr int kAux = kHalf && !DQ ? 2 : 4;        // warps that load and issue
+    static constexpr int kThreads = 32 * kAux + 128 * NG, kArrivals = 128 * NG;
     static constexpr int kCols = kStep / NG, kPacked = kCols / 2;
     static constexpr int SX = kHalf ? 2 : BwdStages<D>::X, SY = kHalf ? 2 : BwdStages<D>::Y;
     // TMEM column (relative to the buffer) of the packed bf16 values of K step kk
@@ -616,12 +617,18 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
 
     if (warp == 0) {
         if (lane == 0) {
-            int ix = 0, i = I0, h = kvh * p.group;
+            int ix = 0, iy = 0, i = I0, h = kvh * p.group;
             for (int r = 0; r < steps; ++r) {
                 if (!span_ring_load<SX, Lay::NSUB>(&tmQ, x_full, x_empty, smem + Lay::OFF_X, Lay::TILE_BYTES, r,
                                                    i * 128, h, z, wctx))
                     break;
                 ix = r + 1;
+                if constexpr (SG::kAux == 2) {
+                    if (!span_ring_load<SY, Lay::NSUB>(&tmDO, y_full, y_empty, smem + Lay::OFF_Y, Lay::TILE_BYTES, r,
+                                                       i * 128, h, z, wctx))
+                        break;
+                    iy = r + 1;
+                }
                 if (++i > I1) {
                     i = I0;
                     ++h;
@@ -629,8 +636,9 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
             }
             mbar_wait_drain(res_full, 0, p.timeout_ns);
             ring_drain<SX>(x_full, ix, p.timeout_ns);
+            ring_drain<SY>(y_full, iy, p.timeout_ns);
         }
-    } else if (warp == 2) {
+    } else if (SG::kAux > 2 && warp == 2) {
         if (lane == 0) {
             int iy = 0, i = I0, h = kvh * p.group;
             for (int r = 0; r < steps; ++r) {
@@ -724,8 +732,8 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
         mma_commit_w(drain);
         mbar_wait_drain(drain, 0, p.timeout_ns);
         __syncwarp();
-    } else if (warp >= 4) {
-        const int w = (warp - 4) >> 2;      // warpgroup: query columns [kCols w, kCols (w + 1))
+    } else if (warp >= SG::kAux) {
+        const int w = (warp - SG::kAux) >> 2;      // warpgroup: query columns [kCols w, kCols (w + 1))
         const int quarter = warp & 3;
         const int key = k0 + quarter * 32 + lane;
         const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;

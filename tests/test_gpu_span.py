@@ -393,3 +393,49 @@ def test_long_rows_pass_the_tail_of_the_grid(dev):
     want = torch.clamp(torch.arange(L) + 1, max=200).float()
     want[L - 5:] = 0
     assert torch.equal(o, want.to(torch.bfloat16).float())
+
+
+def test_module_refuses_a_gradient_of_the_gradient(dev):
+    q, k, v, do = _tensors(1, 64, 2, 2, 64, torch.bfloat16, dev, 71)
+    seq = torch.as_tensor(np.asarray([50], np.int32), device=dev)
+    q.requires_grad_()
+    out = sa.SigmoidAttention(bias=-1.0, cap=5.0)(q, k, v, seq)
+    dq, = torch.autograd.grad(out, q, do, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dq.float().sum(), q)
+
+
+def test_captured_module_step_replays_with_new_inputs(dev):
+    """Forward and backward of the module in one graph, warmed up on a side stream as PyTorch asks."""
+    Z, L, H, Hk, D = 2, 300, 4, 2, 128
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 72)
+    seq = torch.as_tensor(np.asarray([300, 140], np.int32), device=dev)
+    spans = sa.mask_spans(seq, L, causal=True)
+    attn = sa.SigmoidAttention(bias=-3.0, cap=20.0)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+
+    def step():
+        out = attn(*leaves, seq, spans=spans)
+        return (out.detach(), *torch.autograd.grad(out, leaves, do))
+
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream(dev).wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in (73, 74):
+        new = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, seed)
+        with torch.no_grad():
+            for t, u in zip((*leaves, do), new):
+                t.copy_(u)
+        graph.replay()
+        torch.cuda.synchronize()
+        a = dict(spans=spans, cap=20.0)
+        assert torch.equal(outs[0], sa.fwd_span(*new[:3], seq, D ** -0.5, -3.0, **a))
+        for got, want in zip(outs[1:], sa.bwd_span(*new, seq, D ** -0.5, -3.0, **a)):
+            assert torch.equal(got, want)
