@@ -142,12 +142,12 @@ sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream
     // The tile kernel needs nothing of the prefix kernel's, and the join reads
     // its lengths before it waits: both may start early.
     s = launch_with(paged_tiles_kernel<D, SCORE>, dim3(p.groups * p.heads_wide), dim3(kPagedThreads), Lay::bytes(SIGATTN_PAGED_MAX_Z),
-                    Lay::bytes(p.Z), p.splits > 0, st, m.k, m.v, p);
+                    Lay::bytes(p.Z), p.splits > 0, 1u, st, m.k, m.v, p);
     if (s != SIGATTN_OK) return s;
     const int64_t rows = static_cast<int64_t>(p.Z) * p.L * p.H;
     auto join = [&](auto kernel, int per_block) {
         return launch_with(kernel, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)), dim3(kJoinThreads),
-                           0, 0, true, st, p);
+                           0, 0, true, 1u, st, p);
     };
     if (rows <= kJoin8Rows) return join(paged_join_kernel<D, 8>, 1);
     if (rows <= kJoin4Rows) return join(paged_join_kernel<D, 4>, 2);

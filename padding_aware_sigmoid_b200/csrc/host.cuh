@@ -159,10 +159,11 @@ inline std::unordered_set<FuncDev, FuncDevHash> g_attr_set;
 
 // smem_most: the most dynamic shared memory any call asks of this kernel.
 // overlap: the kernel may start while the one before it on the stream still
-// runs (programmatic dependent launch); it waits for it by itself.
+// runs (programmatic dependent launch); it waits for it by itself.  cluster: blocks
+// of a cluster, along x.
 template <typename... KArgs, typename... Args>
 sigattn_status launch_with(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem_most, size_t smem,
-                           bool overlap, cudaStream_t stream, Args... args) {
+                           bool overlap, unsigned cluster, cudaStream_t stream, Args... args) {
     if (smem_most > 48 * 1024) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
@@ -181,11 +182,18 @@ sigattn_status launch_with(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = overlap ? 1 : 0;
+    cudaLaunchAttribute attrs[2] = {};
+    cfg.attrs = attrs;
+    if (overlap) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs].val.clusterDim.x = cluster;
+        attrs[cfg.numAttrs].val.clusterDim.y = 1;
+        attrs[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) return cuda_fail(e);
     return SIGATTN_OK;
@@ -193,7 +201,7 @@ sigattn_status launch_with(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
 template <typename... KArgs, typename... Args>
 sigattn_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                       Args... args) {
-    return launch_with(kernel, grid, block, smem, smem, false, stream, args...);
+    return launch_with(kernel, grid, block, smem, smem, false, 1u, stream, args...);
 }
 
 }  // namespace sigattn

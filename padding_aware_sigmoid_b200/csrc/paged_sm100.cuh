@@ -734,7 +734,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int u = 0; u < 2; ++u) {
                     uint32_t x[32], pk[16];
                     tmem_ld32(tS + 32 * u, x);
-                    score_chunk<MODE, SCORE, false, true>(x, cf, pos - static_cast<float>(key0 + 32 * u), pk, nullptr, pause);
+                    score_chunk<MODE, SCORE, false, true>(x, cf, pos - static_cast<float>(key0 + 32 * u), pk, nullptr, pause,
+                                                          prefix - key0 >= 64, live);
                     if (prefix - key0 < 64) keep_bits(pk, bit_range(0, prefix - key0 - 32 * u));
                     tmem_st16(tS + 16 * u, pk);
                 }

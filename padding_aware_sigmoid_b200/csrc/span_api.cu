@@ -76,6 +76,14 @@ bool heads_first(const SpanArgs &a, int tensors, int64_t tiles) {
     return tiles <= 65535 && static_cast<int64_t>(tensors) * a.Z * a.L * a.Hk * a.D * 2 <= kStreamMost;
 }
 
+// Blocks that share a tile (span_split.cuh): doubled while the grid stays within
+// `most` blocks and each block keeps four of the `steps` that a tile can have.
+unsigned split_of(int64_t blocks, int64_t most, int64_t steps) {
+    unsigned c = 1;
+    while (c < kMostSplit && blocks * c * 2 <= most && steps >= int64_t(8) * c) c *= 2;
+    return c;
+}
+
 // blocks of kF32Rows rows of one head
 unsigned f32_blocks(const SpanArgs &a, int heads) {
     return static_cast<unsigned>((static_cast<int64_t>(a.L) + kF32Rows - 1) / kF32Rows * heads * a.Z);
@@ -205,7 +213,9 @@ sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, voi
     const int per = D == 64 ? SpanTiles<64>::N : SpanTiles<128>::N;
     const unsigned pairs = static_cast<unsigned>((tiles_of(L) + per - 1) / per);
     p.heads_first = heads_first(a, 2, pairs);
-    return launch_span_fwd(kind_of(a), p.heads_first ? dim3(H, pairs, Z) : dim3(pairs, H, Z), mq, mk, mv, p, st);
+    p.split = split_of(static_cast<int64_t>(pairs) * H * Z, int64_t(g_sm_count[dev]) * (2 / per), tiles_of(L));
+    return launch_span_fwd(kind_of(a), p.heads_first ? dim3(H * p.split, pairs, Z) : dim3(pairs * p.split, H, Z), mq, mk, mv,
+                           p, st);
 }
 
 size_t sigattn_bwd_span_workspace_bytes(int Z, int L, sigattn_dtype dtype) {
@@ -274,10 +284,15 @@ sigattn_status sigattn_bwd_span(const void *q, const void *k, const void *v, con
     // dK/dV first: its blocks are the longer ones (a key head's queries of all its
     // heads), and dQ's fill in behind them
     p.heads_first = heads_first(a, 2 * p.group, tiles);
-    s = launch_span_dkdv(kind_of(a), p.heads_first ? dim3(Hk, tiles, Z) : dim3(tiles, Hk, Z), mq, mk, mv, mdo, p, st);
+    const int64_t sms = g_sm_count[dev], slots = sms * (D == 64 ? 2 : 1), key_tiles = static_cast<int64_t>(tiles) * Hk * Z;
+    p.split = split_of(key_tiles, p.group == 1 ? sms : p.group < 8 ? slots : 2 * slots, static_cast<int64_t>(tiles) * p.group);
+    s = launch_span_dkdv(kind_of(a), p.heads_first ? dim3(Hk * p.split, tiles, Z) : dim3(tiles * p.split, Hk, Z), mq, mk, mv,
+                         mdo, p, st);
     if (s != SIGATTN_OK) return s;
     p.heads_first = heads_first(a, 2, tiles);
-    return launch_span_dq(kind_of(a), p.heads_first ? dim3(H, tiles, Z) : dim3(tiles, H, Z), mq, mk, mv, mdo, p, st);
+    p.split = split_of(static_cast<int64_t>(tiles) * H * Z, sms, tiles);
+    return launch_span_dq(kind_of(a), p.heads_first ? dim3(H * p.split, tiles, Z) : dim3(tiles * p.split, H, Z), mq, mk, mv,
+                          mdo, p, st);
 }
 
 sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix, const int32_t *docs, int causal,

@@ -27,6 +27,7 @@
 
 #include "bwd_sm100.cuh"
 #include "span_score.cuh"
+#include "span_split.cuh"
 
 namespace sigattn {
 
@@ -35,6 +36,7 @@ struct SpanBwdParams {
     SpanSource src;
     int H, Hk, group;
     int heads_first;       // grid (heads, tiles, samples) instead of (tiles, heads, samples)
+    unsigned split;        // blocks of a cluster that share a tile (1: none); x is that much wider
     float alpha, bias, cap;
     const float *bias_z, *slopes;
     const int2 *clean;     // [Z][tiles * 128] clipped spans (span_prep_kernel)
@@ -118,6 +120,7 @@ struct SpanBwdLayout {
     static constexpr int SMEM_ALLOC = OFF_HULL + 8 * (SG::kThreads / 32) + 1024;
     static constexpr uint32_t TMEM_COLS = SG::kHalf ? 256 : 512;
     static_assert((DQ ? 3 * SG::kStep + D : 2 * SG::kStep + 2 * D) <= TMEM_COLS, "TMEM budget");
+    static_assert((DQ ? D : 2 * D) * 128 * 4 <= OFF_BAR, "a split's sums fit the tiles' place");
     static_assert(SG::kPerSm * TMEM_COLS <= 512 && SG::kPerSm * (SMEM_ALLOC + 1024) <= 228 * 1024, "SM budget");
 };
 
@@ -160,7 +163,8 @@ __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_
     float2 g[16];
     auto gains = [&](int ch) {
         uint32_t unused[16];
-        score_chunk<MODE, SCORE, true>(r + 32 * ch, cf, static_cast<float>(row - first - 32 * ch), unused, g, pause);
+        score_chunk<MODE, SCORE, true>(r + 32 * ch, cf, static_cast<float>(row - first - 32 * ch), unused, g, pause,
+                                         whole);
     };
     gains(0);   // before dP is waited for
     const uint32_t dc = dcol + SG::kCols * w;
@@ -189,12 +193,13 @@ __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_
 // dkdv_sigma_tile (bwd_sm100.cuh) with the masked score function: one query
 // tile of a dK/dV sigma warpgroup, whose columns are the queries from q_first
 // on.  `key` is this thread's key; `whole`: every row of the tile sees every
-// key of this CTA's tile; otherwise `clean` points at the spans of the columns (lane i reads column i).
+// key of this CTA's tile; keys_there: none of this warp's keys is padding; otherwise `clean` points at the spans of the columns (lane i reads column i).
 template <int D, int MODE, int SCORE>
 __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_t *s_full, uint64_t *s_free,
                                                uint64_t *dp_full, uint64_t *p_ready, uint64_t *ds_ready,
                                                uint32_t par, const ScoreCoef &cf, int key, int q_first,
-                                               bool whole, const int2 *clean, ScorePause &pause, const WaitCtx &wctx) {
+                                               bool whole, bool keys_there, const int2 *clean, ScorePause &pause,
+                                               const WaitCtx &wctx) {
     using SG = SpanBwdShape<D, false>;
     constexpr int W = SG::kPacked / 16;   // words of 32 columns
     float2 g[SG::kPacked];
@@ -241,7 +246,7 @@ __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_
 #pragma unroll
         for (int u = 0; u < W; ++u)
             score_chunk<MODE, SCORE, true>(r + 32 * u, cf, rel - static_cast<float>(32 * u), pk + 16 * u, g + 16 * u,
-                                           pause);
+                                           pause, whole && keys_there);
     }
     auto keep = [&](uint32_t (&x)[SG::kPacked]) {
 #pragma unroll
@@ -301,7 +306,7 @@ __device__ __forceinline__ bool span_ring_load(const CUtensorMap *map, uint64_t 
 // dQ: one CTA per 128-row query tile (the last rows' tiles first).  Tensor
 // memory as bwd_dq_kernel, in steps of kStep keys: S, dP of even and of odd steps,
 // dQ.
-template <int D, int MODE, int SCORE>
+template <int D, int MODE, int SCORE, bool SPLIT>
 __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<D, true>::kPerSm)
     span_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -328,21 +333,25 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_ABORT);
 
     const int warp = warp_id(), lane = lane_id();
-    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), h = p.heads_first ? blockIdx.x : blockIdx.y;
+    const int split = SPLIT ? static_cast<int>(p.split) : 1;
+    const SplitPlace at = split_place(split);
+    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), h = p.heads_first ? at.x : blockIdx.y;
     const int kvh = h / p.group;
-    const int tiles = p.heads_first ? gridDim.y : gridDim.x;
-    const int qtile = tiles - 1 - static_cast<int>(p.heads_first ? blockIdx.y : blockIdx.x);
+    const int tiles = p.heads_first ? gridDim.y : at.wide;
+    const int qtile = tiles - 1 - (p.heads_first ? static_cast<int>(blockIdx.y) : at.x);
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     const bool last = blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
     const int4 hull = __ldg(&p.hull[static_cast<size_t>(z) * tiles + qtile]);
     if (hull.y == 0) {
         // no row of this tile sees a key: zeros, written by every thread
-        zero_rows<D>(p.dq, z, h, qtile * 128, min(128, L - qtile * 128), L, p.H);
+        if (at.rank == 0) zero_rows<D>(p.dq, z, h, qtile * 128, min(128, L - qtile * 128), L, p.H);
         if (last) grid_wait();
         return;
     }
-    const int J0 = hull.x / 128, steps = (hull.y + 127) / 128 - J0;     // key tiles
+    const int K0 = hull.x / 128, all_steps = (hull.y + 127) / 128 - K0;     // key tiles
+    const int begin = split_step(all_steps, at.rank, split);
+    const int J0 = K0 + begin, steps = split_step(all_steps, at.rank + 1, split) - begin;   // this block's
     const bool ragged = (n & 127) != 0 && J0 + steps == (n + 127) / 128;
     if (threadIdx.x == 0) {
         mbar_init(res_full, 1);
@@ -427,7 +436,8 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
             }
         };
         const int all = steps * NP;
-        bool ok = wait(res_full, 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
+        // (a block without a step still waits for its resident tiles, whose place its sums take)
+        bool ok = wait(res_full, 0) && (!SPLIT || steps > 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
         if (ok) {
             tc_fence_after();
             issue_xyT(kColS, sQ, krows(0));
@@ -492,8 +502,12 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
         constexpr int kEpi = D / SG::NG;
         if (ok) {
             tc_fence_after();
-            store_row_from_tmem<D>(tmem + lane_bits + kColDQ, drow, row < L, span.x < span.y, p.alpha, w * kEpi,
-                                   kEpi);
+            if constexpr (SPLIT)
+                split_leave(reinterpret_cast<float4 *>(smem), tmem + lane_bits + kColDQ + w * kEpi, w * kEpi, kEpi,
+                            quarter * 32 + lane, steps == 0);
+            else
+                store_row_from_tmem<D>(tmem + lane_bits + kColDQ, drow, row < L, span.x < span.y, p.alpha, w * kEpi,
+                                       kEpi);
         }
     }
 
@@ -503,6 +517,19 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
         tc_fence_after();
         tmem_dealloc(tmem, Lay::TMEM_COLS);
     }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_meet();
+        split_add(reinterpret_cast<const float4 *>(smem), D / 8, at.rank, split, threadIdx.x, SG::kThreads,
+                  [&](int octet, int r, const float (&x)[8]) {
+                      const int i = qtile * 128 + r;
+                      if (i >= L) return;
+                      const int2 s = p.clean[static_cast<size_t>(z) * tiles * 128 + i];
+                      reinterpret_cast<uint4 *>(p.dq + ((static_cast<size_t>(z) * L + i) * p.H + h) * D)[octet] =
+                          split_pack(x, p.alpha, s.x < s.y);
+                  });
+        cluster_meet();     // the others may still read this block's sums
+    }
     // whatever follows on the stream waits for this kernel alone: it has to end after
     // the dK/dV kernel, beside whose last blocks it may have started
     if (last) grid_wait();
@@ -511,7 +538,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
 // dK/dV: one CTA per 128-key tile of a key head; streams the query tiles that
 // meet it, head after head of its group.  Tensor memory as bwd_dkdv_kernel, in
 // steps of kStep queries: S^T, dP^T then P^T and dS^T over it, dV, dK.
-template <int D, int MODE, int SCORE>
+template <int D, int MODE, int SCORE, bool SPLIT>
 __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape<D, false>::kPerSm)
     span_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -540,9 +567,11 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
     int2 *met = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
 
     const int warp = warp_id(), lane = lane_id();
-    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), kvh = p.heads_first ? blockIdx.x : blockIdx.y;
-    const int tiles = p.heads_first ? gridDim.y : gridDim.x;
-    const int ktile = p.heads_first ? blockIdx.y : blockIdx.x;
+    const int split = SPLIT ? static_cast<int>(p.split) : 1;
+    const SplitPlace at = split_place(split);
+    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), kvh = p.heads_first ? at.x : blockIdx.y;
+    const int tiles = p.heads_first ? gridDim.y : at.wide;
+    const int ktile = p.heads_first ? blockIdx.y : at.x;
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     const int k0 = ktile * 128, k1 = min(k0 + 128, n);
@@ -572,12 +601,16 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
     }
     if (I1 < 0) {
         // no row sees a key of this tile: zeros, written by every thread
+        if (at.rank > 0) return;
         const int rows = min(128, L - k0);
         zero_rows<D>(p.dk, z, kvh, k0, rows, L, p.Hk);
         zero_rows<D>(p.dv, z, kvh, k0, rows, L, p.Hk);
         return;
     }
-    const int per_head = I1 - I0 + 1, steps = per_head * p.group;     // query tiles
+    // query tiles of a head; this block's steps and its first head and query tile
+    const int per_head = I1 - I0 + 1, all_steps = per_head * p.group;
+    const int begin = split_step(all_steps, at.rank, split), steps = split_step(all_steps, at.rank + 1, split) - begin;
+    const int head0 = kvh * p.group + begin / per_head, first_tile = I0 + begin % per_head;
     const bool ragged = (n & 127) != 0 && I1 == n / 128;
     if (threadIdx.x == 0) {
         mbar_init(res_full, 1);
@@ -617,7 +650,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
 
     if (warp == 0) {
         if (lane == 0) {
-            int ix = 0, iy = 0, i = I0, h = kvh * p.group;
+            int ix = 0, iy = 0, i = first_tile, h = head0;
             for (int r = 0; r < steps; ++r) {
                 if (!span_ring_load<SX, Lay::NSUB>(&tmQ, x_full, x_empty, smem + Lay::OFF_X, Lay::TILE_BYTES, r,
                                                    i * 128, h, z, wctx))
@@ -640,7 +673,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
         }
     } else if (SG::kAux > 2 && warp == 2) {
         if (lane == 0) {
-            int iy = 0, i = I0, h = kvh * p.group;
+            int iy = 0, i = first_tile, h = head0;
             for (int r = 0; r < steps; ++r) {
                 if (!span_ring_load<SY, Lay::NSUB>(&tmDO, y_full, y_empty, smem + Lay::OFF_Y, Lay::TILE_BYTES, r,
                                                    i * 128, h, z, wctx))
@@ -683,7 +716,8 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
                            idesc_kv, (!first || kk > 0) ? 1u : 0u);
         };
         const int all = steps * NP;
-        bool ok = wait(res_full, 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
+        // (a block without a step still waits for its resident tiles, whose place its sums take)
+        bool ok = wait(res_full, 0) && (!SPLIT || steps > 0) && wait(&x_full[0], 0) && wait(&y_full[0], 0);
         if (ok) {
             tc_fence_after();
             issue_xyT(kColS, sK, qrows(0));
@@ -691,7 +725,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
             issue_xyT(kColDP, sV, dorows(0));
             mma_commit_w(dp_full);
         }
-        int left = per_head;          // query tiles left of this head
+        int left = I1 + 1 - first_tile;          // query tiles left of this head
         for (int r = 0; ok && r < all; ++r) {
             const bool more = r + 1 < all;
             const int t = r / NP, t1 = (r + 1) / NP;      // tiles of this step and the next
@@ -746,7 +780,8 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
         const uint32_t tS = tmem + lane_bits + kColS + SG::kCols * w;
         const uint32_t tD = tmem + lane_bits + kColDP + SG::kCols * w;
         const float bias = bias_of(p.bias_z, p.bias, z);
-        int i = I0, h = kvh * p.group, part = 0;
+        const bool keys_there = k0 + quarter * 32 + 32 <= n;
+        int i = first_tile, h = head0, part = 0;
         ScoreCoef cf = make_score<SCORE>(p.alpha, bias, p.cap, SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
         bool ok = true;
         ScorePause pause = score_pause(cf);
@@ -755,7 +790,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
             const bool whole = t.z <= k0 && t.w >= k1;
             const int row0 = i * 128 + part * SG::kStep;
             ok = span_dkdv_tile<D, MODE, SCORE>(tS, tD, s_full, s_free, dp_full, p_ready, ds_ready, r & 1, cf, key,
-                                                row0 + SG::kCols * w, whole, clean + row0, pause, wctx);
+                                                row0 + SG::kCols * w, whole, keys_there, clean + row0, pause, wctx);
             if (!ok) break;
             if (++part < NP) continue;
             part = 0;
@@ -770,8 +805,13 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
         if (ok) {
             tc_fence_after();
-            store_row_from_tmem<D>(tmem + lane_bits + (is_dv ? kColDV : kColDK), dst, key < L, key < n,
-                                   is_dv ? 1.0f : p.alpha, (w % kOut) * (D / kOut), D / kOut);
+            const uint32_t sums = tmem + lane_bits + (is_dv ? kColDV : kColDK);
+            const int col = (w % kOut) * (D / kOut);
+            if constexpr (SPLIT)
+                split_leave(reinterpret_cast<float4 *>(smem), sums + col, (is_dv ? 0 : D) + col, D / kOut,
+                            quarter * 32 + lane, steps == 0);
+            else
+                store_row_from_tmem<D>(sums, dst, key < L, key < n, is_dv ? 1.0f : p.alpha, col, D / kOut);
         }
     }
 
@@ -780,6 +820,20 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, Lay::TMEM_COLS);
+    }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_meet();
+        split_add(reinterpret_cast<const float4 *>(smem), 2 * D / 8, at.rank, split, threadIdx.x, SG::kThreads,
+                  [&](int octet, int r, const float (&x)[8]) {
+                      const int j = k0 + r;
+                      if (j >= L) return;
+                      const bool dv = octet < D / 8;
+                      const size_t row = ((static_cast<size_t>(z) * L + j) * p.Hk + kvh) * D;
+                      reinterpret_cast<uint4 *>((dv ? p.dv : p.dk) + row)[octet % (D / 8)] =
+                          split_pack(x, dv ? 1.0f : p.alpha, j < n);
+                  });
+        cluster_meet();     // the others may still read this block's sums
     }
 }
 

@@ -6,7 +6,10 @@ sigattn_status launch_span_dq(const SpanKind &kind, dim3 grid, const CUtensorMap
                                const CUtensorMap &mv, const CUtensorMap &mdo, const SpanBwdParams &p, cudaStream_t st) {
     return with_kind(kind, [&]<int D, int MODE, int SCORE>() {
         constexpr int kSmem = SpanBwdLayout<D, true>::SMEM_ALLOC;
-        return launch_with(span_dq_kernel<D, MODE, SCORE>, grid, dim3(SpanBwdShape<D, true>::kThreads), kSmem, kSmem, true, st, mq, mk, mv, mdo, p);
+        auto run = [&](auto kernel) {
+            return launch_with(kernel, grid, dim3(SpanBwdShape<D, true>::kThreads), kSmem, kSmem, true, p.split, st, mq, mk, mv, mdo, p);
+        };
+        return p.split > 1 ? run(span_dq_kernel<D, MODE, SCORE, true>) : run(span_dq_kernel<D, MODE, SCORE, false>);
     });
 }
 

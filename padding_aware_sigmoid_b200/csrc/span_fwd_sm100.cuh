@@ -24,6 +24,7 @@
 
 #include "fwd_sm100.cuh"
 #include "span_score.cuh"
+#include "span_split.cuh"
 
 namespace sigattn {
 
@@ -35,6 +36,7 @@ struct SpanFwdParams {
     const float *bias_z;   // device float[Z] or null
     const float *slopes;   // device float[H] or null
     int heads_first;       // grid (heads, pairs, samples) instead of (pairs, heads, samples)
+    unsigned split;        // blocks of a cluster that share the tiles (1: none); x is that much wider
     uint64_t timeout_ns;
 };
 
@@ -71,6 +73,7 @@ struct SpanFwdLayout {
     static constexpr uint32_t COL_S = 0, COL_O = 128 * NT;         // S_t, then O_t
     static constexpr uint32_t TMEM_COLS = NT * (128 + D) > 256 ? 512 : 256;
     static_assert(NT * (128 + D) <= TMEM_COLS && SpanTiles<D>::kPerSm * TMEM_COLS <= 512, "TMEM budget");
+    static_assert(NT * D * 128 * 4 <= OFF_BAR, "a split's sums fit the tiles' place");
     static_assert(SpanTiles<D>::kPerSm * (SMEM_ALLOC + 1024) <= 228 * 1024, "shared memory budget");
 };
 
@@ -86,7 +89,7 @@ struct SpanParts {
     static constexpr int N = D == 64 || (SCORE & kScoreCap) ? 2 : 1;
 };
 
-template <int D, int MODE, int SCORE>
+template <int D, int MODE, int SCORE, bool SPLIT>
 __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
     span_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const SpanFwdParams p) {
@@ -110,9 +113,11 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
     int2 *hull = reinterpret_cast<int2 *>(smem + Lay::OFF_HULL);
 
     const int warp = warp_id(), lane = lane_id();
-    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), h = p.heads_first ? blockIdx.x : blockIdx.y;
+    const int split = SPLIT ? static_cast<int>(p.split) : 1;
+    const SplitPlace at = split_place(split);
+    const int z = span_sample(p.src.seqlens, gridDim.z, blockIdx.z), h = p.heads_first ? at.x : blockIdx.y;
     const int kvh = h / p.group;
-    const int qtile0 = NT * static_cast<int>(p.heads_first ? gridDim.y - 1 - blockIdx.y : gridDim.x - 1 - blockIdx.x);
+    const int qtile0 = NT * (p.heads_first ? static_cast<int>(gridDim.y - 1 - blockIdx.y) : at.wide - 1 - at.x);
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     const int loads = min(max((n + 127) / 128 - qtile0, 0), NT);     // query tiles below n
@@ -175,10 +180,22 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
         for (int e = threadIdx.x; e < rows * V4; e += kThreads) {
             uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<size_t>(z) * L + r0 + e / V4) * row_stride +
                                                    static_cast<size_t>(h) * D);
-            dst[e % V4] = make_uint4(0u, 0u, 0u, 0u);
+            if (at.rank == 0) dst[e % V4] = make_uint4(0u, 0u, 0u, 0u);
         }
         if (threadIdx.x == 0 && loads > 0) mbar_wait_drain(q_full, 0, p.timeout_ns);
         return;
+    }
+    if constexpr (SPLIT) {
+        // this block's part of the key tiles
+        const int a = J0 + split_step(J1 - J0, at.rank, split), b = J0 + split_step(J1 - J0, at.rank + 1, split);
+        J0 = a;
+        J1 = b;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            j0[t] = max(j0[t], a);
+            j1[t] = min(j1[t], b);
+            if (j0[t] >= j1[t]) j0[t] = j1[t] = 0;
+        }
     }
     const int steps = J1 - J0;
     // the last key tile, when n ends inside it: its value rows are cleaned
@@ -268,7 +285,8 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
         // j + 1 over it.  MMAs from one thread run in issue order, so P has been
         // read before the next scores are written.  A key tile that neither visits
         // (a gap between the two hulls) passes through the rings unread.
-        bool ok = wt(q_full, 0) && wt(&k_full[0], 0);
+        // (a block without a step still waits for its query tiles, whose place its sums take)
+        bool ok = wt(q_full, 0) && (!SPLIT || steps > 0) && wt(&k_full[0], 0);
         if (ok) {
             tc_fence_after();
 #pragma unroll
@@ -344,7 +362,7 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
                         uint32_t r[32];
                         tmem_ld32(tS + 32 * u, r);
                         score_chunk<MODE, SCORE, false, true>(r, cf, static_cast<float>(row - key0 - 32 * u), pk, nullptr,
-                                                        pause);
+                                                              pause, whole);
                         if (!whole) keep_bits(pk, bit_range(span.x - key0 - 32 * u, span.y - key0 - 32 * u));
                     } else {
                         // none of the warp's rows sees any of the half
@@ -364,7 +382,15 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
         constexpr int HALF = D / 2;
         __nv_bfloat16 *orow = p.o + (static_cast<size_t>(z) * L + row) * row_stride +
                               static_cast<size_t>(h) * D + c * HALF;
-        if (jb > 0) {
+        if constexpr (SPLIT) {
+            // the sums take the place of tiles that the other query tile may still use
+            if (jb == 0) ok = __all_sync(0xffffffffu, mbar_wait(drain, 0, wctx));
+            if (ok) {
+                tc_fence_after();
+                split_leave(reinterpret_cast<float4 *>(smem), tmem + lane_bits + Lay::COL_O + D * t + c * HALF,
+                            D * t + c * HALF, HALF, quarter * 32 + lane, jb == 0);
+            }
+        } else if (jb > 0) {
             if (ok) {
                 tc_fence_after();
                 const uint32_t tO = tmem + lane_bits + Lay::COL_O + D * t + c * HALF;
@@ -402,6 +428,20 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, Lay::TMEM_COLS);
+    }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_meet();
+        split_add(reinterpret_cast<const float4 *>(smem), NT * D / 8, at.rank, split, threadIdx.x, kThreads,
+                  [&](int octet, int r, const float (&x)[8]) {
+                      const int i = (qtile0 + octet / (D / 8)) * 128 + r;
+                      if (i >= L) return;
+                      const int2 s = row_span(p.src, z, i, n);
+                      reinterpret_cast<uint4 *>(p.o + (static_cast<size_t>(z) * L + i) * row_stride +
+                                                static_cast<size_t>(h) * D)[octet % (D / 8)] =
+                          split_pack(x, 1.0f, s.x < s.y);
+                  });
+        cluster_meet();     // the others may still read this block's sums
     }
 }
 

@@ -132,13 +132,15 @@ __device__ __forceinline__ ScorePause score_pause(const ScoreCoef &cf) {
 // P (packed bf16) of 32 neighbouring columns of this thread's row, and with GRAD g
 // = dP/d(alpha s), in TANH mode with the forms POLY (of the cap) and TAIL (of
 // sigma); returns whether both hold for all 32 x 32 scores of the warp (bit 0: the
-// cap's does not, bit 1: the tail's).
+// cap's does not, bit 1: the tail's).  A lane whose row is not there (`live`) has no
+// say.
 //
 // TAIL: in the left tail, u = e^x <= 1/32, sigma = u - u^2 and sigma' = u - 2 u^2 (+
 // O(u^3)) from one ex2: as many MUFU and FMA operations as the tanh form, but a
 // relative error of at most u^2 <= 1e-3 where 0.5 + 0.5 tanh cancels (up to 1.4%).
 template <int SCORE, bool GRAD, bool POLY, bool TAIL>
-__device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk, float2 *g) {
+__device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk, float2 *g,
+                                          bool live) {
     ScoreCoef cx = cf;
     if constexpr (!TAIL) {     // tanh wants x / 2
         constexpr float kHalfLn2 = 0.34657359f;
@@ -172,8 +174,8 @@ __device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf
         pk[i] = pack_bf16x2(p.x, p.y);
     }
     int bad = 0;
-    if constexpr (POLY) bad |= __any_sync(0xffffffffu, largest > cf.most) ? 1 : 0;
-    if constexpr (TAIL) bad |= __any_sync(0xffffffffu, top > kTailMost) ? 2 : 0;
+    if constexpr (POLY) bad |= __any_sync(0xffffffffu, live && largest > cf.most) ? 1 : 0;
+    if constexpr (TAIL) bad |= __any_sync(0xffffffffu, live && top > kTailMost) ? 2 : 0;
     return bad;
 }
 
@@ -184,7 +186,9 @@ __device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf
 // afterwards (the largest s^2 and u, as integers, which order like positive
 // floats); where one does not hold, the chunk is done again without it, and the
 // next kPause chunks of the warp skip it, so that rows of large scores do not pay
-// twice.
+// twice.  Chunks of which some pair is masked (not `whole`) are not tried: what a masked
+// key or a row of padding holds must not choose the form, and with it the last bits,
+// of the pairs that count.
 //
 // The tail form is for b = -ln n of long rows, where nearly every chunk fits:
 // 2-norm error of O 3.3e-3 -> 2.3e-3 at n = 16384 (at n = 2048 the tanh alone has
@@ -199,7 +203,7 @@ __device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf
 // its operands (D = 128 547 -> 663 us).
 template <int MODE, int SCORE, bool GRAD, bool FWD = false>
 __device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk,
-                                            float2 *g, ScorePause &pause) {
+                                            float2 *g, ScorePause &pause, bool whole, bool live = true) {
     if constexpr (MODE == kSigmoidExp) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -216,25 +220,29 @@ __device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &
             pk[i] = pack_bf16x2(p.x, p.y);
         }
     } else if constexpr (FWD && SCORE == kScoreCap) {
-        if (pause.poly == 0) {
-            int bad = 2;
+        if (whole) {
+            if (pause.poly == 0) {
+                int bad = 2;
+                if (pause.tail == 0) {
+                    if ((bad = score_form<SCORE, GRAD, true, true>(r, cf, rel, pk, g, live)) == 0) return;
+                    pause.tail = kPause + 1;
+                }
+                --pause.tail;
+                if (!(bad & 1) && score_form<SCORE, GRAD, true, false>(r, cf, rel, pk, g, live) == 0) return;
+                pause.poly = kPause + 1;
+            }
+            --pause.poly;
+        }
+        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g, live);
+    } else {
+        if (whole) {
             if (pause.tail == 0) {
-                if ((bad = score_form<SCORE, GRAD, true, true>(r, cf, rel, pk, g)) == 0) return;
+                if (score_form<SCORE, GRAD, false, true>(r, cf, rel, pk, g, live) == 0) return;
                 pause.tail = kPause + 1;
             }
             --pause.tail;
-            if (!(bad & 1) && score_form<SCORE, GRAD, true, false>(r, cf, rel, pk, g) == 0) return;
-            pause.poly = kPause + 1;
         }
-        --pause.poly;
-        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g);
-    } else {
-        if (pause.tail == 0) {
-            if (score_form<SCORE, GRAD, false, true>(r, cf, rel, pk, g) == 0) return;
-            pause.tail = kPause + 1;
-        }
-        --pause.tail;
-        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g);
+        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g, live);
     }
 }
 // P of two neighbouring columns to about 2^-20, for kernels whose scores are few:

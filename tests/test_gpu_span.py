@@ -186,10 +186,11 @@ def test_nan_in_padding_never_reaches_a_result(dev, dtype, D):
 
 def test_equals_the_padding_only_call_without_terms(dev, exp_mode):
     """No spans, no cap, no slopes, the EXP form: the same operation as fwd / bwd, to the bit (in TANH mode the masked kernels
-    take a more accurate form in sigma's left tail)."""
-    Z, L, H, D = 2, 700, 2, 128
+    take a more accurate form in sigma's left tail), in a batch that fills the device: a smaller one adds its sums up in
+    another order, over the blocks that share a tile."""
+    Z, L, H, D = 24, 700, 16, 128
     q, k, v, do = _tensors(Z, L, H, H, D, torch.bfloat16, dev, 9)
-    seq = torch.as_tensor(np.asarray([700, 333], np.int32), device=dev)
+    seq = torch.as_tensor(np.asarray([700, 333] * (Z // 2), np.int32), device=dev)
     assert torch.equal(sa.fwd(q, k, v, seq, seq, 0.09, -6.0), sa.fwd_span(q, k, v, seq, 0.09, -6.0))
     for a, b in zip(sa.bwd(q, k, v, do, seq, seq, 0.09, -6.0), sa.bwd_span(q, k, v, do, seq, 0.09, -6.0)):
         assert torch.equal(a, b)
@@ -439,3 +440,67 @@ def test_captured_module_step_replays_with_new_inputs(dev):
         assert torch.equal(outs[0], sa.fwd_span(*new[:3], seq, D ** -0.5, -3.0, **a))
         for got, want in zip(outs[1:], sa.bwd_span(*new, seq, D ** -0.5, -3.0, **a)):
             assert torch.equal(got, want)
+
+
+# few tiles with many steps: 2 or 4 blocks share each (span_split.cuh), some of them without a step of their own
+SHARED = [(1, 2048, 2, 1, 128), (1, 2100, 2, 2, 64), (2, 1500, 2, 1, 64), (1, 1111, 6, 1, 128), (1, 4200, 3, 3, 128), (3, 1030, 2, 1, 64)]
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("shape", SHARED)
+def test_blocks_that_share_a_tile_count_exactly(dev, mask, shape):
+    test_visible_pairs_are_counted_exactly(dev, mask, shape)
+
+
+@pytest.mark.parametrize("case", [(1, 1100, 2, 1, 64, "causal", 20.0, True), (1, 1200, 8, 1, 128, "window", 0.0, False),
+                                  (1, 1025, 2, 2, 128, "prefix", 30.0, True), (1, 2060, 1, 1, 64, "docs_causal", 0.0, False)])
+def test_parity_where_blocks_share_a_tile(dev, exp_mode, case):
+    _run_case(case, dev, torch.bfloat16, False)
+
+
+def test_shared_tiles_keep_nan_in_padding_out_and_repeat_to_the_bit(dev):
+    Z, L, H, Hk, D = 2, 1400, 2, 1, 128
+    n = np.asarray([1390, 700], np.int32)
+    ts = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 81)
+    seq = torch.as_tensor(n, device=dev)
+    spans = _spans("causal", n, L, dev)
+    call = lambda q, k, v, do: (sa.fwd_span(q, k, v, seq, 0.1, -3.0, spans=spans, cap=20.0),      # noqa: E731
+                                *sa.bwd_span(q, k, v, do, seq, 0.1, -3.0, spans=spans, cap=20.0))
+    want = call(*ts)
+    bad = [t.clone() for t in ts]
+    for t in bad:
+        for z in range(Z):
+            t[z, n[z]:] = float("nan")
+    for _ in range(3):
+        for a, b in zip(want, call(*bad)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,bias,sl", [(0.0, -9.5, False), (20.0, -9.5, False), (20.0, -2.0, False), (20.0, -9.5, True)])
+def test_other_documents_and_padding_do_not_change_a_bit(dev, D, cap, bias, sl):
+    """Documents of 100 to 700 tokens: what one of them yields stays the same, to the bit, whatever the others and the padding
+    hold (large scores there choose other forms of the score function for their own chunks only)."""
+    Z, L, H, Hk = 2, 1500, 4, 2
+    n = np.asarray([1490, 1203], np.int32)
+    ids = np.zeros((Z, L), np.int32)
+    for z in range(Z):
+        for edge in (100, 260, 900, 1150, 1300):
+            ids[z, edge + 7 * z:] += 1
+    seq = torch.as_tensor(n, device=dev)
+    docs = torch.as_tensor(ids, device=dev)
+    slopes = torch.linspace(0.1, 0.001, H, device=dev) if sl else None
+    ts = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 91)
+    keep = (docs == 2) & (torch.arange(L, device=dev)[None] < seq[:, None])
+    for causal in (False, True):
+        spans = sa.mask_spans(seq, L, causal=causal, docs=docs)
+        a = dict(spans=spans, cap=cap, slopes=slopes)
+        call = lambda q, k, v, do: (sa.fwd_span(q, k, v, seq, D ** -0.5, bias, **a),      # noqa: E731
+                                    *sa.bwd_span(q, k, v, do, seq, D ** -0.5, bias, **a))
+        want = call(*ts)
+        other = [torch.where(keep[..., None, None], t, u * 30)
+                 for t, u in zip(ts, _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 92))]
+        pad = torch.arange(L, device=dev)[None] >= seq[:, None]
+        other = [t.masked_fill(pad[..., None, None], float("nan")) for t in other]
+        for x, y in zip(want, call(*other)):
+            assert torch.equal(x[keep], y[keep])

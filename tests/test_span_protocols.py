@@ -21,10 +21,8 @@ def _ring_bars(ring, S):
 
 # ------------------------------------------------------------------ forward
 
-def _fwd_mma(j0, j1, KS, VS, NP, early_s=False):
+def _fwd_mma(j0, j1, J0, J1, KS, VS, NP, early_s=False):
     NT = len(j0)
-    J0 = min(a for a, b in zip(j0, j1) if b > 0)
-    J1 = max(j1)
     steps = J1 - J0
     seen = [0] * NT
 
@@ -62,14 +60,16 @@ def _fwd_mma(j0, j1, KS, VS, NP, early_s=False):
     yield ("commit", "drain", 0)
 
 
-def _fwd_sigma(t, part, j0, j1):
-    """A warpgroup of tile t, whose half of the scores part `part` hands over."""
+def _fwd_sigma(t, part, j0, j1, split):
+    """A warpgroup of tile t, whose half of the scores part `part` hands over.  A block that shares its tiles leaves sums for an
+    empty one too, where the other's tiles were."""
     for j in range(j0, j1):
         yield ("wait", f"s_full{t}{part}", j - j0)
         yield ("use", f"s{t}{part}", ("S", j))
         yield ("arrive", f"p_full{t}{part}", j - j0)
-    if j1 > j0:
+    if j1 > j0 or split:
         yield ("wait", "drain", 0)
+    if j1 > j0:
         yield ("use", f"o{t}", j1 - 1)
 
 
@@ -98,19 +98,19 @@ class FwdModel(TurnModel):
     turns = {f"p_full{t}{c}": (f"s{t}{c}", "P") for t in range(2) for c in range(2)}
 
 
-def _fwd(j0, j1, KS, VS, NP, seed, **mistake):
+def _fwd(j0, j1, KS, VS, NP, seed, bounds=None, **mistake):
     NT = len(j0)
-    J0 = min(a for a, b in zip(j0, j1) if b > 0)
-    steps = max(j1) - J0
+    J0, J1 = bounds or (min(a for a, b in zip(j0, j1) if b > 0), max(j1))
+    steps = J1 - J0
     bars = {**_ring_bars("k", KS), **_ring_bars("v", VS), "drain": 1}
     for t in range(NT):
         for c in range(NP):
             bars[f"s_full{t}{c}"] = 1
             bars[f"p_full{t}{c}"] = 2 // NP
-    roles = {"K": _producer(steps, KS, "k"), "V": _producer(steps, VS, "v"), "mma": _fwd_mma(j0, j1, KS, VS, NP, **mistake)}
+    roles = {"K": _producer(steps, KS, "k"), "V": _producer(steps, VS, "v"), "mma": _fwd_mma(j0, j1, J0, J1, KS, VS, NP, **mistake)}
     for t in range(NT):
         for c in range(2):
-            roles[f"wg{t}{c}"] = _fwd_sigma(t, c * NP // 2, j0[t], j1[t])
+            roles[f"wg{t}{c}"] = _fwd_sigma(t, c * NP // 2, j0[t], j1[t], bounds is not None)
     FwdModel(bars, roles, seed).run()
 
 
@@ -123,6 +123,23 @@ RANGES = [((0, 0), (1, 1)), ((0, 0), (7, 8)), ((0, 2), (3, 9)), ((4, 0), (9, 6))
 def test_forward_two_tiles(ranges, NP):
     for seed in range(60):
         _fwd(*ranges, 2, 3, NP, seed)
+
+
+@pytest.mark.parametrize("NP", [1, 2])
+@pytest.mark.parametrize("split", [2, 3, 4])
+@pytest.mark.parametrize("ranges", RANGES)
+def test_forward_shared_by_a_cluster(ranges, split, NP):
+    """Each block's part of the key tiles, gaps between the two hulls among them."""
+    (j0, j1) = ranges
+    J0, J1 = min(a for a, b in zip(j0, j1) if b > 0), max(j1)
+    for rank in range(split):
+        a, b = J0 + (J1 - J0) * rank // split, J0 + (J1 - J0) * (rank + 1) // split
+        if a == b:
+            continue
+        mine = [(max(x, a), min(y, b)) for x, y in zip(j0, j1)]
+        mine = [(x, y) if x < y else (0, 0) for x, y in mine]
+        for seed in range(15):
+            _fwd([x for x, _ in mine], [y for _, y in mine], 2, 3, NP, seed, bounds=(a, b))
 
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 7])
@@ -218,32 +235,52 @@ def test_dq_releasing_a_half_read_tile_is_caught():
 
 # ------------------------------------------------------------------ dK/dV
 
-def _dkdv_mma(tiles, SX, SY, order=True):
+def _dkdv_mma(tiles, SX, SY, NP, order=True):
+    """Steps of 1 / NP of a tile; both rings' slots are released when their tile's last step has been issued (dO's at once where
+    a step is a tile)."""
     yield ("wait", "x_full0", 0)
     yield ("wait", "y_full0", 0)
     yield ("mma", [("x0", 0)], [("s", 0)])
     yield ("commit", "s_full", 0)
     yield ("mma", [("y0", 0)], [("dp", ("dP", 0)), ("ds", ("dP", 0))])
     yield ("commit", "dp_full", 0)
-    for r in range(tiles):
-        nxt = r + 1
-        if nxt < tiles:
-            yield ("wait", f"x_full{nxt % SX}", nxt // SX)
+    for r in range(tiles * NP):
+        nxt, t, t1 = r + 1, r // NP, (r + 1) // NP
+        more, opens, closes = nxt < tiles * NP, nxt % NP == 0, r % NP == NP - 1
+        if more:
+            if opens:
+                yield ("wait", f"x_full{t1 % SX}", t1 // SX)
             yield ("wait", "s_free", r)
-            yield ("mma", [(f"x{nxt % SX}", nxt)], [("s", nxt)])
+            yield ("mma", [(f"x{t1 % SX}", t1)], [("s", nxt)])
             yield ("commit", "s_full", nxt)
         yield ("wait", "p_ready", r)
-        yield ("mma", [("dp", ("P", r)), (f"y{r % SY}", r)], [("dv", r)])
-        yield ("commit", f"y_empty{r % SY}", r // SY)
+        yield ("mma", [("dp", ("P", r)), (f"y{t % SY}", t)], [("dv", r)])
+        if NP == 1:
+            yield ("commit", f"y_empty{t % SY}", t // SY)
         if order:
             yield ("wait", "ds_ready", r)
-        yield ("mma", [("ds", ("dS", r)), (f"x{r % SX}", r)], [("dk", r)])
-        yield ("commit", f"x_empty{r % SX}", r // SX)
-        if nxt < tiles:
-            yield ("wait", f"y_full{nxt % SY}", nxt // SY)
-            yield ("mma", [(f"y{nxt % SY}", nxt)], [("dp", ("dP", nxt)), ("ds", ("dP", nxt))])
+        yield ("mma", [("ds", ("dS", r)), (f"x{t % SX}", t)], [("dk", r)])
+        if closes:
+            if NP > 1:
+                yield ("commit", f"y_empty{t % SY}", t // SY)
+            yield ("commit", f"x_empty{t % SX}", t // SX)
+        if more:
+            if opens:
+                yield ("wait", f"y_full{t1 % SY}", t1 // SY)
+            yield ("mma", [(f"y{t1 % SY}", t1)], [("dp", ("dP", nxt)), ("ds", ("dP", nxt))])
             yield ("commit", "dp_full", nxt)
     yield ("commit", "drain", 0)
+
+
+def _both_rings(n, SX, SY):
+    """One thread that loads a tile of each ring in turn."""
+    x, y = _producer(n, SX, "x"), _producer(n, SY, "y")
+    for _ in range(n):
+        for ring in (x, y):
+            for step in ring:
+                yield step
+                if step[0] == "tma":
+                    break
 
 
 def _dkdv_sigma(n, empty):
@@ -268,16 +305,18 @@ class DkdvModel(TurnModel):
     turns = {"p_ready": ("dp", "P"), "ds_ready": ("ds", "dS")}
 
 
-def _dkdv(tiles, SX, SY, NG, seed, **mistake):
+def _dkdv(tiles, SX, SY, NP, NG, seed, **mistake):
     bars = {**_ring_bars("x", SX), **_ring_bars("y", SY), "s_full": 1, "dp_full": 1, "s_free": NG, "p_ready": NG,
             "ds_ready": NG, "drain": 1}
-    roles = {"X": _producer(tiles, SX, "x"), "Y": _producer(tiles, SY, "y"), "mma": _dkdv_mma(tiles, SX, SY, **mistake)}
+    roles = {"mma": _dkdv_mma(tiles, SX, SY, NP, **mistake)}
+    roles.update({"XY": _both_rings(tiles, SX, SY)} if NP > 1 else
+                 {"X": _producer(tiles, SX, "x"), "Y": _producer(tiles, SY, "y")})
     for g in range(NG):
-        roles[f"wg{g}"] = _dkdv_sigma(tiles, {r for r in range(tiles) if (r + g + seed) % 3 == 0})
+        roles[f"wg{g}"] = _dkdv_sigma(tiles * NP, {r for r in range(tiles * NP) if (r + g + seed) % 3 == 0})
     DkdvModel(bars, roles, seed).run()
 
 
-@pytest.mark.parametrize("shape", [(3, 2, 2), (4, 4, 4)])
+@pytest.mark.parametrize("shape", [(3, 2, 1, 2), (2, 2, 2, 2)])     # D = 128; D = 64 in halves
 @pytest.mark.parametrize("tiles", [1, 2, 3, 9])
 def test_dkdv(shape, tiles):
     for seed in range(60):
@@ -287,7 +326,7 @@ def test_dkdv(shape, tiles):
 def test_dkdv_without_waiting_for_ds_is_caught():
     with pytest.raises(ProtocolError):
         for seed in range(200):
-            _dkdv(5, 3, 2, 2, seed, order=False)
+            _dkdv(5, 3, 2, 1, 2, seed, order=False)
 
 
 # ------------------------------------------------------------------ paged tile kernel
