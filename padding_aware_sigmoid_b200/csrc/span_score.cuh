@@ -220,28 +220,24 @@ __device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &
             pk[i] = pack_bf16x2(p.x, p.y);
         }
     } else if constexpr (FWD && SCORE == kScoreCap) {
-        if (whole) {
-            if (pause.poly == 0) {
-                int bad = 2;
-                if (pause.tail == 0) {
-                    if ((bad = score_form<SCORE, GRAD, true, true>(r, cf, rel, pk, g, live)) == 0) return;
-                    pause.tail = kPause + 1;
-                }
-                --pause.tail;
-                if (!(bad & 1) && score_form<SCORE, GRAD, true, false>(r, cf, rel, pk, g, live) == 0) return;
-                pause.poly = kPause + 1;
-            }
-            --pause.poly;
-        }
-        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g, live);
-    } else {
-        if (whole) {
+        if (whole && pause.poly == 0) {
+            int bad = 2;
             if (pause.tail == 0) {
-                if (score_form<SCORE, GRAD, false, true>(r, cf, rel, pk, g, live) == 0) return;
+                if ((bad = score_form<SCORE, GRAD, true, true>(r, cf, rel, pk, g, live)) == 0) return;
                 pause.tail = kPause + 1;
             }
             --pause.tail;
+            if (!(bad & 1) && score_form<SCORE, GRAD, true, false>(r, cf, rel, pk, g, live) == 0) return;
+            pause.poly = kPause + 1;
         }
+        pause.poly = max(pause.poly - 1, 0);
+        score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g, live);
+    } else {
+        if (whole && pause.tail == 0) {
+            if (score_form<SCORE, GRAD, false, true>(r, cf, rel, pk, g, live) == 0) return;
+            pause.tail = kPause + 1;
+        }
+        pause.tail = max(pause.tail - 1, 0);
         score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g, live);
     }
 }
