@@ -77,7 +77,17 @@ bool heads_first(const SpanArgs &a, int tensors, int64_t tiles) {
 }
 
 // Blocks that share a tile (span_split.cuh): doubled while the grid stays within
-// `most` blocks and each block keeps four of the `steps` that a tile can have.
+// `most` blocks and each block keeps four of the `steps` that a tile can have.  In us,
+// unsplit against split, causal:
+//   forward, most = what fits the device at once: 1 x 8192 tokens, 2 heads, D = 128
+//     126 -> 73, D = 64 81 -> 52; 1 x 4096 67 -> 29, 44 -> 21.  Beyond that it loses: 96 tiles
+//     of at most 16 steps in twos 39.7 -> 35.6, but packed documents 23.9 -> 34.5;
+//   dK/dV, the same where heads are shared (a tile then has at least a step per head),
+//     twice that from eight to a key head: 1 x 2048, 12 over 2 heads 156 -> 57 (D = 128),
+//     197 -> 60 (D = 64); 1 x 8192, 16 over 2 842 -> 745, 1018 -> 567.  Alone in its heads
+//     a block leaves SMs to dQ, and more than a block an SM loses (64 tiles at D = 64 in
+//     fours 71 -> 81, in twos 70);
+//   dQ, a block an SM: 1 x 4096, 2 heads 54 -> 46 (D = 128), 69 -> 46 (D = 64).
 unsigned split_of(int64_t blocks, int64_t most, int64_t steps) {
     unsigned c = 1;
     while (c < kMostSplit && blocks * c * 2 <= most && steps >= int64_t(8) * c) c *= 2;

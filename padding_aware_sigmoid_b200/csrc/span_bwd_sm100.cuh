@@ -75,14 +75,15 @@ static __global__ void __launch_bounds__(128) span_prep_kernel(const SpanSource 
 }
 
 // Shape of the backward blocks.  A step is kStep columns of a streamed 128-row
-// tile (keys in dQ, queries in dK/dV): the whole tile, but half of it in dQ at D =
-// 64, so that scores and accumulator take 256 columns of tensor memory and two
-// blocks share an SM; one's start and end, most of a short document's time, pass
-// while the other computes.  Whole backward, against one block an SM: packed capped
-// documents 133.6 -> 119.1 us, documents 130.7 -> 128.2 us, window 8K 202 -> 200 us;
-// causal 8K 431 -> 440 us, full capped 4K 620 -> 648 us (half steps hand over twice as
-// often).  The same in dK/dV, whose threads hold more, spilled at 80 registers and
-// lost 6 to 25%.
+// tile (keys in dQ, queries in dK/dV): the whole tile, but half of it at D = 64, so
+// that scores and accumulators take 256 columns of tensor memory and two blocks
+// share an SM; one's start and end, most of a short document's time, pass while the
+// other computes.  Whole backward, against one block an SM in both kernels: packed
+// capped documents 133.6 -> 119.4 us, documents 130.7 -> 122.5 us, window 8K 202 -> 198 us,
+// causal 8K 431 -> 425 us, full capped 4K 620 -> 652 us (half steps hand over twice
+// as often).  dK/dV, whose threads hold more, then loads both rings from one warp: two
+// blocks of 320 threads leave 96 registers a thread, of 384 threads 80, which spilled
+// and lost 6 to 25%.
 template <int D, bool DQ>
 struct SpanBwdShape {
     static constexpr bool kHalf = D == 64;
