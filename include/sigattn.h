@@ -252,7 +252,12 @@ size_t sigattn_dbias_workspace_bytes(int Z, int L, int H, sigattn_dtype dtype);
  *
  * Rows at or beyond n may hold anything, NaN included: they are never read into
  * a result.  Within a sample a masked key or query must still be finite (it is
- * multiplied by a weight of zero).
+ * multiplied by a weight of zero); what it holds does not change a bit of the
+ * rows that do not see it.
+ *
+ * The same call gives the same bits every time.  Between calls of other shapes the
+ * order of the fp32 sums may differ: a batch with few tiles splits each tile's keys
+ * or queries over up to four blocks, whose sums are added in order.
  *
  * Outputs must not overlap inputs (the kernels of one call run side by side).
  * sigattn_bwd_span writes dq, dk, dv in full and needs neither O nor any saved
@@ -328,8 +333,8 @@ sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix,
  * exact zeros; cache places that no query sees may hold anything, NaN included.
  * workspace (device, 16-byte aligned, sigattn_fwd_paged_workspace_bytes bytes,
  * 0 for fp32) is overwritten; calls that may overlap, captured graphs included,
- * need one each.  Results do not depend on scheduling.  Z is at most
- * SIGATTN_PAGED_MAX_Z.
+ * need one each.  Results do not depend on scheduling; the last bits of a row may
+ * depend on the other rows of the batch.  Z is at most SIGATTN_PAGED_MAX_Z.
  *
  * Errors of both: SIGATTN_ERR_INVALID_ARG (sigattn_cache_append: also L = 0;
  * sigattn_fwd_paged: also pages = 0), _UNSUPPORTED_HEADDIM,
