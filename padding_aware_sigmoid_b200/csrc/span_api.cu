@@ -99,6 +99,18 @@ unsigned f32_blocks(const SpanArgs &a, int heads) {
     return static_cast<unsigned>((static_cast<int64_t>(a.L) + kF32Rows - 1) / kF32Rows * heads * a.Z);
 }
 
+// Calls f.template operator()<D, G>(): the fp32 kernels with G groups of warps to a
+// block.  Few blocks, or the backward of shared heads, whose blocks of keys run
+// through all of a key head's queries, are bound by a block's length: 2 x 128 tokens,
+// 2 heads, D = 64, backward 13.9 -> 11.0 us with four groups, 4 x 200, 16 over 4 heads 175 ->
+// 141.  Many blocks fill the device without (4 x 200, 12 heads, 89 -> 107 us with them).
+template <typename F>
+sigattn_status with_groups(const SpanArgs &a, int64_t blocks, int sms, bool backward, F &&f) {
+    const bool many = a.L <= kF32Chunk || (blocks > int64_t(4) * sms && !(backward && a.H > a.Hk));
+    if (a.D == 64) return many ? f.template operator()<64, 1>() : f.template operator()<64, 4>();
+    return many ? f.template operator()<128, 1>() : f.template operator()<128, 2>();
+}
+
 // The device's state, for a dtype the device can run.
 sigattn_status span_device(const SpanArgs &a, int *dev, int **status) {
     int cc = 0;
@@ -201,9 +213,11 @@ sigattn_status sigattn_fwd_span(const void *q, const void *k, const void *v, voi
         p.k = static_cast<const float *>(k);
         p.v = static_cast<const float *>(v);
         p.o = static_cast<float *>(o);
-        const dim3 grid(f32_blocks(a, H)), block(32 * kF32Rows);
-        return D == 64 ? launch(span_f32_fwd_kernel<64>, grid, block, 0, st, p)
-                       : launch(span_f32_fwd_kernel<128>, grid, block, 0, st, p);
+        const unsigned blocks = f32_blocks(a, H);
+        return with_groups(a, blocks, g_sm_count[dev], false, [&]<int D_, int G>() {
+            return launch(span_f32_fwd_kernel<D_, G>, dim3(blocks), dim3(SpanF32Smem<D_, G>::kThreads),
+                          sizeof(SpanF32Smem<D_, G>), st, p);
+        });
     }
     CUtensorMap mq, mk, mv;
     if ((s = encode_bf16_map_uncached(&mq, q, Z, L, H, D)) != SIGATTN_OK) return s;
@@ -262,9 +276,11 @@ sigattn_status sigattn_bwd_span(const void *q, const void *k, const void *v, con
         p.dk = static_cast<float *>(dk);
         p.dv = static_cast<float *>(dv);
         const unsigned rows = f32_blocks(a, H);
-        const dim3 grid(rows + f32_blocks(a, Hk)), block(32 * kF32Rows);
-        return D == 64 ? launch(span_f32_bwd_kernel<64>, grid, block, 0, st, p, rows)
-                       : launch(span_f32_bwd_kernel<128>, grid, block, 0, st, p, rows);
+        const unsigned blocks = rows + f32_blocks(a, Hk);
+        return with_groups(a, blocks, g_sm_count[dev], true, [&]<int D_, int G>() {
+            return launch(span_f32_bwd_kernel<D_, G>, dim3(blocks), dim3(SpanF32Smem<D_, G>::kThreads),
+                          sizeof(SpanF32Smem<D_, G>), st, p, rows);
+        });
     }
     CUtensorMap mq, mk, mv, mdo;
     if ((s = encode_bf16_map_uncached(&mq, q, Z, L, H, D)) != SIGATTN_OK) return s;
