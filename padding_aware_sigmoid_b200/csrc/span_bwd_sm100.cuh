@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
     if (hull.y == 0) {
         // no row of this tile sees a key: zeros, written by every thread
         if (at.rank == 0) zero_rows<D>(p.dq, z, h, qtile * 128, min(128, L - qtile * 128), L, p.H);
+        if constexpr (SPLIT) cluster_skip();
         if (last) grid_wait();
         return;
     }
@@ -602,10 +603,12 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
     }
     if (I1 < 0) {
         // no row sees a key of this tile: zeros, written by every thread
-        if (at.rank > 0) return;
         const int rows = min(128, L - k0);
-        zero_rows<D>(p.dk, z, kvh, k0, rows, L, p.Hk);
-        zero_rows<D>(p.dv, z, kvh, k0, rows, L, p.Hk);
+        if (at.rank == 0) {
+            zero_rows<D>(p.dk, z, kvh, k0, rows, L, p.Hk);
+            zero_rows<D>(p.dv, z, kvh, k0, rows, L, p.Hk);
+        }
+        if constexpr (SPLIT) cluster_skip();
         return;
     }
     // query tiles of a head; this block's steps and its first head and query tile

@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
             if (at.rank == 0) dst[e % V4] = make_uint4(0u, 0u, 0u, 0u);
         }
         if (threadIdx.x == 0 && loads > 0) mbar_wait_drain(q_full, 0, p.timeout_ns);
+        if constexpr (SPLIT) cluster_skip();
         return;
     }
     if constexpr (SPLIT) {

@@ -41,6 +41,14 @@ __device__ __forceinline__ int split_step(int steps, int rank, int split) {
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// What a block does that has nothing to add or to leave: its shared memory has to
+// outlive the others' reads, should they find rows that see keys (spans written by
+// another stream meanwhile give wrong results, but must not fault).
+__device__ __forceinline__ void cluster_skip() {
+    __syncwarp();
+    cluster_meet();
+    cluster_meet();
+}
 // 16 bytes at this block's shared address `a`, of block `rank`.
 __device__ __forceinline__ float4 cluster_load(uint32_t a, int rank) {
     float4 v;
