@@ -77,8 +77,13 @@ __device__ __forceinline__ float2 score_addend(const ScoreCoef &cf, float rel) {
 
 // tanh of two capped scores, and 1 - tanh^2.  TANH mode takes the hardware
 // tanh (relative error 2^-11, so the capped score moves by at most 2^-11 of
-// itself); EXP mode forms (1 - e) / (1 + e) with e = exp(-2 |y|), accurate to
-// 2^-21 absolutely, and 4 e / (1 + e)^2, in which nothing cancels.
+// itself).  EXP mode forms (1 - e) / (1 + e) with e = exp(-2 |y|), and 4 e / (1 +
+// e)^2, in which nothing cancels.  Below |y| = 1/4 the former does, and a cap far above
+// the scores would bring its absolute error back as cap times that; there tanh(y) /
+// y is a polynomial in y^2 (minimax fit in relative error, fitted for this library as
+// the one above, maximum 4e-7).  Either side is within 2^-20 of tanh, relatively, so a
+// capped score is within 2^-20 of itself whatever the cap.
+constexpr float kTanh0 = 0.999999583f, kTanh1 = -0.333219081f, kTanh2 = 0.128416136f, kTanhMost = 0.25f;
 template <int MODE, bool GRAD>
 __device__ __forceinline__ float2 cap_tanh2(float2 y, float2 &f) {
     if constexpr (MODE == kSigmoidTanh) {
@@ -90,7 +95,9 @@ __device__ __forceinline__ float2 cap_tanh2(float2 y, float2 &f) {
         const float2 r = f2(rcp_approx(1.0f + e.x), rcp_approx(1.0f + e.y));
         const float2 t = mul2(fma2(e, f2(-1.0f, -1.0f), f2(1.0f, 1.0f)), r);
         if constexpr (GRAD) f = mul2(mul2(f2(4.0f, 4.0f), e), mul2(r, r));
-        return f2(copysignf(t.x, y.x), copysignf(t.y, y.y));
+        const float2 z = mul2(y, y);
+        const float2 n = mul2(y, fma2(z, fma2(z, f2(kTanh2, kTanh2), f2(kTanh1, kTanh1)), f2(kTanh0, kTanh0)));
+        return f2(fabsf(y.x) < kTanhMost ? n.x : copysignf(t.x, y.x), fabsf(y.y) < kTanhMost ? n.y : copysignf(t.y, y.y));
     }
 }
 
@@ -241,8 +248,9 @@ __device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &
         score_form<SCORE, GRAD, false, false>(r, cf, rel, pk, g, live);
     }
 }
-// P of two neighbouring columns to about 2^-20, for kernels whose scores are few:
-// one ex2 and one reciprocal, e^-|x| keeping both tails.
+// P of two neighbouring columns, for kernels whose scores are few: one ex2 and one
+// reciprocal, e^-|x| keeping both tails.  Relative error about 2^-20, and what the
+// argument's own error moves: 2^-23 of x without a cap, 2^-20 of the score with one.
 template <int SCORE>
 __device__ __forceinline__ float2 score_p2(float s0, float s1, const ScoreCoef &cf, float rel) {
     float2 f;

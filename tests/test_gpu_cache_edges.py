@@ -1,0 +1,65 @@
+"""GPU tests of the paged cache beyond the usual cases: places beyond 2^24, far caps, outputs over inputs, many heads and samples,
+shared pages, infinities, and a decoding loop inside a graph."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _compare as C
+from tests import _span_ref as R
+
+pytestmark = pytest.mark.gpu
+
+sa = pytest.importorskip("padding_aware_sigmoid_b200")
+
+
+@pytest.fixture
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sa.last_device_status()
+    yield torch.device("cuda", 0)
+    assert sa.last_device_status() == 0
+
+
+@pytest.fixture
+def exp_mode():
+    old = sa.get_sigmoid_mode()
+    sa.set_sigmoid_mode(sa.SIGMOID_EXP)
+    yield
+    sa.set_sigmoid_mode(old)
+
+
+def _i(a, dev):
+    return torch.as_tensor(np.asarray(a, np.int32), device=dev)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [1, 5, 30])
+@pytest.mark.parametrize("cap", [30.0, 1e6, 1e12])
+def test_far_caps(dev, exp_mode, D, rows, cap):
+    """As test_far_caps_in_exp_mode of the masked forward, in each row tile of the tile kernel and, with 30 rows a sample, in the
+    prefix kernel."""
+    Z, H, Hk, page, prefix = 3, 4, 2, 16, 100
+    own = np.asarray([rows, 90, 61])
+    nq = np.minimum(own, rows)
+    g = torch.Generator().manual_seed(D + rows)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(dev)      # noqa: E731
+    table = np.arange(18).reshape(3, 6)
+    pre = np.arange(18, 25)
+    kp, vp, q = r(25, page, Hk, D) * 2, r(25, page, Hk, D), r(Z, rows, H, D) * 2
+    alpha, bias = D ** -0.5, -3.0
+    o = sa.fwd_paged(q, kp, vp, _i(table, dev), _i(own, dev), _i(nq, dev), alpha, bias, cap=cap, prefix_table=_i(pre, dev),
+                     prefix_len=_i([prefix], dev)).cpu().double()
+    kc, vc, qc = (t.cpu().double() for t in (kp, vp, q))
+    for z in range(Z):
+        m, n = int(nq[z]), int(own[z])
+        k = torch.cat([kc[pre].flatten(0, 1)[:prefix], kc[table[z]].flatten(0, 1)[:n]]).repeat_interleave(H // Hk, 1).transpose(0, 1)
+        v = torch.cat([vc[pre].flatten(0, 1)[:prefix], vc[table[z]].flatten(0, 1)[:n]]).repeat_interleave(H // Hk, 1).transpose(0, 1)
+        i, j = prefix + n - m + torch.arange(m)[:, None], torch.arange(prefix + n)[None]
+        P = torch.sigmoid(cap * torch.tanh(alpha * (qc[z, :m].transpose(0, 1) @ k.mT) / cap) + bias) * (j <= i)
+        want = (P @ v).transpose(0, 1)
+        bound = R.HALF_BF16 * want.abs() + (R.HALF_BF16 + 1.1e-3) * (P @ v.abs()).transpose(0, 1)
+        off = (o[z, :m] - want).abs()
+        assert (off <= bound).all(), f"sample {z}: {float((off / bound).max()):.3g} of the bound"
