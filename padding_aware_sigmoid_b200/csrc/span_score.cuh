@@ -142,9 +142,10 @@ __device__ __forceinline__ ScorePause score_pause(const ScoreCoef &cf) {
 // cap's does not, bit 1: the tail's).  A lane whose row is not there (`live`) has no
 // say.
 //
-// TAIL: in the left tail, u = e^x <= 1/32, sigma = u - u^2 and sigma' = u - 2 u^2 (+
-// O(u^3)) from one ex2: as many MUFU and FMA operations as the tanh form, but a
-// relative error of at most u^2 <= 1e-3 where 0.5 + 0.5 tanh cancels (up to 1.4%).
+// TAIL: in the left tail, u = e^x <= 1/32, p = u - u^2 stands for sigma and p - p^2 for
+// sigma' from one ex2: as many MUFU and FMA operations as the tanh form, but a
+// relative error of -u^2 (either one; the next term is u^3), at most 1e-3, where 0.5 +
+// 0.5 tanh cancels (up to 1.4%).  (u - 2 u^2 for sigma' would have -3 u^2.)
 template <int SCORE, bool GRAD, bool POLY, bool TAIL>
 __device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk, float2 *g,
                                           bool live) {
@@ -171,7 +172,7 @@ __device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf
             const float2 u = f2(ex2_approx(y.x), ex2_approx(y.y)), n = f2(-u.x, -u.y);
             top = __vimax3_s32(top, __float_as_int(u.x), __float_as_int(u.y));
             p = fma2(n, u, u);
-            if constexpr (GRAD) g[i] = fma2(n, u, p);
+            if constexpr (GRAD) g[i] = fma2(f2(-p.x, -p.y), p, p);
         } else if constexpr (GRAD) {
             sigma_grad2<kSigmoidTanh>(y, p, g[i]);
         } else {

@@ -56,3 +56,33 @@ def test_far_caps_in_exp_mode(dev, exp_mode, D, cap):
     ref, bound = R.reference(q, k, v, do, R.visible(spans, n, L), alpha, [bias] * Z, cap, None)
     for name, x in zip(("O", "dQ", "dK", "dV"), got):
         R.assert_within(x, ref[name], bound[name], name)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 40.0])
+def test_the_tail_gradient_has_the_bias_it_states(dev, D, cap):
+    """Rows long enough for sigma's tail form, every score at x = -3.5, where u = e^x = 0.0302: sigma' is formed with a relative
+    error of -u^2 and no more.  What else moves an output averages out: roundings of dS and of the result, each within 2^-8 with
+    mean 0, over more than 10^5 of them leave less than 1e-4.  A cap adds the hardware tanh's error: 2^-11 of the capped score
+    of 5 (2.5e-3 of sigma), and twice that, of 1 - tanh^2 = 0.984, 1e-5."""
+    Z, L, H = 1, 2048, 2
+    g = torch.Generator().manual_seed(D)
+    x = -3.5
+    y = 5.0 if not cap else cap * math.atanh(5.0 / cap)          # the product that the cap takes to 5
+    f = 1.0 if not cap else 1.0 - (5.0 / cap) ** 2
+    alpha, bias = y / 5.0, -8.5
+    u = math.exp(x)
+    slope = u / (1 + u) ** 2 * f
+    pos = lambda: (0.5 + 0.5 * torch.rand(Z, L, H, D, generator=g)).to(torch.bfloat16).to(dev)      # noqa: E731
+    for side in ("dQ", "dK"):
+        a, b = pos(), pos()
+        one, other = torch.zeros_like(a), pos()                # their product is 2.5 * 2.0 whatever `other` holds
+        one[..., 0], other[..., 0] = 2.5, 2.0
+        q, k = (one, other) if side == "dQ" else (other, one)
+        grads = sa.bwd_span(q, k, a, b, _seq([L], dev), alpha, bias, cap=cap)
+        got = grads[0 if side == "dQ" else 1][..., 1:].double()
+        vt, dt, ot = (t.double().transpose(1, 2) for t in (a, b, other))
+        dp = dt @ vt.mT                                         # [Z, H, query, key]
+        want = alpha * slope * ((dp if side == "dQ" else dp.mT) @ ot)
+        off = (got.transpose(1, 2) / want[..., 1:] - 1.0).mean()
+        assert abs(float(off)) <= u * u + 1e-4 + (2.5e-3 if cap else 0.0), f"{side}: off by {float(off):.2e} on average"
