@@ -92,7 +92,8 @@ class SigmoidAttention(torch.nn.Module):
       call already holds it.
 
     ``cap`` > 0 caps the scores, cap tanh(alpha q . k / cap), and ``slopes`` (one
-    number per head) takes slopes[h] |i - j| off them; both are constants.  A call
+    number per head, float32 whatever the module is cast to) takes slopes[h] |i - j|
+    off them; both are constants.  A call
     with ``spans`` (``mask_spans``: causal, prefix, document and window masks), or
     with k and v of fewer heads, which groups of query heads share, runs the
     masked attention as well; it needs one length per sample for queries and
@@ -128,6 +129,17 @@ class SigmoidAttention(torch.nn.Module):
                                  "for b = -ln(max_len)")
             init = float(bias) if bias is not None else -math.log(max_len)
             self.b = torch.nn.Parameter(torch.tensor(init))
+
+    def _apply(self, fn, recurse=True):
+        """Moves of the module.  The slopes follow to the device but stay float32,
+        what the kernels take, with the values they were given: a model cast to bf16
+        would otherwise round them to 8 bits."""
+        slopes = self.slopes
+        super()._apply(fn, recurse)
+        if slopes is not None:
+            to = self.slopes.device
+            self.slopes = slopes.to(to) if not slopes.is_meta else torch.empty_like(slopes, device=to)
+        return self
 
     def forward(self, q, k, v, seqlens_q, seqlens_k=None, spans=None):
         if spans is not None or self.cap or self.slopes is not None or k.shape[2] != q.shape[2]:

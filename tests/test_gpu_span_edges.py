@@ -86,3 +86,20 @@ def test_the_tail_gradient_has_the_bias_it_states(dev, D, cap):
         want = alpha * slope * ((dp if side == "dQ" else dp.mT) @ ot)
         off = (got.transpose(1, 2) / want[..., 1:] - 1.0).mean()
         assert abs(float(off)) <= u * u + 1e-4 + (2.5e-3 if cap else 0.0), f"{side}: off by {float(off):.2e} on average"
+
+
+@pytest.mark.parametrize("cast", ["bfloat16", "half", "double", "to"])
+def test_a_cast_module_keeps_its_slopes(dev, cast):
+    """A module inside a model that is converted to another type runs with the slopes it was given, to the bit."""
+    Z, L, H, Hk, D = 2, 200, 6, 2, 64
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 61)
+    slopes = torch.linspace(0.4, 0.01, H)
+    model = torch.nn.ModuleDict({"attn": sa.SigmoidAttention(bias=-3.0, cap=25.0, slopes=slopes)})
+    model = model.to(dev, torch.bfloat16) if cast == "to" else getattr(model, cast)().to(dev)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    out = model["attn"](*leaves, _seq([200, 91], dev))
+    out.backward(do)
+    args = dict(cap=25.0, slopes=slopes.to(dev))
+    assert torch.equal(out, sa.fwd_span(q, k, v, _seq([200, 91], dev), D ** -0.5, -3.0, **args))
+    for leaf, want in zip(leaves, sa.bwd_span(q, k, v, do, _seq([200, 91], dev), D ** -0.5, -3.0, **args)):
+        assert torch.equal(leaf.grad, want)

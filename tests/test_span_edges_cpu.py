@@ -1,0 +1,26 @@
+"""The masked attention's and the cache's refusals and host state beyond the usual cases, without a GPU."""
+import pytest
+import torch
+
+from tests.test_span_cpu import sa  # noqa: F401  (the built package)
+
+
+@pytest.mark.parametrize("cast", [lambda m: m.bfloat16(), lambda m: m.half(), lambda m: m.double(), lambda m: m.to(torch.bfloat16),
+                                  lambda m: m.bfloat16().float(), lambda m: m.to("meta").to_empty(device="cpu")])
+def test_casts_leave_the_slopes_as_they_are(sa, cast):  # noqa: F811
+    slopes = [0.3, 1 / 3, 1e-5]
+    model = torch.nn.Sequential(torch.nn.Linear(2, 2), sa.SigmoidAttention(slopes=slopes))
+    cast(model)
+    got = model[1].slopes
+    assert got.dtype == torch.float32 and got.shape == (3,) and "slopes" in dict(model[1].named_buffers())
+    assert got.device.type == "cpu"
+
+
+def test_casts_round_no_slope(sa):  # noqa: F811
+    m = sa.SigmoidAttention(slopes=[0.3, 1 / 3, 1e-5])
+    want = m.slopes.clone()
+    for cast in (m.bfloat16, m.half, m.double, m.float):
+        assert cast() is m and torch.equal(m.slopes, want)
+    assert sa.SigmoidAttention(cap=3.0).bfloat16().slopes is None
+    p = sa.SigmoidAttention(learnable_bias=True, bias=-1.0).bfloat16()
+    assert p.b.dtype == torch.bfloat16
