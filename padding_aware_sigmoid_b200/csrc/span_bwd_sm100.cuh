@@ -520,7 +520,6 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
         tmem_dealloc(tmem, Lay::TMEM_COLS);
     }
     if constexpr (SPLIT) {
-        __syncwarp();
         cluster_meet();
         split_add(reinterpret_cast<const float4 *>(smem), D / 8, at.rank, split, threadIdx.x, SG::kThreads,
                   [&](int octet, int r, const float (&x)[8]) {
@@ -826,7 +825,6 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
         tmem_dealloc(tmem, Lay::TMEM_COLS);
     }
     if constexpr (SPLIT) {
-        __syncwarp();
         cluster_meet();
         split_add(reinterpret_cast<const float4 *>(smem), 2 * D / 8, at.rank, split, threadIdx.x, SG::kThreads,
                   [&](int octet, int r, const float (&x)[8]) {

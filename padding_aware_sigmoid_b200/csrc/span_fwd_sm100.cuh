@@ -439,7 +439,6 @@ __global__ void __launch_bounds__(SpanTiles<D>::kThreads, SpanTiles<D>::kPerSm)
         tmem_dealloc(tmem, Lay::TMEM_COLS);
     }
     if constexpr (SPLIT) {
-        __syncwarp();
         cluster_meet();
         split_add(reinterpret_cast<const float4 *>(smem), NT * D / 8, at.rank, split, threadIdx.x, kThreads,
                   [&](int octet, int r, const float (&x)[8]) {

@@ -37,15 +37,17 @@ __device__ __forceinline__ int split_step(int steps, int rank, int split) {
     return static_cast<int>(static_cast<int64_t>(steps) * rank / split);
 }
 
-// Barrier over all threads of the cluster's blocks, with their shared memory.
+// Barrier over all threads of the cluster's blocks, with their shared memory.  The
+// .aligned form wants whole warps, and rows that end inside a warp's may have split
+// the caller's.
 __device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // What a block does that has nothing to add or to leave: its shared memory has to
 // outlive the others' reads, should they find rows that see keys (spans written by
 // another stream meanwhile give wrong results, but must not fault).
 __device__ __forceinline__ void cluster_skip() {
-    __syncwarp();
     cluster_meet();
     cluster_meet();
 }

@@ -103,3 +103,23 @@ def test_a_cast_module_keeps_its_slopes(dev, cast):
     assert torch.equal(out, sa.fwd_span(q, k, v, _seq([200, 91], dev), D ** -0.5, -3.0, **args))
     for leaf, want in zip(leaves, sa.bwd_span(q, k, v, do, _seq([200, 91], dev), D ** -0.5, -3.0, **args)):
         assert torch.equal(leaf.grad, want)
+
+
+# lengths that end inside a warp's 32 rows and inside its octets of columns' work: the lanes of a block that shares a tile part there
+@pytest.mark.parametrize("L", [1026, 1039, 1057, 1151])
+@pytest.mark.parametrize("D", [64, 128])
+def test_ragged_tiles_that_blocks_share(dev, exp_mode, D, L):
+    """Z = 1, few heads: the blocks of a cluster add their sums (span_split.cuh), rows beyond L left out lane by lane."""
+    H, Hk = 2, 1
+    q, k, v, do = _tensors(1, L, H, Hk, D, torch.bfloat16, dev, L)
+    spans = R.make_spans("causal", [L], L).to(dev)
+    # the outputs end where a guard begins
+    guard = lambda t: torch.full((t.numel() + 512,), 7.0, dtype=t.dtype, device=dev)      # noqa: E731
+    bufs = [guard(t) for t in (q, q, k, v)]
+    o, dq, dk, dv = (b[:t.numel()].view_as(t) for b, t in zip(bufs, (q, q, k, v)))
+    sa.fwd_span(q, k, v, _seq([L], dev), D ** -0.5, -3.0, spans=spans, out=o)
+    sa.bwd_span(q, k, v, do, _seq([L], dev), D ** -0.5, -3.0, spans=spans, dq=dq, dk=dk, dv=dv)
+    ref, bound = R.reference(q, k, v, do, R.visible(spans, [L], L), D ** -0.5, [-3.0], 0.0, None)
+    for name, x, b in zip(("O", "dQ", "dK", "dV"), (o, dq, dk, dv), bufs):
+        R.assert_within(x, ref[name], bound[name], name)
+        assert (b[-512:] == 7.0).all()

@@ -1,8 +1,12 @@
 """The masked attention's and the cache's refusals and host state beyond the usual cases, without a GPU."""
+import os
+
 import pytest
 import torch
 
 from tests.test_span_cpu import sa  # noqa: F401  (the built package)
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "padding_aware_sigmoid_b200", "csrc")
 
 
 @pytest.mark.parametrize("cast", [lambda m: m.bfloat16(), lambda m: m.half(), lambda m: m.double(), lambda m: m.to(torch.bfloat16),
@@ -24,3 +28,13 @@ def test_casts_round_no_slope(sa):  # noqa: F811
     assert sa.SigmoidAttention(cap=3.0).bfloat16().slopes is None
     p = sa.SigmoidAttention(learnable_bias=True, bias=-1.0).bfloat16()
     assert p.b.dtype == torch.bfloat16
+
+
+def test_cluster_barriers_meet_whole_warps():
+    """barrier.cluster's .aligned form is undefined for a warp whose lanes have parted; rows beyond L part them (split_add).  The
+    barrier is written in one place, which brings the warp together first, so no caller can leave that out."""
+    src = {f: open(os.path.join(CSRC, f)).read() for f in os.listdir(CSRC)}
+    at = [f for f, text in src.items() if "barrier.cluster" in text]
+    assert at == ["span_split.cuh"] and src[at[0]].count("barrier.cluster.arrive") == 1
+    body = src[at[0]].split("void cluster_meet() {")[1].split("}")[0]
+    assert body.index("__syncwarp()") < body.index("barrier.cluster.arrive")
