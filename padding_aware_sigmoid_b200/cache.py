@@ -34,7 +34,8 @@ def cache_append(k, v, k_pages, v_pages, page_table, cache_lens, seqlens_new, in
     position of each pair of the first rot entries of a head (a multiple of 16);
     None for no rotation.  ``interleaved``: pairs (2 i, 2 i + 1) instead of (i, i +
     rot / 2).  ``q``: [Z, L, H, D] queries to rotate as well.  ``prefix_len``: int32
-    [1], tokens that stand before every sample's own."""
+    [1], tokens that stand before every sample's own.  ``lens_out`` may be
+    ``cache_lens`` itself for single tokens (L = 1) and overlaps no length otherwise."""
     return native().cache_append(k, v, k_pages, v_pages, page_table, cache_lens, seqlens_new, inv_freq, interleaved, q,
                                  prefix_len, q_out, lens_out)
 

@@ -139,6 +139,12 @@ struct Call {
 void *ws_ptr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 size_t ws_bytes(const at::Tensor &t) { return t.defined() ? t.nbytes() : 0; }
 
+// Whether two contiguous tensors of one device share a byte.
+bool overlap(const at::Tensor &a, const at::Tensor &b) {
+    const char *x = static_cast<const char *>(a.data_ptr()), *y = static_cast<const char *>(b.data_ptr());
+    return a.nbytes() > 0 && b.nbytes() > 0 && x < y + b.nbytes() && y < x + a.nbytes();
+}
+
 // bias: a number, or float32 [Z]; slopes: float32 [H] or None.
 struct Score {
     float alpha, bias = 0.0f, cap;
@@ -285,8 +291,10 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         at::Tensor out;
         if (q != nullptr) out = c.output(a[11], *q, "q_out");
         at::Tensor after = c.output(a[12], lens, "lens_out");
-        if (c.L > 1 && c.Z > 0 && after.data_ptr() == lens.data_ptr())
-            refuse("lens_out can be cache_lens itself only for single tokens");
+        // a sample's lengths are read by many warps, of which one writes the new one
+        const bool itself = c.L == 1 && after.data_ptr() == lens.data_ptr();
+        if ((overlap(after, lens) && !itself) || overlap(after, add) || (prefix != nullptr && overlap(after, *prefix)))
+            refuse("lens_out must not overlap the lengths (it can be cache_lens itself for single tokens)");
         run(c, "sigattn_cache_append", [&](void *stream) {
             return g_cache_append(ptr(&k), ptr(&v), ptr(q), q != nullptr ? ptr(&out) : nullptr, ptr(&kp), ptr(&vp),
                                   ints(&table), ints(&lens), ints(&add), ints(prefix), static_cast<int32_t *>(ptr(&after)),

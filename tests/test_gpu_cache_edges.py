@@ -63,3 +63,26 @@ def test_far_caps(dev, exp_mode, D, rows, cap):
         bound = R.HALF_BF16 * want.abs() + (R.HALF_BF16 + 1.1e-3) * (P @ v.abs()).transpose(0, 1)
         off = (o[z, :m] - want).abs()
         assert (off <= bound).all(), f"sample {z}: {float((off / bound).max()):.3g} of the bound"
+
+
+def test_append_refuses_lengths_over_lengths(dev):
+    """lens_out may be cache_lens itself for single tokens; any other overlap with the lengths would be read after it is written."""
+    Z, Hk, D, page = 4, 2, 64, 16
+    kp = torch.zeros(8, page, Hk, D, dtype=torch.bfloat16, device=dev)
+    vp, table = torch.zeros_like(kp), _i(np.arange(8).reshape(4, 2), dev)
+    buf = _i(np.arange(3 * Z), dev)
+    call = lambda L, have, add, out, **a: sa.cache_append(torch.zeros(Z, L, Hk, D, dtype=kp.dtype, device=dev),      # noqa: E731
+                                                          torch.zeros(Z, L, Hk, D, dtype=kp.dtype, device=dev), kp, vp, table,
+                                                          have, add, lens_out=out, **a)
+    a, b, c = buf[:Z], buf[Z:2 * Z].fill_(1), buf[2 * Z:]
+    for L, out in ((1, b), (2, a), (2, b), (1, buf[1:Z + 1]), (2, buf[Z - 1:2 * Z - 1])):
+        with pytest.raises(ValueError, match="lens_out"):
+            call(L, a, b, out)
+    with pytest.raises(ValueError, match="lens_out"):
+        call(1, a, b, c, prefix_len=c[1:2])
+    call(1, a, b, c)
+    assert c.tolist() == [1, 2, 3, 4]
+    call(1, a, b, a)
+    assert a.tolist() == [1, 2, 3, 4]
+    call(2, a, b, c)
+    assert c.tolist() == [2, 3, 4, 5]
