@@ -310,8 +310,8 @@ sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix,
  * behind the cache_lens[z] places that sample z has, and lens_out[z] =
  * cache_lens[z] + seqlens_new[z] (device int32[Z]; may be cache_lens itself when
  * L = 1, and must not overlap the lengths, prefix_len or other outputs otherwise).  Keys are rotated on the way, and so are the queries q
- * ([Z][L][H][D] -> q_out, which may be q; both NULL and H = 0 for none; rows of
- * padding are written as zeros): token l has position p = prefix_len[0] +
+ * ([Z][L][H][D] -> q_out, which may be q and overlaps no input otherwise; both
+ * NULL and H = 0 for none; rows of padding are written as zeros): token l has position p = prefix_len[0] +
  * cache_lens[z] + l, and pair i of the first rot entries of each head turns by
  * p inv_freq[i] (angles in 64 bits),
  *     (a, b) -> (a cos - b sin, b cos + a sin),

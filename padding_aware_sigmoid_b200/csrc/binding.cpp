@@ -145,6 +145,17 @@ bool overlap(const at::Tensor &a, const at::Tensor &b) {
     return a.nbytes() > 0 && b.nbytes() > 0 && x < y + b.nbytes() && y < x + a.nbytes();
 }
 
+// Outputs that the caller gave must not lie over the inputs, which other blocks still
+// read, or over one another.
+void apart(std::initializer_list<const at::Tensor *> outs, std::initializer_list<const at::Tensor *> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const at::Tensor *i : ins)
+            if (overlap(**o, *i)) refuse("outputs must not overlap inputs");
+        for (auto u = outs.begin(); u != o; ++u)
+            if (overlap(**o, **u)) refuse("outputs must not overlap one another");
+    }
+}
+
 // bias: a number, or float32 [Z]; slopes: float32 [H] or None.
 struct Score {
     float alpha, bias = 0.0f, cap;
@@ -212,6 +223,7 @@ PyObject *fwd_span(PyObject *, PyObject *const *a, Py_ssize_t n) {
         c.vector(spans, at::kInt, {c.Z, c.L, 2}, "spans");
         const Score s(c, a[4], a[5], a[7], a[8]);
         at::Tensor out = c.output(a[9], c.q, "out");
+        if (a[9] != Py_None) apart({&out}, {&c.q, &k, &v});
         run(c, "sigattn_fwd_span", [&](void *stream) {
             return g_fwd_span(ptr(&c.q), ptr(&k), ptr(&v), ptr(&out), ints(&seqlens), ints(spans), c.Z, c.L, c.H, c.Hk,
                               c.D, s.alpha, s.bias, s.bias_z, s.cap, s.slopes, dtype_of(c.q), stream);
@@ -233,6 +245,7 @@ PyObject *bwd_span(PyObject *, PyObject *const *a, Py_ssize_t n) {
         c.vector(spans, at::kInt, {c.Z, c.L, 2}, "spans");
         const Score s(c, a[5], a[6], a[8], a[9]);
         at::Tensor dq = c.output(a[10], c.q, "dq"), dk = c.output(a[11], k, "dk"), dv = c.output(a[12], v, "dv");
+        if (a[10] != Py_None || a[11] != Py_None || a[12] != Py_None) apart({&dq, &dk, &dv}, {&c.q, &k, &v, &dout});
         const sigattn_dtype dt = dtype_of(c.q);
         const at::Tensor ws = c.workspace(a[13], g_bwd_span_bytes(c.Z, c.L, dt));
         run(c, "sigattn_bwd_span", [&](void *stream) {
@@ -289,7 +302,11 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int interleaved = PyObject_IsTrue(a[8]);
         if (interleaved < 0) throw Refusal{nullptr, ""};
         at::Tensor out;
-        if (q != nullptr) out = c.output(a[11], *q, "q_out");
+        if (q != nullptr) {
+            out = c.output(a[11], *q, "q_out");
+            if (overlap(out, k) || overlap(out, v) || (overlap(out, *q) && out.data_ptr() != q->data_ptr()))
+                refuse("q_out must be q itself or overlap no input");
+        }
         at::Tensor after = c.output(a[12], lens, "lens_out");
         // a sample's lengths are read by many warps, of which one writes the new one
         const bool itself = c.L == 1 && after.data_ptr() == lens.data_ptr();

@@ -33,7 +33,8 @@ def fwd_span(q, k, v, seqlens, alpha: float, bias, spans=None, cap: float = 0.0,
     a multiple of Hk.  ``seqlens``: int32 [Z] true lengths.  ``bias``: a number, or
     float32 [Z] with one bias per sample.  ``spans``: int32 [Z, L, 2], the keys
     [lo, hi) that each row sees (``mask_spans``; None: all).  ``cap``: 0 for none.
-    ``slopes``: float32 [H], how fast a head's scores fall with |i - j|."""
+    ``slopes``: float32 [H], how fast a head's scores fall with |i - j|.  ``out``
+    must not overlap the inputs."""
     return native().fwd_span(q, k, v, seqlens, alpha, bias, spans, cap, slopes, out)
 
 
@@ -47,7 +48,8 @@ def bwd_span(q, k, v, dout, seqlens, alpha: float, bias, spans=None, cap: float 
              dq=None, dk=None, dv=None, workspace=None):
     """(dQ, dK, dV) of ``fwd_span`` given dout = dLoss/dO; P is recomputed, O is
     not needed.  ``workspace``: a device uint8 tensor of at least
-    ``bwd_span_workspace_bytes`` bytes (allocated here when omitted)."""
+    ``bwd_span_workspace_bytes`` bytes (allocated here when omitted).  The outputs
+    must not overlap the inputs or one another."""
     return native().bwd_span(q, k, v, dout, seqlens, alpha, bias, spans, cap, slopes, dq, dk, dv, workspace)
 
 

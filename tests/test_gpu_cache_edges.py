@@ -86,3 +86,15 @@ def test_append_refuses_lengths_over_lengths(dev):
     assert a.tolist() == [1, 2, 3, 4]
     call(2, a, b, c)
     assert c.tolist() == [2, 3, 4, 5]
+
+
+def test_append_refuses_queries_half_over_themselves(dev):
+    Z, L, H, D = 1, 4, 2, 64
+    buf = torch.zeros(2 * Z * L * H * D, dtype=torch.bfloat16, device=dev)
+    q, half = buf[:L * H * D].view(Z, L, H, D), buf[64:64 + L * H * D].view(Z, L, H, D)
+    kp = torch.zeros(1, 16, H, D, dtype=torch.bfloat16, device=dev)
+    k = torch.zeros_like(q)
+    call = lambda **a: sa.cache_append(k, k, kp, kp.clone(), _i([[0]], dev), _i([0], dev), _i([L], dev), q=q, **a)      # noqa: E731
+    with pytest.raises(ValueError, match="q_out"):
+        call(q_out=half)
+    call(q_out=q)

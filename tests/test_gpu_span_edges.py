@@ -123,3 +123,20 @@ def test_ragged_tiles_that_blocks_share(dev, exp_mode, D, L):
     for name, x, b in zip(("O", "dQ", "dK", "dV"), (o, dq, dk, dv), bufs):
         R.assert_within(x, ref[name], bound[name], name)
         assert (b[-512:] == 7.0).all()
+
+
+def test_outputs_over_inputs_are_refused(dev):
+    Z, L, H, Hk, D = 2, 40, 4, 2, 64
+    q, k, v, do = _tensors(Z, L, H, Hk, D, torch.bfloat16, dev, 63)
+    seq = _seq([40, 7], dev)
+    both = torch.empty(2, Z, L, H, D, dtype=q.dtype, device=dev)
+    shifted = both.flatten()[64:64 + q.numel()].view_as(q)
+    with pytest.raises(ValueError, match="overlap"):
+        sa.fwd_span(q, k, v, seq, 0.1, 0.0, out=q)
+    with pytest.raises(ValueError, match="overlap"):
+        sa.fwd_span(both[0], k, v, seq, 0.1, 0.0, out=shifted)
+    for outs in (dict(dq=q), dict(dq=do), dict(dk=k), dict(dk=v), dict(dv=v), dict(dk=(t := torch.empty_like(k)), dv=t)):
+        with pytest.raises(ValueError, match="overlap"):
+            sa.bwd_span(q, k, v, do, seq, 0.1, 0.0, **outs)
+    sa.fwd_span(both[0].zero_(), k, v, seq, 0.1, 0.0, out=both[1])       # side by side is fine
+    sa.bwd_span(q, k, k, q, seq, 0.1, 0.0)                               # so is an input given twice
