@@ -175,17 +175,19 @@ struct Score {
     }
 };
 
-// Runs f(stream) with the tensors' device current and without the interpreter's
-// lock; raises what the library answers.
-template <typename F>
-void run(const Call &c, const char *name, F &&f) {
+// Calls entry point f of the library, the stream its last argument, with the
+// tensors' device current and without the interpreter's lock; raises what it answers.
+// The arguments are values by now: a refusal or an error of PyTorch's while they are
+// formed must find the lock held.
+template <typename F, typename... Args>
+void run(const Call &c, const char *name, F *f, Args... args) {
     sigattn_status s;
     {
         std::optional<c10::cuda::CUDAGuard> guard;
         if (c10::cuda::current_device() != c.device) guard.emplace(static_cast<c10::DeviceIndex>(c.device));
         void *stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(c.device)).stream();
         Py_BEGIN_ALLOW_THREADS;
-        s = f(stream);
+        s = f(args..., stream);
         Py_END_ALLOW_THREADS;
     }
     if (s != SIGATTN_OK) {
@@ -224,10 +226,8 @@ PyObject *fwd_span(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Score s(c, a[4], a[5], a[7], a[8]);
         at::Tensor out = c.output(a[9], c.q, "out");
         if (a[9] != Py_None) apart({&out}, {&c.q, &k, &v});
-        run(c, "sigattn_fwd_span", [&](void *stream) {
-            return g_fwd_span(ptr(&c.q), ptr(&k), ptr(&v), ptr(&out), ints(&seqlens), ints(spans), c.Z, c.L, c.H, c.Hk,
-                              c.D, s.alpha, s.bias, s.bias_z, s.cap, s.slopes, dtype_of(c.q), stream);
-        });
+        run(c, "sigattn_fwd_span", g_fwd_span, ptr(&c.q), ptr(&k), ptr(&v), ptr(&out), ints(&seqlens), ints(spans),
+            c.Z, c.L, c.H, c.Hk, c.D, s.alpha, s.bias, s.bias_z, s.cap, s.slopes, dtype_of(c.q));
         return THPVariable_Wrap(std::move(out));
     });
 }
@@ -248,18 +248,16 @@ PyObject *bwd_span(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (a[10] != Py_None || a[11] != Py_None || a[12] != Py_None) apart({&dq, &dk, &dv}, {&c.q, &k, &v, &dout});
         const sigattn_dtype dt = dtype_of(c.q);
         const at::Tensor ws = c.workspace(a[13], g_bwd_span_bytes(c.Z, c.L, dt));
-        run(c, "sigattn_bwd_span", [&](void *stream) {
-            return g_bwd_span(ptr(&c.q), ptr(&k), ptr(&v), ptr(&dout), ptr(&dq), ptr(&dk), ptr(&dv), ints(&seqlens),
-                              ints(spans), c.Z, c.L, c.H, c.Hk, c.D, s.alpha, s.bias, s.bias_z, s.cap, s.slopes,
-                              ws_ptr(ws), ws_bytes(ws), dt, stream);
-        });
+        run(c, "sigattn_bwd_span", g_bwd_span, ptr(&c.q), ptr(&k), ptr(&v), ptr(&dout), ptr(&dq), ptr(&dk), ptr(&dv),
+            ints(&seqlens), ints(spans), c.Z, c.L, c.H, c.Hk, c.D, s.alpha, s.bias, s.bias_z, s.cap, s.slopes,
+            ws_ptr(ws), ws_bytes(ws), dt);
         return Py_BuildValue("(NNN)", THPVariable_Wrap(std::move(dq)), THPVariable_Wrap(std::move(dk)),
                              THPVariable_Wrap(std::move(dv)));
     });
 }
 
-// Cache pages [pages, page_size, Hk, D] beside a call's tensors.
-void check_pages(const Call &c, const at::Tensor &k, const at::Tensor &v) {
+// Cache pages [pages, page_size, Hk, D] beside a call's tensors; how many there are.
+int check_pages(const Call &c, const at::Tensor &k, const at::Tensor &v) {
     if (k.dim() != 4 || k.size(3) != c.D || v.sizes() != k.sizes())
         refuse("k_pages and v_pages must be [pages, page_size, Hk, D]");
     for (const at::Tensor *t : {&k, &v})
@@ -268,6 +266,7 @@ void check_pages(const Call &c, const at::Tensor &k, const at::Tensor &v) {
     const int64_t page = k.size(1);
     if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)
         refuse("page_size must be 16, 32, 64, 128 or 256, got " + std::to_string(page));
+    return narrow(k.size(0));
 }
 int check_table(const Call &c, const at::Tensor &t) {
     if (t.dim() != 2) refuse("page_table must be a contiguous int32 [Z, max_pages] tensor");
@@ -284,7 +283,7 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         c.keys({&k, &v});
         const at::Tensor &kp = tensor(a[2], "k_pages"), &vp = tensor(a[3], "v_pages"), &table = tensor(a[4], "page_table");
         const at::Tensor &lens = tensor(a[5], "cache_lens"), &add = tensor(a[6], "seqlens_new");
-        check_pages(c, kp, vp);
+        const int pages = check_pages(c, kp, vp);
         if (kp.size(2) != c.Hk) refuse("k_pages and v_pages must be [pages, page_size, Hk, D]");
         const int most = check_table(c, table);
         c.vector(&lens, at::kInt, {c.Z}, "cache_lens");
@@ -312,12 +311,10 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const bool itself = c.L == 1 && after.data_ptr() == lens.data_ptr();
         if ((overlap(after, lens) && !itself) || overlap(after, add) || (prefix != nullptr && overlap(after, *prefix)))
             refuse("lens_out must not overlap the lengths (it can be cache_lens itself for single tokens)");
-        run(c, "sigattn_cache_append", [&](void *stream) {
-            return g_cache_append(ptr(&k), ptr(&v), ptr(q), q != nullptr ? ptr(&out) : nullptr, ptr(&kp), ptr(&vp),
-                                  ints(&table), ints(&lens), ints(&add), ints(prefix), static_cast<int32_t *>(ptr(&after)),
-                                  c.Z, c.L, q != nullptr ? c.H : 0, c.Hk, c.D, narrow(kp.size(0)),
-                                  static_cast<int>(kp.size(1)), most, floats(freq), rot, interleaved, dtype_of(k), stream);
-        });
+        run(c, "sigattn_cache_append", g_cache_append, ptr(&k), ptr(&v), ptr(q), q != nullptr ? ptr(&out) : nullptr,
+            ptr(&kp), ptr(&vp), ints(&table), ints(&lens), ints(&add), ints(prefix),
+            static_cast<int32_t *>(ptr(&after)), c.Z, c.L, q != nullptr ? c.H : 0, c.Hk, c.D, pages,
+            static_cast<int>(kp.size(1)), most, floats(freq), rot, interleaved, dtype_of(k));
         PyObject *first = q != nullptr ? THPVariable_Wrap(std::move(out)) : (Py_INCREF(Py_None), Py_None);
         return Py_BuildValue("(NN)", first, THPVariable_Wrap(std::move(after)));
     });
@@ -329,7 +326,7 @@ PyObject *fwd_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Call c(tensor(a[0], "q"));
         const at::Tensor &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages"), &table = tensor(a[3], "page_table");
         const at::Tensor &nk = tensor(a[4], "seqlens_k"), &nq = tensor(a[5], "seqlens_q");
-        check_pages(c, kp, vp);
+        const int pages = check_pages(c, kp, vp);
         c.share(kp.size(2));
         const int most = check_table(c, table);
         c.vector(&nk, at::kInt, {c.Z}, "seqlens_k");
@@ -346,11 +343,9 @@ PyObject *fwd_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         at::Tensor out = c.output(a[12], c.q, "out");
         const sigattn_dtype dt = dtype_of(c.q);
         const at::Tensor ws = c.workspace(a[13], g_fwd_paged_bytes(c.Z, c.L, c.H, c.Hk, c.D, dt));
-        run(c, "sigattn_fwd_paged", [&](void *stream) {
-            return g_fwd_paged(ptr(&c.q), ptr(&kp), ptr(&vp), ptr(&out), ints(&table), ints(&nk), ints(&nq), ints(pre),
-                               ints(len), c.Z, c.L, c.H, c.Hk, c.D, narrow(kp.size(0)), static_cast<int>(kp.size(1)), most,
-                               ahead, s.alpha, s.bias, s.bias_z, s.cap, s.slopes, ws_ptr(ws), ws_bytes(ws), dt, stream);
-        });
+        run(c, "sigattn_fwd_paged", g_fwd_paged, ptr(&c.q), ptr(&kp), ptr(&vp), ptr(&out), ints(&table), ints(&nk),
+            ints(&nq), ints(pre), ints(len), c.Z, c.L, c.H, c.Hk, c.D, pages, static_cast<int>(kp.size(1)), most,
+            ahead, s.alpha, s.bias, s.bias_z, s.cap, s.slopes, ws_ptr(ws), ws_bytes(ws), dt);
         return THPVariable_Wrap(std::move(out));
     });
 }

@@ -98,3 +98,14 @@ def test_append_refuses_queries_half_over_themselves(dev):
     with pytest.raises(ValueError, match="q_out"):
         call(q_out=half)
     call(q_out=q)
+
+
+def test_too_many_empty_pages_are_refused_with_an_exception(dev):
+    """A size that does not fit the library's int raises, from whatever place it is found in: 2^31 pages of no heads hold no byte."""
+    pages = torch.empty(2 ** 31, 16, 0, 64, dtype=torch.bfloat16, device=dev)
+    q = torch.empty(1, 1, 0, 64, dtype=torch.bfloat16, device=dev)
+    one = _i([1], dev)
+    with pytest.raises(ValueError, match="2\\^31"):
+        sa.fwd_paged(q, pages, pages, _i([[0]], dev), one, one, 1.0, 0.0)
+    with pytest.raises(ValueError, match="2\\^31"):
+        sa.cache_append(q, q, pages, pages, _i([[0]], dev), one, one)
