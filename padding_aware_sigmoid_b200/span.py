@@ -70,7 +70,8 @@ def mask_spans(seqlens, L: int, causal: bool = False, prefix=None, docs=None, wi
     device = seqlens.get_device()
     if device < 0 or seqlens.dim() != 1:
         raise ValueError("seqlens must be a contiguous int32 [Z] CUDA tensor")
-    Z, L, window = seqlens.shape[0], int(L), int(window)
+    Z, L = seqlens.shape[0], int(L)
+    window = max(-1, min(int(window), L))     # wider windows hide nothing; the library takes an int
     _check_ints(seqlens, (Z,), device, "seqlens")
     if prefix is not None:
         _check_ints(prefix, (Z,), device, "prefix")

@@ -140,3 +140,15 @@ def test_outputs_over_inputs_are_refused(dev):
             sa.bwd_span(q, k, v, do, seq, 0.1, 0.0, **outs)
     sa.fwd_span(both[0].zero_(), k, v, seq, 0.1, 0.0, out=both[1])       # side by side is fine
     sa.bwd_span(q, k, k, q, seq, 0.1, 0.0)                               # so is an input given twice
+
+
+def test_windows_beyond_32_bits_hide_nothing(dev):
+    seq = _seq([40, 7], dev)
+    docs = (torch.arange(50, device=dev, dtype=torch.int32) // 9).expand(2, 50).contiguous()
+    for causal in (False, True):
+        want = sa.mask_spans(seq, 50, causal=causal, docs=docs)
+        for window in (50, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 40 + 1):
+            assert torch.equal(sa.mask_spans(seq, 50, causal=causal, docs=docs, window=window), want)
+    for window in (-1, -2 ** 31, -2 ** 32 + 3):
+        with pytest.raises(sa.SigattnError):
+            sa.mask_spans(seq, 50, window=window)
