@@ -202,7 +202,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // warp's 16): where they come from and what they see.
 struct PagedRows {
     const __nv_bfloat16 *q[2];   // null: no such row
-    float pos[2];                // place of the query among the item's keys
+    int pos[2];                  // place of the query among the item's keys (distances are taken in
+                                 // whole numbers: fp32 does not hold places beyond 2^24)
     int limit[2];                // keys below it are seen
 };
 
@@ -226,7 +227,7 @@ struct PagedItem {
             const int h = c.kvh * p.group + static_cast<int>(r % p.group);
             const bool in = c.z < 0 ? tok < static_cast<int64_t>(p.Z) * p.L : r < static_cast<int64_t>(p.L) * p.group;
             rows.q[i] = nullptr;
-            rows.pos[i] = 0.0f;
+            rows.pos[i] = 0;
             rows.limit[i] = 0;
             cf[i] = ScoreCoef{};
             if (!in) continue;
@@ -235,7 +236,7 @@ struct PagedItem {
             if (l >= n.y) continue;
             const int at = n.x - n.y + l;     // own place
             rows.q[i] = p.q + (static_cast<size_t>(tok) * p.H + h) * D;
-            rows.pos[i] = static_cast<float>(c.z < 0 ? prefix + at : at);
+            rows.pos[i] = c.z < 0 ? prefix + at : at;
             rows.limit[i] = c.z < 0 ? prefix : at + 1;
             cf[i] = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                             SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
@@ -284,7 +285,7 @@ struct PagedItem {
                 for (int i = 0; i < 2; ++i) {
                     const int key = key0 + k16 + 8 * n8 + 2 * (lane & 3);
                     float2 w = score_p2<SCORE>(s[n8][2 * i], s[n8][2 * i + 1], cf[i],
-                                                     rows.pos[i] - static_cast<float>(key));
+                                                     static_cast<float>(rows.pos[i] - key));
                     w.x = key < rows.limit[i] ? w.x : 0.0f;
                     w.y = key + 1 < rows.limit[i] ? w.y : 0.0f;
                     const uint32_t hi = pack_bf16x2(w.x, w.y);
@@ -710,12 +711,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int h = kvh * p.group + row % p.group;
             ScoreCoef cf = {0.0f, -64.0f};    // of rows that are not there: sigma of almost nothing
             bool live = row < p.tile_tokens * p.group && tok < tokens;
-            float pos = 0.0f;
+            int pos = 0;
             if (live) {
                 const int z = static_cast<int>(tok / p.L), l = static_cast<int>(tok % p.L);
                 const int2 n = paged_lengths(p, z);
                 live = l < n.y;
-                pos = static_cast<float>(prefix + n.x - n.y + l);
+                pos = prefix + n.x - n.y + l;
                 cf = make_score<SCORE>(p.alpha, bias_of(p.bias_z, p.bias, z), p.cap,
                                        SCORE & kScoreSlope ? p.slopes[h] : 0.0f);
             }
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int u = 0; u < 2; ++u) {
                     uint32_t x[32], pk[16];
                     tmem_ld32(tS + 32 * u, x);
-                    score_chunk<MODE, SCORE, false, true>(x, cf, pos - static_cast<float>(key0 + 32 * u), pk, nullptr, pause,
+                    score_chunk<MODE, SCORE, false, true>(x, cf, static_cast<float>(pos - key0 - 32 * u), pk, nullptr, pause,
                                                           prefix - key0 >= 64, live);
                     if (prefix - key0 < 64) keep_bits(pk, bit_range(0, prefix - key0 - 32 * u));
                     tmem_st16(tS + 16 * u, pk);

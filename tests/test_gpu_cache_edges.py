@@ -109,3 +109,34 @@ def test_too_many_empty_pages_are_refused_with_an_exception(dev):
         sa.fwd_paged(q, pages, pages, _i([[0]], dev), one, one, 1.0, 0.0)
     with pytest.raises(ValueError, match="2\\^31"):
         sa.cache_append(q, q, pages, pages, _i([[0]], dev), one, one)
+
+
+@pytest.mark.parametrize("where", ["own", "own, odd", "prefix, few rows", "prefix, many rows"])
+def test_distances_beyond_two_to_the_24(dev, exp_mode, where):
+    """Places that fp32 does not hold: distances to the nearest keys are exact all the same.  All pages of the long part are one page
+    with zero keys, so that a key's weight is sigma(-distance); its values mark the place within the page, entry e every place that
+    is e modulo 64.  Weights fall by e a place: those nearer than 64 decide each sum, and the rest is below e^-64 of them.
+    Bounds: P within 1e-3 and 2^-8 of itself, and the result's rounding 2^-8 (tests/_span_ref.py)."""
+    D, page, far = 64, 256, 2 ** 24 + (6 if where == "own, odd" else 5)
+    H, L = (16, 8) if where == "prefix, many rows" else (1, 1)
+    pages = -(-far // page)
+    kp = torch.zeros(2, page, 1, D, dtype=torch.bfloat16, device=dev)
+    vp = torch.zeros_like(kp)
+    vp[0, torch.arange(page), 0, torch.arange(page) % D] = 1.0
+    q = torch.zeros(1, L, H, D, dtype=torch.bfloat16, device=dev)
+    slopes = torch.ones(H, device=dev)
+    if where.startswith("own"):
+        o = sa.fwd_paged(q, kp, vp, torch.zeros(1, pages, dtype=torch.int32, device=dev), _i([far], dev), _i([1], dev), 1.0, 0.0,
+                         slopes=slopes)
+    else:           # own tokens of zero values behind the prefix
+        o = sa.fwd_paged(q, kp, vp, _i([[1]], dev), _i([L], dev), _i([L], dev), 1.0, 0.0, slopes=slopes,
+                         prefix_table=torch.zeros(pages, dtype=torch.int32, device=dev), prefix_len=_i([far], dev))
+    e = torch.arange(D)
+    for l in range(L):
+        last = far - 1                                           # the nearest key that is marked
+        first = 0 if where.startswith("own") else l + 1                   # and its distance
+        near = (last - e) % D                                    # of the nearest place that is e modulo 64, behind `last`
+        want = torch.sigmoid(-(first + near).double())
+        want = want + torch.sigmoid(-(first + near + 64).double())
+        off = (o[0, l].double().cpu() - want).abs()
+        assert (off <= (2.0 ** -7 + 1.1e-3) * want).all(), f"row {l}: {float((off / want).max()):.3g}"
