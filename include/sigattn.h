@@ -339,7 +339,9 @@ sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix,
  * Errors of both: SIGATTN_ERR_INVALID_ARG (sigattn_cache_append: also L = 0;
  * sigattn_fwd_paged: also pages = 0), _UNSUPPORTED_HEADDIM,
  * _UNSUPPORTED_DTYPE, _UNSUPPORTED_DEVICE, _MISALIGNED, _TOO_LARGE (2^31 places,
- * tokens, rows or, over all samples of sigattn_fwd_paged, 64-place tiles), _CUDA.  On error nothing is launched. */
+ * tokens, rows or, over all samples of sigattn_fwd_paged, 64-place tiles; 65536
+ * heads; sigattn_fwd_paged: tokens that make 65536 pairs of row tiles, of 128 / (H /
+ * Hk) tokens each), _CUDA.  On error nothing is launched. */
 #define SIGATTN_PAGED_MAX_Z 4096
 sigattn_status sigattn_cache_append(const void *k, const void *v, const void *q, void *q_out,
                                     void *k_pages, void *v_pages, const int32_t *page_table,

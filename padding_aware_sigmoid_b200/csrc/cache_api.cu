@@ -36,7 +36,8 @@ sigattn_status check_cache(const CacheShape &c, bool queries, bool *empty) {
     // places are int32, and the work of a call is counted in 32 bits
     const int64_t most = int64_t(INT_MAX) - 4096;
     const int64_t own = static_cast<int64_t>(c.max_pages) << shift, ahead = static_cast<int64_t>(c.prefix_pages) << shift;
-    if (own + ahead > most || static_cast<int64_t>(c.Z) * c.L > most || c.H > 65535) return SIGATTN_ERR_TOO_LARGE;
+    if (own + ahead > most || static_cast<int64_t>(c.Z) * c.L > most || c.H > 65535 || c.Hk > 65535)
+        return SIGATTN_ERR_TOO_LARGE;
     return SIGATTN_OK;
 }
 

@@ -1,4 +1,5 @@
 """The masked attention's and the cache's refusals and host state beyond the usual cases, without a GPU."""
+import ctypes
 import os
 
 import pytest
@@ -38,3 +39,11 @@ def test_cluster_barriers_meet_whole_warps():
     assert at == ["span_split.cuh"] and src[at[0]].count("barrier.cluster.arrive") == 1
     body = src[at[0]].split("void cluster_meet() {")[1].split("}")[0]
     assert body.index("__syncwarp()") < body.index("barrier.cluster.arrive")
+
+
+def test_append_refuses_heads_that_do_not_count_in_32_bits(sa):  # noqa: F811
+    """H + 2 Hk heads of a token are counted in 32 bits: beyond that the call wrote nothing and answered OK."""
+    lib, P = sa.load_library(), ctypes.c_void_p(16)
+    call = lambda H, Hk: lib.sigattn_cache_append(P, P, P if H else None, P if H else None, P, P, P, P, P, None, P, 1, 1, H, Hk, 64, 1,      # noqa: E731
+                                                  16, 1, None, 0, 0, 0, None)
+    assert call(0, 2 ** 30) == 9 and call(0, 65536) == 9 and call(2 ** 31 - 2, 2 ** 30 - 1) == 9
