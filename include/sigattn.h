@@ -252,8 +252,12 @@ size_t sigattn_dbias_workspace_bytes(int Z, int L, int H, sigattn_dtype dtype);
  *
  * Rows at or beyond n may hold anything, NaN included: they are never read into
  * a result.  Within a sample a masked key or query must still be finite (it is
- * multiplied by a weight of zero); what it holds does not change a bit of the
- * rows that do not see it.
+ * multiplied by a weight of zero).  What a key or query holds does not change a
+ * bit of the rows that do not see it in SIGATTN_SIGMOID_EXP mode and in fp32.  In
+ * SIGATTN_SIGMOID_TANH mode one form of the score function is chosen for 32
+ * neighbouring rows and the keys that all of them see (queries and keys changed
+ * round in dK, dV), so the last bits of a row may depend on the queries (keys) of the
+ * 31 beside it; keys outside its span, other documents and padding still have no say.
  *
  * The same call gives the same bits every time.  Between calls of other shapes the
  * order of the fp32 sums may differ: a batch with few tiles splits each tile's keys

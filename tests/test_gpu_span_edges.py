@@ -152,3 +152,29 @@ def test_windows_beyond_32_bits_hide_nothing(dev):
     for window in (-1, -2 ** 31, -2 ** 32 + 3):
         with pytest.raises(sa.SigattnError):
             sa.mask_spans(seq, 50, window=window)
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, -9.5), (20.0, -9.5), (20.0, -2.0)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_later_queries_of_the_same_warp(dev, D, cap, bias):
+    """Causal rows, the queries of rows 480 ... 511 behind row 490 made large.  What rows up to 490 yield does not depend on them to
+    the bit in EXP mode; in TANH mode, which chooses a chunk's form for 32 rows at once, it stays within the bar of that mode."""
+    Z, L, H = 1, 600, 2
+    q, k, v, do = _tensors(Z, L, H, H, D, torch.bfloat16, dev, 15)
+    seq = _seq([L], dev)
+    spans = sa.mask_spans(seq, L, causal=True)
+    large = q.clone()
+    large[:, 491:512] *= 60.0
+    call = lambda x: (sa.fwd_span(x, k, v, seq, D ** -0.5, bias, spans=spans, cap=cap),      # noqa: E731
+                      sa.bwd_span(x, k, v, do, seq, D ** -0.5, bias, spans=spans, cap=cap)[0])
+    ref, _ = R.reference(q, k, v, do, R.visible(spans, [L], L), D ** -0.5, [bias], cap, None)
+    for got, name in zip(call(large), ("O", "dQ")):
+        C.assert_close(got[:, :491].float().cpu().numpy(), ref[name][:, :491].numpy(), "bf16", name)
+    old = sa.get_sigmoid_mode()
+    try:
+        sa.set_sigmoid_mode(sa.SIGMOID_EXP)
+        for a, b in zip(call(q), call(large)):
+            assert torch.equal(a[:, :491], b[:, :491])
+            assert torch.equal(a[:, 512:], b[:, 512:])
+    finally:
+        sa.set_sigmoid_mode(old)
