@@ -331,8 +331,10 @@ sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix,
  * are sample z's last tokens, and seqlens_k[z] >= seqlens_q[z] its own tokens in
  * the cache, theirs included.  Query l, at own place i = seqlens_k - seqlens_q + l,
  * sees its own places up to i and, with a prefix, all prefix_len[0] places of
- * the pages prefix_table (device int32[prefix_pages]), which are read once for
- * the whole batch.  Scores as in sigattn_fwd_span, |i - j| being the distance
+ * the pages prefix_table (device int32[prefix_pages]).  In bf16 these are read once
+ * per key head for up to 256 rows (tokens times query heads) of the batch together, and
+ * not once a sample; the fp32 path, made for accuracy, reads all keys for each row.
+ * Scores as in sigattn_fwd_span, |i - j| being the distance
  * between positions (the prefix comes first).  Padded query rows are written as
  * exact zeros; cache places that no query sees may hold anything, NaN included.
  * workspace (device, 16-byte aligned, sigattn_fwd_paged_workspace_bytes bytes,

@@ -53,8 +53,8 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens_k, seqlens_q, alpha: floa
     Sample z has seqlens_k[z] own tokens in the pages page_table[z]; its
     seqlens_q[z] <= L queries are the last of them, each seeing its own tokens up
     to itself.  ``prefix_table`` (int32 [prefix_pages]) and ``prefix_len`` (int32
-    [1]): the pages and length of a prefix that every query sees, read once for
-    the batch.  ``bias``, ``cap`` and ``slopes`` as in ``fwd_span``, distances
+    [1]): the pages and length of a prefix that every query sees, read for up to 256
+    rows of the batch at a time (bf16).  ``bias``, ``cap`` and ``slopes`` as in ``fwd_span``, distances
     counted in positions with the prefix first.  ``workspace``: a device uint8
     tensor of at least ``fwd_paged_workspace_bytes`` bytes (allocated here when
     omitted)."""
