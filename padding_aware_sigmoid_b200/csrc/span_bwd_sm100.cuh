@@ -214,7 +214,7 @@ __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_
         some = false;
 #pragma unroll
         for (int u = 0; u < W; ++u) {
-            const int2 s = __ldg(clean + 32 * u + (threadIdx.x & 31));
+            const int2 s = clean[32 * u + (threadIdx.x & 31)];
             bits[u] = warp_transpose(bit_range(s.x - key0, s.y - key0));
             some |= __any_sync(0xffffffffu, bits[u] != 0u);
         }
@@ -343,7 +343,11 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     const bool last = blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
-    const int4 hull = __ldg(&p.hull[static_cast<size_t>(z) * tiles + qtile]);
+    // span_prep_kernel's tables.  This kernel does not wait for it: it starts once every
+    // block of the dK/dV kernel has passed its own wait for that kernel's end, so the
+    // tables are in L2.  They are read there (.cg), past an L1 that may hold the tables
+    // of an earlier call in the same workspace, since only a wait promises more.
+    const int4 hull = __ldcg(&p.hull[static_cast<size_t>(z) * tiles + qtile]);
     if (hull.y == 0) {
         // no row of this tile sees a key: zeros, written by every thread
         if (at.rank == 0) zero_rows<D>(p.dq, z, h, qtile * 128, min(128, L - qtile * 128), L, p.H);
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, true>::kThreads, SpanBwdShape<
                   [&](int octet, int r, const float (&x)[8]) {
                       const int i = qtile * 128 + r;
                       if (i >= L) return;
-                      const int2 s = p.clean[static_cast<size_t>(z) * tiles * 128 + i];
+                      const int2 s = __ldcg(&p.clean[static_cast<size_t>(z) * tiles * 128 + i]);
                       reinterpret_cast<uint4 *>(p.dq + ((static_cast<size_t>(z) * L + i) * p.H + h) * D)[octet] =
                           split_pack(x, p.alpha, s.x < s.y);
                   });
@@ -576,7 +580,8 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
     const int L = p.src.L;
     const int n = span_tokens(p.src, z);
     const int k0 = ktile * 128, k1 = min(k0 + 128, n);
-    grid_wait();        // span_prep_kernel's tables
+    grid_wait();        // span_prep_kernel's tables (read with plain loads: they are written
+                        // while this kernel may already have started)
     grid_release();     // dQ needs nothing else of this kernel
     // first and last query tile whose hull meets this key tile
     const int4 *hull = p.hull + static_cast<size_t>(z) * tiles;
@@ -789,7 +794,7 @@ __global__ void __launch_bounds__(SpanBwdShape<D, false>::kThreads, SpanBwdShape
         bool ok = true;
         ScorePause pause = score_pause(cf);
         for (int r = 0; r < steps * NP; ++r) {
-            const int4 t = __ldg(hull + i);
+            const int4 t = hull[i];
             const bool whole = t.z <= k0 && t.w >= k1;
             const int row0 = i * 128 + part * SG::kStep;
             ok = span_dkdv_tile<D, MODE, SCORE>(tS, tD, s_full, s_free, dp_full, p_ready, ds_ready, r & 1, cf, key,

@@ -178,3 +178,24 @@ def test_later_queries_of_the_same_warp(dev, D, cap, bias):
             assert torch.equal(a[:, 512:], b[:, 512:])
     finally:
         sa.set_sigmoid_mode(old)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", [(3, 700, 8), (1, 1300, 2)])       # blocks of their own, and blocks that share tiles
+def test_calls_in_a_row_on_one_workspace(dev, D, shape):
+    """The backward's kernels overlap and hand tables over in the workspace: calls of unlike masks and lengths, one after the other
+    on one workspace without a wait between them, equal the same calls alone."""
+    Z, L, H = shape
+    q, k, v, do = _tensors(Z, L, H, H, D, torch.bfloat16, dev, 45)
+    kinds = []
+    for mask, n in (("causal", [L] * Z), ("docs", [L // 2] * Z), ("window", [L - 1] * Z), ("scatter", [L] * Z), ("holes", [130] * Z)):
+        kinds.append((R.make_spans(mask, n, L).to(dev), _seq(n, dev)))
+    call = lambda s, n, **a: sa.bwd_span(q, k, v, do, n, 0.1, -3.0, spans=s, **a)      # noqa: E731
+    want = []
+    for s, n in kinds:
+        want.append(call(s, n))
+        torch.cuda.synchronize()
+    ws = torch.empty(sa.bwd_span_workspace_bytes(Z, L, q.dtype), dtype=torch.uint8, device=dev)
+    got = [(at, call(*kinds[at], workspace=ws)) for at in [0, 1, 2, 3, 4, 2, 0, 4, 1, 3] * 4]
+    for at, outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[at]))
