@@ -140,3 +140,144 @@ def test_distances_beyond_two_to_the_24(dev, exp_mode, where):
         want = want + torch.sigmoid(-(first + near + 64).double())
         off = (o[0, l].double().cpu() - want).abs()
         assert (off <= (2.0 ** -7 + 1.1e-3) * want).all(), f"row {l}: {float((off / want).max()):.3g}"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_key_heads_than_blocks(dev, D):
+    """500 key heads, above the tile kernel's grid: each block takes one head after the other."""
+    Z, L, H, page = 2, 2, 500, 16
+    own, nq = np.asarray([70, 33]), np.asarray([2, 1])
+    table = np.arange(10).reshape(2, 5)
+    g = np.random.default_rng(4)
+    mark = (g.random((10, page, H)) < 0.3).astype(np.float32)
+    vp = torch.zeros(10, page, H, D)
+    vp[..., 5] = torch.as_tensor(2 * mark)
+    kp = torch.randn(10, page, H, D, generator=torch.Generator().manual_seed(1)).to(dev, torch.bfloat16)
+    q = torch.zeros(Z, L, H, D, device=dev, dtype=torch.bfloat16)
+    o = sa.fwd_paged(q, kp, vp.to(dev, torch.bfloat16), _i(table, dev), _i(own, dev), _i(nq, dev), 1.0, 0.0).float().cpu().numpy()
+    for z in range(Z):
+        for l in range(L):
+            at = np.arange(own[z] - nq[z] + l + 1 if l < nq[z] else 0)
+            want = mark[table[z][at // page], at % page].sum(0) if len(at) else np.zeros(H)
+            assert (o[z, l, :, 5] == want).all()
+
+
+def test_the_most_samples(dev):
+    """PAGED_MAX_Z samples of one to three tokens, their pages shared by many: marked values are counted."""
+    Z, H, D, page = sa.PAGED_MAX_Z, 2, 64, 16
+    own = 1 + np.arange(Z) % 3
+    table = (np.arange(Z) % 7)[:, None]
+    mark = np.asarray([[(p + s) % 2 for s in range(page)] for p in range(7)], np.float32)
+    vp = torch.zeros(7, page, 1, D)
+    vp[..., 0, 3] = torch.as_tensor(2 * mark)
+    kp = torch.randn(7, page, 1, D, generator=torch.Generator().manual_seed(1)).to(dev, torch.bfloat16)
+    q = torch.zeros(Z, 1, H, D, device=dev, dtype=torch.bfloat16)
+    o = sa.fwd_paged(q, kp, vp.to(dev, torch.bfloat16), _i(table, dev), _i(own, dev), _i(np.ones(Z), dev), 1.0, 0.0).float().cpu().numpy()
+    want = np.asarray([mark[table[z, 0], :own[z]].sum() for z in range(Z)])
+    assert (o[:, 0, 0, 3] == want).all() and (o[:, 0, 1, 3] == want).all()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_infinite_keys(dev, rows, cap):
+    """Live keys of infinite entries, in the prefix and among a sample's own: sigma is 1 or 0 by the score's sign."""
+    Z, H, D, page, prefix = 2, 2, 64, 16, 200
+    own = np.asarray([90, 64])
+    nq = np.asarray([rows, rows])
+    g = torch.Generator().manual_seed(rows)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(dev)      # noqa: E731
+    table, pre = np.arange(12).reshape(2, 6), np.arange(12, 25)
+    kp, vp, q = r(25, page, 1, D), r(25, page, 1, D), r(Z, rows, H, D)
+    kp[0, 3, 0, 0] = kp[7, 1, 0, 1] = float("inf")
+    kp[14, 9, 0, 2] = float("-inf")
+    o = sa.fwd_paged(q, kp, vp, _i(table, dev), _i(own, dev), _i(nq, dev), 0.125, -4.0, cap=cap, prefix_table=_i(pre, dev),
+                     prefix_len=_i([prefix], dev)).cpu().double()
+    assert torch.isfinite(o).all()
+    kc, vc, qc = (t.cpu().double()[..., :] for t in (kp, vp, q))
+    for z in range(Z):
+        n, m = int(own[z]), rows
+        k = torch.cat([kc[pre].flatten(0, 1)[:prefix], kc[table[z]].flatten(0, 1)[:n]])[:, 0]
+        v = torch.cat([vc[pre].flatten(0, 1)[:prefix], vc[table[z]].flatten(0, 1)[:n]])[:, 0]
+        y = 0.125 * (qc[z].transpose(0, 1) @ k.T)
+        y = cap * torch.tanh(y / cap) if cap else y
+        sees = torch.arange(prefix + n)[None] <= prefix + n - m + torch.arange(m)[:, None]
+        want = ((torch.sigmoid(y - 4.0) * sees) @ v).transpose(0, 1)
+        C.assert_close(o[z].numpy(), want.numpy(), "bf16", f"sample {z}")
+
+
+def test_a_decoding_loop_in_a_graph(dev):
+    """One captured step of append (lengths in place) and attention, replayed over page borders, equals the same steps called."""
+    Z, H, Hk, D, page, prefix = 3, 8, 2, 128, 16, 50
+    g = torch.Generator().manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(dev)      # noqa: E731
+    have = np.asarray([0, 15, 30])
+    table, pre = _i(np.arange(15).reshape(3, 5), dev), _i(np.arange(15, 19), dev)
+    inv = torch.logspace(0, -4, D // 2, device=dev)
+    kp, vp = r(19, page, Hk, D), r(19, page, Hk, D)
+    one, plen = _i([1] * Z, dev), _i([prefix], dev)
+    steps = [(r(Z, 1, Hk, D), r(Z, 1, Hk, D), r(Z, 1, H, D)) for _ in range(25)]
+
+    def step(k, v, q, kp, vp, lens, out, ws):
+        sa.cache_append(k, v, kp, vp, table, lens, one, inv_freq=inv, q=q, prefix_len=plen, q_out=q, lens_out=lens)
+        return sa.fwd_paged(q, kp, vp, table, lens, one, D ** -0.5, -5.0, prefix_table=pre, prefix_len=plen, cap=15.0, out=out,
+                            workspace=ws)
+
+    want, kw, vw, lens = [], kp.clone(), vp.clone(), _i(have, dev)
+    for k, v, q in steps:
+        want.append(step(k, v, q.clone(), kw, vw, lens, None, None))
+    bufs = [torch.empty_like(t) for t in steps[0]]
+    out, lens2 = torch.empty_like(bufs[2]), _i(have, dev)
+    ws = torch.empty(sa.fwd_paged_workspace_bytes(Z, 1, H, Hk, D, out.dtype), dtype=torch.uint8, device=dev)
+    spare = kp.clone(), vp.clone()
+    step(*(t.zero_() for t in bufs), *spare, lens2.clone(), out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*bufs, kp, vp, lens2, out, ws)
+    for at, new in enumerate(steps):
+        for b, t in zip(bufs, new):
+            b.copy_(t)
+        graph.replay()
+        assert torch.equal(out, want[at]), f"step {at}"
+    assert torch.equal(kp, kw) and torch.equal(vp, vw) and torch.equal(lens2, lens)
+    assert lens.tolist() == (have + 25).tolist()
+
+
+def test_two_threads_on_two_streams(dev):
+    """Calls made at the same time from two threads, each on its own stream, equal the same calls alone."""
+    import threading
+    Z, H, Hk, D, page = 8, 8, 2, 128, 16
+    g = torch.Generator().manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(dev)      # noqa: E731
+    kp, vp, table = r(40, page, Hk, D), r(40, page, Hk, D), _i(np.arange(40).reshape(8, 5), dev)
+    own, one = _i(1 + 9 * np.arange(8), dev), _i([1] * 8, dev)
+    qs = [r(Z, 1, H, D) for _ in range(2)]
+    ts = [r(2, 500, H, D) for _ in range(2)]
+    seq = _i([500, 130], dev)
+
+    def work(w):
+        return (sa.fwd_paged(qs[w], kp, vp, table, own, one, 0.1, -3.0), sa.fwd_span(ts[w], ts[w], ts[w], seq, 0.1, -3.0),
+                *sa.bwd_span(ts[w], ts[w], ts[w], ts[1 - w], seq, 0.1, -3.0))
+
+    want = [work(w) for w in range(2)]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def run(w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream(dev)):
+                got[w] = [work(w) for _ in range(30)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:          # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(w,)) for w in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for w in range(2):
+        for outs in got[w]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[w]))
+    assert math.isfinite(float(want[0][0].float().sum()))

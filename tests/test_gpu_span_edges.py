@@ -199,3 +199,47 @@ def test_calls_in_a_row_on_one_workspace(dev, D, shape):
     got = [(at, call(*kinds[at], workspace=ws)) for at in [0, 1, 2, 3, 4, 2, 0, 4, 1, 3] * 4]
     for at, outs in got:
         assert all(torch.equal(a, b) for a, b in zip(outs, want[at]))
+
+
+@pytest.mark.parametrize("mode", ["SIGMOID_TANH", "SIGMOID_EXP"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cap,sl,bias", [(0.0, False, -9.5), (0.0, False, -1.0), (20.0, False, -9.5), (20.0, True, -1.0)])
+def test_infinities_and_nan_in_live_rows(dev, dtype, mode, cap, sl, bias):
+    """A live key of infinite entries: sigma is 1 or 0 by the sign of the score, and O stays finite.  A query of NaN makes its own
+    row NaN and no other."""
+    Z, L, H, D = 1, 300, 2, 64
+    q, k, v, _ = _tensors(Z, L, H, H, D, dtype, dev, 25)
+    k[:, 100, :, 0], k[:, 207, :, 1] = float("inf"), float("-inf")
+    slopes = torch.tensor([0.02, 0.001], device=dev) if sl else None
+    seq = _seq([290], dev)
+    alpha = D ** -0.5
+    old = sa.get_sigmoid_mode()
+    try:
+        sa.set_sigmoid_mode(getattr(sa, mode))
+        o = sa.fwd_span(q, k, v, seq, alpha, bias, cap=cap, slopes=slopes)
+        bad = q.clone()
+        bad[:, 77] = float("nan")
+        ob = sa.fwd_span(bad, k, v, seq, alpha, bias, cap=cap, slopes=slopes)
+    finally:
+        sa.set_sigmoid_mode(old)
+    ref, _ = R.reference(q, k, v, None, R.visible(None, [290], L), alpha, [bias], cap, slopes)
+    kind = "fp32" if dtype == torch.float32 else "bf16"
+    assert torch.isfinite(o).all()
+    C.assert_close(o.float().cpu().numpy(), ref["O"].numpy(), kind, "O")
+    assert torch.isnan(ob[:, 77]).all()
+    others = torch.arange(L, device=dev) != 77
+    C.assert_close(ob[:, others].float().cpu().numpy(), ref["O"][:, others.cpu()].numpy(), kind, "O beside a row of NaN")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_short_samples(dev, exp_mode, dtype):
+    """More samples than are ranked by length, of 0 to 10 tokens."""
+    Z, L, H, Hk, D = 200, 10, 4, 2, 64
+    n = np.arange(Z) % 11
+    q, k, v, do = _tensors(Z, L, H, Hk, D, dtype, dev, 35)
+    spans = sa.mask_spans(_seq(n, dev), L, causal=True)
+    bias = [-1.0] * Z
+    got = (sa.fwd_span(q, k, v, _seq(n, dev), 0.125, -1.0, spans=spans), *sa.bwd_span(q, k, v, do, _seq(n, dev), 0.125, -1.0, spans=spans))
+    ref, bound = R.reference(q, k, v, do, R.visible(spans, n, L), 0.125, bias, 0.0, None, dtype == torch.float32)
+    for name, x in zip(("O", "dQ", "dK", "dV"), got):
+        R.assert_within(x, ref[name], bound[name], name)
