@@ -327,7 +327,8 @@ sigattn_status sigattn_mask_spans(const int32_t *seqlens, const int32_t *prefix,
  * (SIGATTN_ERR_SEQLEN_RANGE) and clamped.  No place but the new tokens' is
  * touched.
  *
- * sigattn_fwd_paged: queries q, output o [Z][L][H][D]; seqlens_q[z] <= L of them
+ * sigattn_fwd_paged: queries q, output o [Z][L][H][D] (o may be q, and overlaps no
+ * input otherwise); seqlens_q[z] <= L of them
  * are sample z's last tokens, and seqlens_k[z] >= seqlens_q[z] its own tokens in
  * the cache, theirs included.  Query l, at own place i = seqlens_k - seqlens_q + l,
  * sees its own places up to i and, with a prefix, all prefix_len[0] places of

@@ -57,6 +57,6 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens_k, seqlens_q, alpha: floa
     rows of the batch at a time (bf16).  ``bias``, ``cap`` and ``slopes`` as in ``fwd_span``, distances
     counted in positions with the prefix first.  ``workspace``: a device uint8
     tensor of at least ``fwd_paged_workspace_bytes`` bytes (allocated here when
-    omitted)."""
+    omitted).  ``out`` may be ``q`` and overlaps no input otherwise."""
     return native().fwd_paged(q, k_pages, v_pages, page_table, seqlens_k, seqlens_q, alpha, bias, prefix_table,
                               prefix_len, cap, slopes, out, workspace)

@@ -341,6 +341,10 @@ PyObject *fwd_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         const Score s(c, a[6], a[7], a[10], a[11]);
         at::Tensor out = c.output(a[12], c.q, "out");
+        // over q itself: in bf16 the last kernel writes, when all have read; in fp32 each
+        // row's block reads its queries first, and no other row's
+        if (a[12] != Py_None && ((overlap(out, c.q) && out.data_ptr() != c.q.data_ptr()) || overlap(out, kp) || overlap(out, vp)))
+            refuse("out must be q itself or overlap no input");
         const sigattn_dtype dt = dtype_of(c.q);
         const at::Tensor ws = c.workspace(a[13], g_fwd_paged_bytes(c.Z, c.L, c.H, c.Hk, c.D, dt));
         run(c, "sigattn_fwd_paged", g_fwd_paged, ptr(&c.q), ptr(&kp), ptr(&vp), ptr(&out), ints(&table), ints(&nk),

@@ -281,3 +281,21 @@ def test_two_threads_on_two_streams(dev):
         for outs in got[w]:
             assert all(torch.equal(a, b) for a, b in zip(outs, want[w]))
     assert math.isfinite(float(want[0][0].float().sum()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_the_output_may_be_the_queries(dev, dtype, rows):
+    """O over q gives the same as O beside it: with few rows and with the prefix kernel.  O half over q is refused."""
+    Z, H, Hk, D, page, prefix = 3, 4, 2, 64, 16, 70
+    g = torch.Generator().manual_seed(rows)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype).to(dev)      # noqa: E731
+    kp, vp = r(20, page, Hk, D), r(20, page, Hk, D)
+    buf = r(Z * rows * H * D + 64)
+    q = buf[:-64].view(Z, rows, H, D)
+    args = (kp, vp, _i(np.arange(15).reshape(3, 5), dev), _i([80, 41, 66], dev), _i([rows, 1, rows // 2 + 1], dev), 0.125, -2.0)
+    more = dict(prefix_table=_i(np.arange(15, 20), dev), prefix_len=_i([prefix], dev))
+    want = sa.fwd_paged(q, *args, **more)
+    with pytest.raises(ValueError, match="out"):
+        sa.fwd_paged(q, *args, out=buf[64:].view(Z, rows, H, D), **more)
+    assert torch.equal(sa.fwd_paged(q, *args, out=q, **more), want) and torch.equal(q, want)
