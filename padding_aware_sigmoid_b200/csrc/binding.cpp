@@ -162,6 +162,7 @@ struct Score {
     const float *bias_z = nullptr, *slopes;
     Score(const Call &c, PyObject *a, PyObject *b, PyObject *cp, PyObject *sl)
         : alpha(static_cast<float>(number(a, "alpha"))), cap(static_cast<float>(number(cp, "cap"))) {
+        if (cap == 0.0f && number(cp, "cap") != 0.0) refuse("cap is too small for fp32 (0 stands for none)");
         if (THPVariable_Check(b)) {
             const at::Tensor &t = THPVariable_Unpack(b);
             c.vector(&t, at::kFloat, {c.Z}, "bias");

@@ -243,3 +243,12 @@ def test_many_short_samples(dev, exp_mode, dtype):
     ref, bound = R.reference(q, k, v, do, R.visible(spans, n, L), 0.125, bias, 0.0, None, dtype == torch.float32)
     for name, x in zip(("O", "dQ", "dK", "dV"), got):
         R.assert_within(x, ref[name], bound[name], name)
+
+
+def test_caps_that_round_to_nothing_are_refused(dev):
+    q, k, v, do = _tensors(1, 20, 2, 2, 64, torch.bfloat16, dev, 2)
+    for cap in (1e-46, 1e-300):
+        with pytest.raises(ValueError, match="cap"):
+            sa.fwd_span(q, k, v, _seq([20], dev), 1.0, 0.0, cap=cap)
+        with pytest.raises(ValueError, match="cap"):
+            sa.bwd_span(q, k, v, do, _seq([20], dev), 1.0, 0.0, cap=cap)
