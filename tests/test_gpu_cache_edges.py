@@ -299,3 +299,114 @@ def test_the_output_may_be_the_queries(dev, dtype, rows):
     with pytest.raises(ValueError, match="out"):
         sa.fwd_paged(q, *args, out=buf[64:].view(Z, rows, H, D), **more)
     assert torch.equal(sa.fwd_paged(q, *args, out=q, **more), want) and torch.equal(q, want)
+
+
+def _reference(q, keys, values, prefix, n, m, alpha, bias, cap, slopes):
+    """O and its bound (tests/_span_ref.py) of one sample's last m tokens: keys and values [prefix + n, Hk, D] in 64 bits."""
+    H, G = q.shape[1], q.shape[1] // keys.shape[1]
+    k, v = (t.repeat_interleave(G, 1).transpose(0, 1) for t in (keys, values))
+    y = alpha * (q[:m].transpose(0, 1) @ k.mT)
+    y = cap * torch.tanh(y / cap) if cap else y
+    i, j = prefix + n - m + torch.arange(m, device=q.device)[:, None], torch.arange(prefix + n, device=q.device)[None]
+    if slopes is not None:
+        y = y - slopes.to(q.device).double().view(H, 1, 1) * (i - j).abs()
+    P = torch.sigmoid(y + bias) * (j <= i)
+    o = (P @ v).transpose(0, 1)
+    return o, R.HALF_BF16 * o.abs() + (R.HALF_BF16 + 1.1e-3) * (P @ v.abs()).transpose(0, 1)
+
+
+@pytest.mark.parametrize("heads,D,page,prefix,cap,sl", [((4, 1), 128, 64, 333, 0.0, False), ((6, 6), 64, 16, 0, 30.0, True),
+                                                        ((8, 2), 64, 32, 1000, 20.0, False)])
+def test_prompts(dev, exp_mode, heads, D, page, prefix, cap, sl):
+    """Hundreds of new tokens a sample, behind cached ones and behind a prefix: many row tiles, ragged at both ends."""
+    (H, Hk), Z, L = heads, 3, 300
+    own, nq = np.asarray([300, 777, 431]), np.asarray([300, 257, 1])
+    need = -(-own // page)
+    g = torch.Generator().manual_seed(prefix)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(dev)      # noqa: E731
+    ahead = -(-prefix // page)
+    pool = np.random.default_rng(1).permutation(ahead + need.sum())
+    table = np.full((Z, need.max()), -1)
+    at = ahead
+    for z in range(Z):
+        table[z, :need[z]] = pool[at:at + need[z]]
+        at += need[z]
+    kp, vp, q = r(len(pool), page, Hk, D), r(len(pool), page, Hk, D), r(Z, L, H, D)
+    slopes = torch.linspace(0.2, 0.001, H, device=dev) if sl else None
+    more = dict(prefix_table=_i(pool[:ahead], dev), prefix_len=_i([prefix], dev)) if prefix else {}
+    o = sa.fwd_paged(q, kp, vp, _i(table, dev), _i(own, dev), _i(nq, dev), D ** -0.5, -4.0, cap=cap, slopes=slopes, **more)
+    for z in range(Z):
+        n, m = int(own[z]), int(nq[z])
+        rows = lambda t: torch.cat([t[pool[:ahead]].flatten(0, 1)[:prefix], t[table[z, :need[z]]].flatten(0, 1)[:n]]).double()  # noqa: E731,B023
+        want, bound = _reference(q[z].double(), rows(kp), rows(vp), prefix, n, m, D ** -0.5, -4.0, cap, slopes)
+        off = (o[z, :m].double() - want).abs()
+        assert (off <= bound).all(), f"sample {z}: {float((off / bound).max()):.3g} of the bound"
+        assert not o[z, m:].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_bad_pages_of_the_prefix_weigh_nothing(dtype, rows):
+    """Page numbers outside the cache in the prefix's table are flagged and count as keys of weight zero; a prefix length outside its
+    table is flagged and clamped."""
+    dev = torch.device("cuda", 0)
+    Z, H, D, page = 2, 4, 64, 16
+    g = torch.Generator().manual_seed(rows)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype).to(dev)      # noqa: E731
+    kp, vp, q = r(8, page, 1, D), r(8, page, 1, D), r(Z, rows, H, D)
+    kp[7], vp[7] = 0.0, 0.0                                       # keys that weigh nothing, as values
+    call = lambda pre, n: sa.fwd_paged(q, kp, vp, _i([[0, 1, 2], [3, 4, 4]], dev), _i([40, 40], dev), _i([rows, rows], dev), 0.1, -1.0,      # noqa: E731
+                                       prefix_table=_i(pre, dev), prefix_len=_i([n], dev))
+    sa.last_device_status()
+    good, short, none = call([5, 7, 6, 7], 64), call([5, 7, 6, 7], 40), call([5, 7, 6, 7], 0)
+    assert sa.last_device_status() == 0
+    for bad in (8, -1, 2 ** 31 - 1, -2 ** 31):
+        got = call([5, bad, 6, bad], 64)
+        assert sa.last_device_status() == 10
+        assert torch.equal(got, good)
+    call([5, 7, 6, -3], 40)                                      # a page that no place reaches is not read
+    assert sa.last_device_status() == 0
+    for n, want in ((65, good), (2 ** 31 - 1, good), (-1, none), (-2 ** 31, none)):
+        got = call([5, 7, 6, 7], n)
+        assert sa.last_device_status() == 8
+        assert torch.equal(got, want)
+    assert not torch.equal(good, short)
+
+
+def test_nothing_to_answer(dev):
+    """No queries at all: zeros, whatever the cache and the queries hold."""
+    Z, L, H, D, page = 3, 40, 4, 64, 16
+    nan = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=dev)      # noqa: E731
+    for own in ([0, 0, 0], [30, 0, 5]):
+        for prefix in (0, 40):
+            o = sa.fwd_paged(nan(Z, L, H, D), nan(9, page, 2, D), nan(9, page, 2, D), _i([[0, 1], [2, 3], [4, 5]], dev), _i(own, dev),
+                             _i([0, 0, 0], dev), 1.0, 0.0, prefix_table=_i([6, 7, 8], dev), prefix_len=_i([prefix], dev), out=nan(Z, L, H, D))
+            assert not o.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pages_beyond_two_to_the_31_entries(dev, dtype):
+    """A cache of more than 2^31 entries: what is appended to its last pages, and read from them, equals the same in a small one."""
+    Z, H, Hk, D, page = 2, 16, 16, 128, 16
+    big = 2 ** 31 // (page * Hk * D) + 40
+    kp, vp = (torch.zeros(big, page, Hk, D, dtype=dtype, device=dev) for _ in range(2))
+    assert kp.numel() > 2 ** 31
+    ks, vs = (torch.zeros(12, page, Hk, D, dtype=dtype, device=dev) for _ in range(2))
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype).to(dev)      # noqa: E731
+    k, v, q = r(Z, 60, Hk, D), r(Z, 60, Hk, D), r(Z, 60, H, D)
+    inv = torch.logspace(0, -4, D // 2, device=dev)
+    table = np.arange(8).reshape(2, 4)
+    pre = np.arange(8, 12)
+    outs = []
+    for pages_k, pages_v, first in ((ks, vs, 0), (kp, vp, big - 12)):
+        t = _i(first + table, dev)
+        pages_k[first + 8:first + 12], pages_v[first + 8:first + 12] = k[0, 0, 0] * 0.5, v[0, 0, 0]
+        qr, lens = sa.cache_append(k, v, pages_k, pages_v, t, _i([0, 3], dev), _i([60, 41], dev), inv_freq=inv, q=q)
+        for last in (1, 40):
+            outs.append([sa.fwd_paged(qr[:, :last].contiguous(), pages_k, pages_v, t, lens, _i([last, last], dev), 0.1, -2.0,
+                                      prefix_table=_i(first + pre, dev), prefix_len=_i([50], dev))])
+        outs[-1] += [qr, pages_k[first:first + 12].clone(), pages_v[first:first + 12].clone()]
+        assert not first or not (pages_k[:first].any() or pages_v[:first].any())
+    for a, b in zip(outs[:2], outs[2:]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

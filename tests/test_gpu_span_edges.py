@@ -252,3 +252,38 @@ def test_caps_that_round_to_nothing_are_refused(dev):
             sa.fwd_span(q, k, v, _seq([20], dev), 1.0, 0.0, cap=cap)
         with pytest.raises(ValueError, match="cap"):
             sa.bwd_span(q, k, v, do, _seq([20], dev), 1.0, 0.0, cap=cap)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_tensors_beyond_two_to_the_31_entries(dev, D):
+    """Queries of more than 2^31 entries, their heads sharing one key head: with all scores 0 sigma is 1/2 and its derivative 1/4, and
+    marked rows are counted (tests/test_gpu_span.py), the last samples' as the first's."""
+    L, H = 2048, 128
+    Z = 2 ** 31 // (L * H * D) + 2
+    window = 40
+    n = np.full(Z, L)
+    n[-1] = L - 77
+    seq = _seq(n, dev)
+    spans = sa.mask_spans(seq, L, causal=True, window=window)
+    q = torch.zeros(Z, L, H, D, dtype=torch.bfloat16, device=dev)
+    assert q.numel() > 2 ** 31
+    k, v = (torch.zeros(Z, L, 1, D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    mark = (torch.arange(L, device=dev) % 5 == 0).to(q.dtype)
+    q[..., 0] = (torch.arange(H, device=dev) % 64 == 3).to(q.dtype)
+    k[..., 1] = mark[None, :, None]
+    v[..., 2], v[..., 3] = 2.0, 2.0 * mark[None, :, None]
+    do = torch.zeros_like(q)
+    do[..., 2] = 1.0                                             # dP = 2, dS = 1/2
+    do[..., 4] = q[..., 0] * 2.0
+    o = sa.fwd_span(q, k, v, seq, 2.0, 0.0, spans=spans)
+    dq, dk, dv = sa.bwd_span(q, k, v, do, seq, 2.0, 0.0, spans=spans)
+    i = torch.arange(L, device=dev)
+    for z in (0, 1, Z - 2, Z - 1):
+        sees = ((i[None] <= i[:, None]) & (i[None] > i[:, None] - window) & (i[:, None] < int(n[z]))).float()
+        rows, keys = sees @ mark.float(), sees.sum(0)
+        for x, e in ((o, 3), (dq, 1)):
+            assert torch.equal(x[z, :, :, e].float(), rows[:, None].expand(L, H))
+            assert not x[z, :, :, 5:].any()
+        assert torch.equal(dv[z, :, 0, 4].float(), 2.0 * keys)   # two marked heads
+        assert torch.equal(dk[z, :, 0, 0].float(), 2.0 * keys)
+        assert not dk[z, :, 0, 5:].any() and not dv[z, :, 0, 5:].any()
