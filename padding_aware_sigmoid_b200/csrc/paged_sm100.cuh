@@ -257,6 +257,11 @@ struct PagedItem {
     __device__ __forceinline__ void tile(uint32_t sK, uint32_t sV, int key0) {
         const int lane = lane_id(), wk = warp_id() / WM;
         if (!__any_sync(0xffffffffu, max(rows.limit[0], rows.limit[1]) > key0 + wk * KW)) return;
+        // distance of this thread's first key; the others' follow in fp32, where a step that
+        // rounds is one of 2^24 places or more (a conversion for each pair would go through
+        // the MUFU's pipe)
+        const int first = key0 + wk * KW + 2 * (lane & 3);
+        const float rel[2] = {static_cast<float>(rows.pos[0] - first), static_cast<float>(rows.pos[1] - first)};
 #pragma unroll
         for (int g = 0; g < KW / 16; ++g) {
             const int k16 = wk * KW + 16 * g;     // first of 16 keys
@@ -283,9 +288,8 @@ struct PagedItem {
             for (int n8 = 0; n8 < 2; ++n8)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int key = key0 + k16 + 8 * n8 + 2 * (lane & 3);
-                    float2 w = score_p2<SCORE>(s[n8][2 * i], s[n8][2 * i + 1], cf[i],
-                                                     static_cast<float>(rows.pos[i] - key));
+                    const int key = first + 16 * g + 8 * n8;
+                    float2 w = score_p2<SCORE>(s[n8][2 * i], s[n8][2 * i + 1], cf[i], rel[i] - static_cast<float>(16 * g + 8 * n8));
                     w.x = key < rows.limit[i] ? w.x : 0.0f;
                     w.y = key + 1 < rows.limit[i] ? w.y : 0.0f;
                     const uint32_t hi = pack_bf16x2(w.x, w.y);
