@@ -136,7 +136,7 @@ sigattn_status paged_launch(const PagedMaps &m, const PagedParams &p, cudaStream
     using Lay = PagedLayout<D>;
     sigattn_status s = SIGATTN_OK;
     if (p.splits > 0) {
-        s = g_sigmoid_mode.load() == kSigmoidTanh ? prefix_launch<D, kSigmoidTanh, SCORE>(m, p, st)
+        s = g_sigmoid_mode.load() == kSigmoidTanh ? prefix_launch<D, kSigmoidTanh, SCORE & ~kScoreFar>(m, p, st)
                                                   : prefix_launch<D, kSigmoidExp, SCORE>(m, p, st);
         if (s != SIGATTN_OK) return s;
     }
@@ -161,7 +161,9 @@ sigattn_status paged_score(int score, const PagedMaps &m, const PagedParams &p, 
         case 0: return paged_launch<D, 0>(m, p, st);
         case kScoreCap: return paged_launch<D, kScoreCap>(m, p, st);
         case kScoreSlope: return paged_launch<D, kScoreSlope>(m, p, st);
-        default: return paged_launch<D, kScoreCap | kScoreSlope>(m, p, st);
+        case kScoreCap | kScoreSlope: return paged_launch<D, kScoreCap | kScoreSlope>(m, p, st);
+        case kScoreCap | kScoreFar: return paged_launch<D, kScoreCap | kScoreFar>(m, p, st);
+        default: return paged_launch<D, kScoreCap | kScoreSlope | kScoreFar>(m, p, st);
     }
 }
 
@@ -342,7 +344,7 @@ sigattn_status sigattn_fwd_paged(const void *q, const void *k_pages, const void 
                             {64, static_cast<cuuint32_t>(group), 1, static_cast<cuuint32_t>(z.tile_tokens)})) != SIGATTN_OK)
             return s;
     }
-    const int score = (cap > 0.0f ? kScoreCap : 0) | (slopes != nullptr ? kScoreSlope : 0);
+    const int score = score_terms(cap, slopes);
     return D == 64 ? paged_score<64>(score, m, p, st) : paged_score<128>(score, m, p, st);
 }
 

@@ -44,8 +44,7 @@ sigattn_status check_span(const SpanArgs &a, bool *empty) {
 }
 
 SpanKind kind_of(const SpanArgs &a) {
-    return SpanKind{a.D, g_sigmoid_mode.load(),
-                    (a.cap > 0.0f ? kScoreCap : 0) | (a.slopes != nullptr ? kScoreSlope : 0)};
+    return SpanKind{a.D, g_sigmoid_mode.load(), score_terms(a.cap, a.slopes)};
 }
 
 SpanSource source_of(const SpanArgs &a, int *status) {

@@ -28,8 +28,11 @@ sigattn_status with_score(int score, F &&f) {
         case 0: return f.template operator()<D, MODE, 0>();
         case kScoreCap: return f.template operator()<D, MODE, kScoreCap>();
         case kScoreSlope: return f.template operator()<D, MODE, kScoreSlope>();
-        default: return f.template operator()<D, MODE, kScoreCap | kScoreSlope>();
+        case kScoreCap | kScoreSlope: return f.template operator()<D, MODE, kScoreCap | kScoreSlope>();
     }
+    constexpr int kFar = MODE == kSigmoidExp ? kScoreFar : 0;     // the hardware tanh has no such form
+    return score & kScoreSlope ? f.template operator()<D, MODE, kScoreCap | kScoreSlope | kFar>()
+                               : f.template operator()<D, MODE, kScoreCap | kFar>();
 }
 template <typename F>
 sigattn_status with_kind(const SpanKind &k, F &&f) {

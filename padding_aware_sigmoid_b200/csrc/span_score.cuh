@@ -17,8 +17,13 @@
 
 namespace sigattn {
 
-// SCORE: which terms a kernel instance evaluates.
-enum ScoreTerms : int { kScoreCap = 1, kScoreSlope = 2 };
+// SCORE: which terms a kernel instance evaluates.  kScoreFar goes with a cap above
+// kCapFar, in the EXP form only (cap_tanh2).
+enum ScoreTerms : int { kScoreCap = 1, kScoreSlope = 2, kScoreFar = 4 };
+constexpr float kCapFar = 64.0f;
+inline int score_terms(float cap, const float *slopes) {
+    return (cap > 0.0f ? kScoreCap : 0) | (cap > kCapFar ? kScoreFar : 0) | (slopes != nullptr ? kScoreSlope : 0);
+}
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
@@ -78,13 +83,16 @@ __device__ __forceinline__ float2 score_addend(const ScoreCoef &cf, float rel) {
 // tanh of two capped scores, and 1 - tanh^2.  TANH mode takes the hardware
 // tanh (relative error 2^-11, so the capped score moves by at most 2^-11 of
 // itself).  EXP mode forms (1 - e) / (1 + e) with e = exp(-2 |y|), and 4 e / (1 +
-// e)^2, in which nothing cancels.  Below |y| = 1/4 the former does, and a cap far above
-// the scores would bring its absolute error back as cap times that; there tanh(y) /
-// y is a polynomial in y^2 (minimax fit in relative error, fitted for this library as
-// the one above, maximum 4e-7).  Either side is within 2^-20 of tanh, relatively, so a
-// capped score is within 2^-20 of itself whatever the cap.
+// e)^2, in which nothing cancels.  Below |y| = 1/4 the former does: an absolute error
+// of about 2^-21, which the cap multiplies: a score is off by 2^-15 at kCapFar.  FAR, above
+// that, takes tanh(y) / y there as a polynomial in y^2 (minimax fit in relative error,
+// fitted for this library as the one above, maximum 4e-7).  Either side is then within
+// 2^-20 of tanh, relatively, and so is a capped score, whatever the cap.  For every cap
+// that would be 9 to 15% of the EXP mode's time (cap 30, forward of 2 x 4001, 16 over 4
+// heads, D = 128: 275 -> 314 us, backward 695 -> 799; D = 64, full 4K forward 405 -> 441) and 3 to
+// 5% of the paged attention's (32 x 4 drafts 53.6 -> 55.6).
 constexpr float kTanh0 = 0.999999583f, kTanh1 = -0.333219081f, kTanh2 = 0.128416136f, kTanhMost = 0.25f;
-template <int MODE, bool GRAD>
+template <int MODE, bool GRAD, bool FAR>
 __device__ __forceinline__ float2 cap_tanh2(float2 y, float2 &f) {
     if constexpr (MODE == kSigmoidTanh) {
         const float2 t = f2(tanh_approx(y.x), tanh_approx(y.y));
@@ -95,6 +103,7 @@ __device__ __forceinline__ float2 cap_tanh2(float2 y, float2 &f) {
         const float2 r = f2(rcp_approx(1.0f + e.x), rcp_approx(1.0f + e.y));
         const float2 t = mul2(fma2(e, f2(-1.0f, -1.0f), f2(1.0f, 1.0f)), r);
         if constexpr (GRAD) f = mul2(mul2(f2(4.0f, 4.0f), e), mul2(r, r));
+        if constexpr (!FAR) return f2(copysignf(t.x, y.x), copysignf(t.y, y.y));
         const float2 z = mul2(y, y);
         const float2 n = mul2(y, fma2(z, fma2(z, f2(kTanh2, kTanh2), f2(kTanh1, kTanh1)), f2(kTanh0, kTanh0)));
         return f2(fabsf(y.x) < kTanhMost ? n.x : copysignf(t.x, y.x), fabsf(y.y) < kTanhMost ? n.y : copysignf(t.y, y.y));
@@ -106,7 +115,7 @@ __device__ __forceinline__ float2 cap_tanh2(float2 y, float2 &f) {
 template <int MODE, int SCORE, bool GRAD>
 __device__ __forceinline__ float2 score_arg2(float s0, float s1, const ScoreCoef &cf, float2 add, float2 &f) {
     if constexpr (SCORE & kScoreCap) {
-        const float2 t = cap_tanh2<MODE, GRAD>(mul2(f2(s0, s1), f2(cf.a, cf.a)), f);
+        const float2 t = cap_tanh2<MODE, GRAD, (SCORE & kScoreFar) != 0>(mul2(f2(s0, s1), f2(cf.a, cf.a)), f);
         return fma2(t, f2(cf.cap, cf.cap), add);
     } else {
         return fma2(f2(s0, s1), f2(cf.a, cf.a), add);
@@ -251,7 +260,7 @@ __device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &
 }
 // P of two neighbouring columns, for kernels whose scores are few: one ex2 and one
 // reciprocal, e^-|x| keeping both tails.  Relative error about 2^-20, and what the
-// argument's own error moves: 2^-23 of x without a cap, 2^-20 of the score with one.
+// argument's own error moves: 2^-23 of x without a cap, that of cap_tanh2 with one.
 template <int SCORE>
 __device__ __forceinline__ float2 score_p2(float s0, float s1, const ScoreCoef &cf, float rel) {
     float2 f;

@@ -287,3 +287,30 @@ def test_tensors_beyond_two_to_the_31_entries(dev, D):
         assert torch.equal(dv[z, :, 0, 4].float(), 2.0 * keys)   # two marked heads
         assert torch.equal(dk[z, :, 0, 0].float(), 2.0 * keys)
         assert not dk[z, :, 0, 5:].any() and not dv[z, :, 0, 5:].any()
+
+
+@pytest.mark.parametrize("mode", ["SIGMOID_TANH", "SIGMOID_EXP"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_caps_on_both_sides_of_far(dev, D, mode):
+    """A cap of 64 and the next fp32 above it, which the accurate form evaluates otherwise, with slopes and without, alone in a tile
+    and shared: both within the bounds of their mode, and next to each other."""
+    old = sa.get_sigmoid_mode()
+    caps = (64.0, float(np.nextafter(np.float32(64.0), np.float32(65.0))))
+    for (Z, L, H), sl in (((2, 260, 2), False), ((1, 1100, 2), True)):
+        q, k, v, do = _tensors(Z, L, H, H, D, torch.bfloat16, dev, 5, 2.0)
+        n = [L - 3] * Z
+        spans = R.make_spans("causal", n, L).to(dev)
+        slopes = torch.tensor([0.05, 0.001], device=dev) if sl else None
+        ref, bound = R.reference(q, k, v, do, R.visible(spans, n, L), D ** -0.5, [-3.0] * Z, 64.0, slopes)
+        for cap in caps:
+            a = dict(spans=spans, cap=cap, slopes=slopes)
+            try:
+                sa.set_sigmoid_mode(getattr(sa, mode))
+                got = (sa.fwd_span(q, k, v, _seq(n, dev), D ** -0.5, -3.0, **a), *sa.bwd_span(q, k, v, do, _seq(n, dev), D ** -0.5, -3.0, **a))
+            finally:
+                sa.set_sigmoid_mode(old)
+            for name, x in zip(("O", "dQ", "dK", "dV"), got):
+                if mode == "SIGMOID_EXP":
+                    R.assert_within(x, ref[name], bound[name], name)
+                else:
+                    C.assert_close(x.float().cpu().numpy(), ref[name].numpy(), "bf16", name)
