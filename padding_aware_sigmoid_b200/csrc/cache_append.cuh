@@ -6,13 +6,18 @@
 // position p = prefix_len + at: pair i of the first `rot` entries of each head
 // turns by the angle p * inv_freq[i].  Values are copied, queries rotated out.
 //
-// Pure traffic: every row is read once and written once, 16 bytes a thread and
-// access.  One warp takes a token (or a share of its heads, when tokens are few).
-// Its lanes keep their place within a head, so that each holds the angles of its
-// pairs in registers for all heads of the token; what is left per head is the
-// loads, two FMAs an entry and the stores.  (One thread per unit of any head with the
-// angles in shared memory spent its time on instructions: 40 us for 4 x 4096 prompt
-// tokens, 16 + 4 heads of 128.)
+// Every row is read once and written once, 16 bytes a thread and access.  One warp takes
+// a token (or a share of its heads, when tokens are few).  Its lanes keep their place
+// within a head, so that each holds the angles of its pairs in registers for all heads
+// of the token; what is left per head is the loads, two FMAs an entry and the stores.
+// (One thread per unit of any head with the angles in shared memory spent its time on
+// instructions: 40 us for 4 x 4096 prompt tokens, 16 + 4 heads of 128.)
+//
+// Bound, for many tokens, by latency: a warp's chain is the lengths, the page, its
+// angles in 64 bits and two or three rounds of loads and stores, and then it ends.  The
+// same 4 x 4096 tokens now take 38.4 us, 4.3 TB/s of the 6.46 that a copy reaches, with
+// DRAM 39% busy under ncu and 7.8 cycles an issue spent on loads.  The bf16 instances
+// spill 16 bytes at 64 registers, four blocks an SM.
 #pragma once
 
 #include <stdint.h>

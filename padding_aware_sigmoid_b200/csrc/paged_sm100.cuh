@@ -33,6 +33,9 @@
 //  paged_join_kernel adds the partials of each row in a fixed order (the result
 //    does not depend on scheduling) and rounds once.
 //
+// The prefix kernel and the tile kernel with 64 rows round P to one bf16 number, as the
+// masked forward does; with fewer rows the tile kernel keeps it in two (PagedItem).
+//
 // Bound: memory.  Every key and value is read once per row tile; a 64-key tile
 // at D = 128 is 32 KB, 1.4 kclk of an SM's share of HBM.  The few rows of one
 // sample leave a tcgen05 tile of 128 rows mostly empty and its sigma warps with

@@ -100,9 +100,10 @@ unsigned f32_blocks(const SpanArgs &a, int heads) {
 
 // Calls f.template operator()<D, G>(): the fp32 kernels with G groups of warps to a
 // block.  Few blocks, or the backward of shared heads, whose blocks of keys run
-// through all of a key head's queries, are bound by a block's length: 2 x 128 tokens,
-// 2 heads, D = 64, backward 13.9 -> 11.0 us with four groups, 4 x 200, 16 over 4 heads 175 ->
-// 141.  Many blocks fill the device without (4 x 200, 12 heads, 89 -> 107 us with them).
+// through all of a key head's queries, are bound by a block's length: backward, D = 64,
+// 2 x 128 tokens, 2 heads, slopes, 14.4 -> 12.3 us with four groups, 4 x 200 causal, 16
+// over 4 heads 229 -> 201.  Many blocks fill the device without (4 x 200 causal, 12 heads,
+// 130 -> 151 us with them).
 template <typename F>
 sigattn_status with_groups(const SpanArgs &a, int64_t blocks, int sms, bool backward, F &&f) {
     const bool many = a.L <= kF32Chunk || (blocks > int64_t(4) * sms && !(backward && a.H > a.Hk));

@@ -7,6 +7,7 @@
 //    span_prep_kernel writes (one entry per 128 rows), so neither kernel
 //    touches a tile that no pair needs under causal, prefix, document or
 //    window masks;
+//  - P and dS are rounded to bf16 (span_score.cuh says why); all sums are fp32;
 //  - a key head serves `group` query heads: the dK/dV CTA of a key head runs
 //    through the query tiles of all of them and accumulates in tensor memory,
 //    so shared heads need no second pass and the sum's order is fixed;
@@ -82,8 +83,12 @@ static __global__ void __launch_bounds__(128) span_prep_kernel(const SpanSource 
 // capped documents 133.6 -> 119.4 us, documents 130.7 -> 122.5 us, window 8K 202 -> 198 us,
 // causal 8K 431 -> 425 us, full capped 4K 620 -> 652 us (half steps hand over twice
 // as often).  dK/dV, whose threads hold more, then loads both rings from one warp: two
-// blocks of 320 threads leave 96 registers a thread, of 384 threads 80, which spilled
-// and lost 6 to 25%.
+// blocks of 320 threads leave 96 registers a thread, of 384 threads 80, which lost 6 to
+// 25%.
+// Spills, bytes a thread stored and loaded (tanh form): dK/dV at D = 64 none to 84 / 152,
+// at D = 128, 168 registers, 104 to 148 / 176 to 252 (the padding-only kernel, whose score
+// has one form, 12 / 12); dQ at D = 64 up to 48 / 64, at D = 128 none.  Two copies of the
+// score's forms, 32 packed weights and 32 gains are live together there.
 template <int D, bool DQ>
 struct SpanBwdShape {
     static constexpr bool kHalf = D == 64;
@@ -194,7 +199,8 @@ __device__ __forceinline__ bool span_dq_tile(uint32_t trow, int w, uint32_t col_
 // dkdv_sigma_tile (bwd_sm100.cuh) with the masked score function: one query
 // tile of a dK/dV sigma warpgroup, whose columns are the queries from q_first
 // on.  `key` is this thread's key; `whole`: every row of the tile sees every
-// key of this CTA's tile; keys_there: none of this warp's keys is padding; otherwise `clean` points at the spans of the columns (lane i reads column i).
+// key of this CTA's tile, otherwise `clean` points at the spans of the columns (lane
+// i reads column i); keys_there: none of this warp's keys is padding.
 template <int D, int MODE, int SCORE>
 __device__ __forceinline__ bool span_dkdv_tile(uint32_t tS, uint32_t tD, uint64_t *s_full, uint64_t *s_free,
                                                uint64_t *dp_full, uint64_t *p_ready, uint64_t *ds_ready,

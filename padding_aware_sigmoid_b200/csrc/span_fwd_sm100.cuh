@@ -18,6 +18,9 @@
 //    while the sigma warps work on its scores, so that NaN in padding never
 //    meets the product.
 //
+// P is rounded to bf16 before its product with V (span_score.cuh says why); O is summed
+// in fp32 and rounded once.
+//
 // Bound: as the padding-only forward, one MUFU op per score (two with a cap)
 // against 4 D tensor FLOP; at D = 128 without a cap the two pipes balance.
 #pragma once

@@ -215,9 +215,18 @@ __device__ __forceinline__ int score_form(const uint32_t *r, const ScoreCoef &cf
 // larger weight keep the tanh: there the weights that cancel are the small ones.
 //
 // FWD: the cap as a polynomial, in the forward and without slopes (D = 64, full 4K:
-// 280 -> 222 us).  With slopes the FMA and ALU pipes are the bound already (D = 128
-// 193 -> 194 us, D = 64 packed 56 -> 62 us), and the backward's registers do not hold
-// its operands (D = 128 547 -> 663 us).
+// 280 -> 222 us).  With slopes it gained nothing (D = 128 193 -> 194 us, D = 64 packed 56 ->
+// 62 us), though no pipe is full there (with the tanh, D = 128: MUFU 71%, FMA 24%, ALU
+// 17%, issue 40%): a warp's load of scores, its arithmetic and its store follow one
+// another, and more instructions make that chain longer.  The backward's registers do
+// not hold its operands (D = 128 547 -> 663 us).
+//
+// P, and in the backward dS, is rounded to bf16, half a step of 2^-8 at most: the type
+// of the tensor pipe's operands.  It is the larger part of a bf16 result's error (2-norm
+// of O, dQ, dK, dV 2.35e-3 of the definition's in 64 bits, 1.66e-3 with P in 32 bits
+// and one rounding at the end), as in the padding-only kernels.  A second bf16 part
+// would double the products that are the bound at D = 128; the paged tile kernel, whose
+// few rows leave them room, keeps two.
 template <int MODE, int SCORE, bool GRAD, bool FWD = false>
 __device__ __forceinline__ void score_chunk(const uint32_t *r, const ScoreCoef &cf, float rel, uint32_t *pk,
                                             float2 *g, ScorePause &pause, bool whole, bool live = true) {
